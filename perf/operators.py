@@ -3,9 +3,9 @@
 select: from router logits to the chosen experts, their weights and the grouping of the rows by expert
         (moe_select): softmax or sigmoid scores, a balance bias that moves the choice and not the weights, groups of
         experts of which a token keeps the best few, renormalised and scaled weights.
-ffn:    the experts' products in 8-bit integers with a scale for each token and each output channel: the tokens are
-        quantised (moe_quantize), each expert's group of rows goes through its SwiGLU feed-forward (moe_ffn for lists
-        made on the host, moe_ffn_grouped for lists on the GPU) and the rows are combined (moe_combine).
+experts: the experts' products in 8-bit integers with a scale for each token and each output channel (moe_experts):
+        the tokens are quantised, each expert's group of rows goes through its SwiGLU feed-forward, the SwiGLU products
+        quantised row by row in between, and a token's rows are added with its routing weights.
 
 `own` is False: `run` computes the plain form in elementary torch operations. True: the framework's calls.
 """
@@ -27,8 +27,8 @@ def _select(name, T, E, k, score, groups=1, keep=1, top=1, balance=True, renorm=
                 renorm=renorm, scale=scale)
 
 
-def _ffn(name, T, E, k, H, I, skew=0.0, call="list"):
-    return dict(name=name, op="ffn", T=T, E=E, k=k, H=H, I=I, skew=skew, call=call)
+def _experts(name, T, E, k, H, I, skew=0.0):
+    return dict(name=name, op="experts", T=T, E=E, k=k, H=H, I=I, skew=skew)
 
 
 def listed():
@@ -44,19 +44,19 @@ def listed():
         # the longest chunk, groups and balance bias
         _select("select_long", 16384, 256, 8, "sigmoid", groups=8, keep=4, top=2, scale=2.5),
         # one decoded token: six experts' weights stream through once
-        _ffn("ffn_one", 1, 64, 6, 4096, 2048),
+        _experts("experts_one", 1, 64, 6, 4096, 2048),
         # a decode batch over small experts
-        _ffn("ffn_small", 4, 128, 8, 2048, 768, skew=1.2),
+        _experts("experts_small", 4, 128, 8, 2048, 768, skew=1.2),
         # a decode batch that shares experts
-        _ffn("ffn_batch", 8, 64, 6, 4096, 2048, skew=1.0),
+        _experts("experts_batch", 8, 64, 6, 4096, 2048, skew=1.0),
         # many short groups, some past one tile of tokens
-        _ffn("ffn_mid", 64, 128, 8, 2048, 768, skew=0.5),
+        _experts("experts_mid", 64, 128, 8, 2048, 768, skew=0.5),
         # ragged groups of odd sizes
-        _ffn("ffn_odd", 333, 20, 5, 1280, 640, skew=0.5, call="grouped"),
+        _experts("experts_odd", 333, 20, 5, 1280, 640, skew=0.5),
         # a prefill chunk over every expert of a layer: the weights' bytes bound it
-        _ffn("ffn_chunk", 4096, 256, 6, 4096, 2048, call="grouped"),
+        _experts("experts_chunk", 4096, 256, 6, 4096, 2048),
         # long groups: the products bound it
-        _ffn("ffn_long", 16384, 64, 6, 4096, 2048, skew=0.3, call="grouped"),
+        _experts("experts_long", 16384, 64, 6, 4096, 2048, skew=0.3),
     ]
 
 
@@ -78,12 +78,9 @@ def draw(rng):
     T = _log(rng, 1, 8192)
     if T <= 96:  # a decode step
         H, I = 128 * rng.randint(4, 32), 128 * rng.randint(3, 16)
-        call = "list"
     else:
         H, I = 256 * rng.randint(2, 16), 128 * rng.randint(3, 16)
-        call = "grouped"
-    return dict(op="ffn", T=T, E=rng.randint(max(8, k), 96), k=k, H=H, I=I, skew=rng.choice([0.0, 0.4, 0.8]),
-                call=call)
+    return dict(op="experts", T=T, E=rng.randint(max(8, k), 96), k=k, H=H, I=I, skew=rng.choice([0.0, 0.4, 0.8]))
 
 
 def work(case):
@@ -124,7 +121,7 @@ def _select_inputs(case, seed):
     return dict(logits=logits, balance=balance)
 
 
-def _ffn_inputs(case, seed):
+def _experts_inputs(case, seed):
     T, E, k, H, I = (case[n] for n in ("T", "E", "k", "H", "I"))
     g = _gen(seed, 2)
     st = dict(q1=_codes((E, H, I), g), q3=_codes((E, H, I), g), q2=_codes((E, I, H), g))
@@ -148,9 +145,9 @@ def _ffn_inputs(case, seed):
     st["offsets"] = offsets.to(torch.int32)
     st["perm_src"] = (order // k).to(torch.int32)
     st["perm_pos"] = pos.reshape(T, k).to(torch.int32)
-    # the plan on the host, as a decode step's cache resolve leaves it: {expert, slot, first row, rows}
+    # {expert, first row, rows} of the experts with rows, for the plain forms
     c, o = counts.tolist(), offsets.tolist()
-    st["plan"] = np.array([[e, e, o[e], c[e]] for e in range(E) if c[e] > 0], dtype=np.int32)
+    st["plan"] = np.array([[e, o[e], c[e]] for e in range(E) if c[e] > 0], dtype=np.int32)
     return st
 
 
@@ -175,21 +172,20 @@ def prepare(case, seed):
                              perm_src=torch.empty(T * k, **i32), perm_pos=torch.empty((T, k), **i32))
             st["ws"] = torch.empty(L.moe_select_workspace_size(T, E, k), dtype=torch.uint8, device=DEV)
     else:
-        st = _ffn_inputs(case, seed)
+        st = _experts_inputs(case, seed)
         st["order"] = torch.from_numpy(st["plan"][:, 0].astype(np.int64)).to(DEV)
         if own:
             from routed_expert_layer_amd import _lib as L
             H, I = case["H"], case["I"]
             stride = (L.moe_expert_bytes(L.MOE_W_INT8, H, I) + 4095) // 4096 * 4096
             slots = torch.empty(E * stride, dtype=torch.uint8, device=DEV)
-            for e in range(E):
+            for e in range(E):  # expert e in slot E - 1 - e
                 L.moe_pack_expert(L.MOE_W_INT8, H, I, st["q1"][e], st["q3"][e], st["q2"][e], st["s1"][e], st["s3"][e],
-                                  st["s2"][e], slots[e * stride:])
-            rows = T * k
-            st.update(stride=stride, slots=slots, y=torch.empty((rows, H), device=DEV),
-                      xq=torch.empty((T, L.moe_quant_row_bytes(H)), dtype=torch.uint8, device=DEV),
-                      ws=torch.empty(L.moe_ffn_workspace_size(rows, H, I, L.MOE_W_INT8), dtype=torch.uint8, device=DEV),
-                      out=torch.empty((T, H), dtype=torch.bfloat16, device=DEV))
+                                  st["s2"][e], slots[(E - 1 - e) * stride:])
+            st.update(stride=stride, slots=slots, out=torch.empty((T, H), dtype=torch.bfloat16, device=DEV),
+                      slot_of=torch.arange(E - 1, -1, -1, dtype=torch.int32, device=DEV),
+                      ws=torch.empty(L.moe_experts_workspace_size(T, k, E, H, I, L.MOE_W_INT8), dtype=torch.uint8,
+                                     device=DEV))
     st["case"] = case
     return st
 
@@ -198,7 +194,7 @@ def prepare(case, seed):
 # one pass
 # -------------------------------------------------------------------------------------------------------------------
 def run(st):
-    return _run_select(st) if st["case"]["op"] == "select" else _run_ffn(st)
+    return _run_select(st) if st["case"]["op"] == "select" else _run_experts(st)
 
 
 def _run_select(st):
@@ -246,22 +242,16 @@ def _quantised(a):
     return q, amax / 127.0
 
 
-def _run_ffn(st):
+def _run_experts(st):
     case = st["case"]
     T, E, k, H, I = (case[n] for n in ("T", "E", "k", "H", "I"))
     if own:
         from routed_expert_layer_amd import _lib as L
-        L.moe_quantize(st["x"], st["xq"])
-        if case["call"] == "list":
-            L.moe_ffn(st["xq"], st["perm_src"], st["plan"], st["slots"], st["stride"], L.MOE_W_INT8, H, I, st["y"],
-                      st["ws"])
-        else:
-            L.moe_ffn_grouped(st["xq"], st["perm_src"], st["counts"], st["offsets"], None, E, T * k, st["slots"],
-                              st["stride"], L.MOE_W_INT8, H, I, st["y"], st["ws"])
-        L.moe_combine(st["y"], st["perm_pos"], st["topk_w"], st["out"])
+        L.moe_experts(st["x"], st["perm_src"], st["perm_pos"], st["topk_w"], st["counts"], st["offsets"], st["slot_of"],
+                      E, st["slots"], st["stride"], L.MOE_W_INT8, H, I, st["out"], st["ws"])
         return st["out"]
     plan, ex = st["plan"], st["order"]
-    n, cap = len(plan), int(plan[:, 3].max())
+    n, cap = len(plan), int(plan[:, 2].max())
     # every group padded to the longest one's rows; rows past a group's end are its last row again and are not used
     first = st["offsets"][ex].long()[:, None]
     last = first + st["counts"][ex].long()[:, None] - 1
@@ -286,7 +276,7 @@ def _run_ffn(st):
 # the definitions in 64 bits
 # -------------------------------------------------------------------------------------------------------------------
 def exact(case, seed):
-    return _exact_select(case, seed) if case["op"] == "select" else _exact_ffn(case, seed)
+    return _exact_select(case, seed) if case["op"] == "select" else _exact_experts(case, seed)
 
 
 def _exact_select(case, seed):
@@ -324,8 +314,8 @@ def _exact_select(case, seed):
                 perm_pos=i(pos.reshape(T, k)))
 
 
-def _exact_ffn(case, seed):
-    st = _ffn_inputs(case, seed)
+def _exact_experts(case, seed):
+    st = _experts_inputs(case, seed)
     H = case["H"]
 
     def codes(a):
@@ -335,7 +325,7 @@ def _exact_ffn(case, seed):
     out = torch.zeros((case["T"], H), dtype=torch.float64, device=DEV)
     weight = torch.zeros(case["T"] * case["k"], dtype=torch.float64, device=DEV)
     weight[st["perm_pos"].long().reshape(-1)] = st["topk_w"].double().reshape(-1)
-    for e, _, first, rows in st["plan"].tolist():
+    for e, first, rows in st["plan"].tolist():
         t = st["perm_src"][first:first + rows].long()
         qx, sx = codes(st["x"][t].double())
         g = (qx @ st["q1"][e].double()) * (sx * st["s1"][e].double())
