@@ -134,6 +134,7 @@ def _experts_inputs(case, seed):
     val, idx = torch.topk(score, k, dim=1)
     w = torch.exp(val - val[:, :1])
     st["topk_w"] = (w / w.sum(1, keepdim=True)).contiguous()
+    st["topk_idx"] = idx.to(torch.int32)
     flat = idx.reshape(-1)
     order = torch.argsort(flat, stable=True)
     pos = torch.empty_like(order)
@@ -247,8 +248,9 @@ def _run_experts(st):
     T, E, k, H, I = (case[n] for n in ("T", "E", "k", "H", "I"))
     if own:
         from routed_expert_layer_amd import _lib as L
-        L.moe_experts(st["x"], st["perm_src"], st["perm_pos"], st["topk_w"], st["counts"], st["offsets"], st["slot_of"],
-                      E, st["slots"], st["stride"], L.MOE_W_INT8, H, I, st["out"], st["ws"])
+        L.moe_experts(st["x"], st["topk_idx"], st["topk_w"], st["perm_src"], st["perm_pos"], st["counts"],
+                      st["offsets"], st["slot_of"], E, st["slots"], st["stride"], L.MOE_W_INT8, H, I, st["out"],
+                      st["ws"])
         return st["out"]
     plan, ex = st["plan"], st["order"]
     n, cap = len(plan), int(plan[:, 2].max())
