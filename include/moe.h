@@ -50,7 +50,7 @@ enum {
 enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 };
 
 /* Expert weight formats (the layout of one expert blob, see moe_pack_expert). */
-enum { MOE_W_F32 = 0, MOE_W_BF16 = 1, MOE_W_INT4 = 2, MOE_W_MXFP4 = 3 };
+enum { MOE_W_F32 = 0, MOE_W_BF16 = 1, MOE_W_INT4 = 2, MOE_W_MXFP4 = 3, MOE_W_INT8 = 4 };
 
 /* FFN kernel choice for moe_ffn. */
 enum { MOE_FFN_AUTO = 0, MOE_FFN_DECODE = 1, MOE_FFN_PREFILL = 2 };
@@ -119,6 +119,55 @@ int moe_route_noalloc(const void* x, int dtype, const void* Wr, const float* bia
                       void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * Gates with scores: the choice of experts by softmax or sigmoid scores, with
+ * a balance bias, groups of experts and scaled weights. For logits l of a
+ * token (E experts, n_group groups of E / n_group consecutive ones):
+ *   s_e = softmax(l)_e (over all experts) or 1 / (1 + exp(-l_e))
+ *   c_e = s_e + balance_e                  (the bias moves the choice only)
+ *   R_g = the largest c of group g (group_top 1), or the sum of its two
+ *         largest (group_top 2; of a group of one expert, its c)
+ *   the topk_group groups of largest R stay, equal ones the lower group first
+ *   S_t = the k largest c of their experts, largest first, equal ones the
+ *         lower expert first
+ *   w_j = s of S_t[j], divided by the sum over j when renorm is set (0 if that
+ *         sum is 0), times scale; rounded once to fp32
+ * Scores, sums and comparisons are those of 64-bit floating point. A NaN logit
+ * counts as -inf and a NaN c as -inf; an infinite largest logit takes all of
+ * the softmax (equal ones share it), and logits of -inf only share it evenly.
+ * The grouping outputs are moe_route's.
+ *
+ * moe_select: from logits, device fp32 [T, E]. Scratch of at least
+ *   moe_select_workspace_size(T, E, k) bytes, 16-byte aligned.
+ * moe_route_scored: from x and Wr, with moe_route's logits (bias [E] is added
+ *   to the logits), arguments, scratch and limits.
+ * Limits: 1 <= k <= min(E, 16), E <= 1024, n_group <= 64 dividing E,
+ * 1 <= topk_group <= n_group, k <= topk_group * (E / n_group), group_top 1 or
+ * 2, scale finite; balance device fp32 [E] or NULL. The gate is read during
+ * the call; its balance array must stay until the work has run. T = 0 writes
+ * counts = offsets = 0. Errors: MOE_EINVAL, MOE_EHIP.
+ *
+ * moe_decoder_set_gate, moe_device_decoder_set_gate: the decoder's later steps
+ * route with moe_route_scored under this gate (copied; NULL: moe_route again).
+ * A captured graph keeps the gate it was captured with.
+ * moe_prefill_layer_scored: moe_prefill_layer under a gate.
+ * ------------------------------------------------------------------------ */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct {
+  int32_t score, n_group, topk_group, group_top, renorm;
+  float scale;
+  const float* balance;
+} moe_gate_t;
+size_t moe_select_workspace_size(int T, int E, int k);
+int moe_select(const float* logits, const moe_gate_t* gate, int T, int E, int k,
+               int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* offsets,
+               int32_t* perm_src, int32_t* perm_pos, void* workspace, size_t ws_bytes, void* stream);
+int moe_route_scored(const void* x, int dtype, const void* Wr, const float* bias, const moe_gate_t* gate,
+                     int T, int H, int E, int k,
+                     int32_t* topk_idx, float* topk_w, float* logits,
+                     int32_t* counts, int32_t* offsets, int32_t* perm_src, int32_t* perm_pos,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * Expert blobs and the host pool.
  *
  * Page "FreeToken-rtx-4090": the complete expert pool lives in host memory
@@ -142,14 +191,25 @@ int moe_route_noalloc(const void* x, int dtype, const void* Wr, const float* bia
  * 1..254 with every dequantised weight a normal bf16 value (the kernels form
  * each weight exactly in bf16); activations stay bf16.
  *
+ * For MOE_W_INT8 the weights are q * s with int8 codes q of the same shapes
+ * and one fp32 scale per output channel: s1, s3 [I], s2 [H]. The activations
+ * are codes too: a row's scale is its largest magnitude / 127 and its codes
+ * 127 v / (largest magnitude) rounded to nearest even; the tokens (bf16) and
+ * each row of the SwiGLU product (fp32) are quantised so, and the products
+ * are exact integer sums times both scales. A row of zeros has scale 0; a row
+ * with an infinity or NaN has scale NaN, and so have its results.
+ *
  * moe_expert_bytes: size of one blob. Requirements: H and I multiples of 32
- * (bf16), of 128 (int4, MXFP4), I a multiple of 8; any H, I >= 1 for fp32.
+ * (bf16), of 128 (int4, MXFP4), of 64 (int8, H <= 16384, I <= 8192), I a
+ * multiple of 8; any H, I >= 1 for fp32.
  * moe_pack_expert: writes one blob from canonical device arrays, on `stream`.
  *   MOE_W_F32:  W1, W3, W2 fp32 device;  s1, s3, s2 ignored (NULL)
  *   MOE_W_BF16: W1, W3, W2 bf16 device;  s* ignored
  *   MOE_W_INT4: W1, W3, W2 are int8 codes (device), s1, s3, s2 fp16 device
  *   MOE_W_MXFP4: W1, W3, W2 are uint8 FP4 codes (device), s1, s3, s2 uint8
  *               E8M0 scales (device)
+ *   MOE_W_INT8: W1, W3, W2 are int8 codes (device), s1, s3, s2 fp32 device;
+ *               the blob 16-byte aligned
  *   blob: device out, moe_expert_bytes() bytes; the caller may then copy it
  *   into a pool or a cache slot.
  * moe_pool_alloc: page-locked host memory (hipHostMalloc) for the pool;
@@ -302,8 +362,10 @@ int cache_fill_async(moe_cache_t* cache, const moe_miss_t* misses, int n,
  * slot_base device base of the expert blobs; slot_stride bytes between slots
  * wfmt     MOE_W_F32 (x fp32), MOE_W_BF16, MOE_W_INT4 or MOE_W_MXFP4 (x bf16);
  *          the tiled GEMM (MOE_FFN_PREFILL) takes bf16 weights (H % 128,
- *          I % 64 == 0) and MXFP4 weights (H % 256 == 0); AUTO runs the
- *          matrix-vector kernels for the other formats
+ *          I % 64 == 0), MXFP4 weights (H % 256 == 0) and int8 weights
+ *          (H % 256 == 0, I % 128 == 0); AUTO runs the matrix-vector kernels
+ *          for the other formats. MOE_W_INT8 (x bf16, quantised here through
+ *          perm_src) needs 16-byte aligned x, slots, y_perm and workspace
  * y_perm   device out fp32 [rows_total, H] (only listed rows are written)
  * workspace device scratch, >= moe_ffn_workspace_size(rows_total, H, I, wfmt)
  *          bytes, where rows_total bounds every row index used
@@ -340,6 +402,34 @@ int moe_ffn_grouped(const void* x, int dtype, const int32_t* perm_src, const int
                     const int32_t* offsets, const int32_t* slot_of, int E, int n_slots, int rows_max,
                     const void* slot_base, size_t slot_stride, int wfmt, int H, int I, float* y_perm,
                     void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * The expert half of a layer with int8 experts: from the tokens and their
+ * routing (as moe_route, moe_route_scored or moe_select writes it) to the
+ * weighted output. The tokens are quantised, each expert's group of rows goes
+ * through its SwiGLU feed-forward (MOE_W_INT8, above) and
+ *   out[t, :] = sum_j topk_w[t,j] * y(t, S_t[j]),  j ascending, fp32 sums.
+ * Experts without a slot (slot_of[e] outside [0, n_slots)) are left out of the
+ * sum: a GPU that holds a part of a layer's experts gets that part's output.
+ * The work list is planned on the GPU: the call neither waits nor allocates
+ * and can be captured; launch shapes depend on T and the sizes only.
+ *   x        device bf16 [T, H] (dtype MOE_DT_BF16)
+ *   topk_idx, topk_w, perm_src, perm_pos, counts, offsets: device, a routing
+ *   slot_of  device int32 [E], or NULL for slot e (then n_slots >= E)
+ *   slots    n_slots blobs at slot_base, slot_stride bytes apart
+ *   wfmt     MOE_W_INT8; other formats run moe_ffn or moe_ffn_grouped, then
+ *            moe_combine
+ *   out      device [T, H] of out_dtype (fp32 or bf16)
+ *   workspace device scratch, >= moe_experts_workspace_size(...) bytes
+ * x, slots, out and workspace 16-byte aligned. Limits: E <= 1024; the codes of
+ * the tokens and of the T*k rows within 4 GiB each.
+ * Errors: MOE_EINVAL (null, sizes, formats, alignment), MOE_EHIP.
+ * ------------------------------------------------------------------------ */
+size_t moe_experts_workspace_size(int T, int k, int E, int H, int I, int wfmt);
+int moe_experts(const void* x, int dtype, const int32_t* topk_idx, const float* topk_w,
+                const int32_t* perm_src, const int32_t* perm_pos, const int32_t* counts, const int32_t* offsets,
+                const int32_t* slot_of, int T, int k, int E, int n_slots, const void* slot_base, size_t slot_stride,
+                int wfmt, int H, int I, void* out, int out_dtype, void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * Weighted combine. Page "FreeToken-rtx-4090", section "How the MoE Memory
@@ -448,6 +538,8 @@ int moe_clock_record(unsigned long long* sums);
  *   owns, for their expert's gate/up blocks (so one decoder's steps must
  *   stay ordered on one stream).
  *   out_dtype other than MOE_DT_F32 / MOE_DT_BF16 is MOE_EINVAL.
+ *   int8 experts (bf16 activations) run their two projections as two launches
+ *   behind the quantisation of the step's tokens.
  *   When the cache splits misses (moe_cache_set_split), the misses assigned
  *   to the CPU run with moe_cpu_ffn from the pool on the calling thread while
  *   the GPU works on the others (bf16 activations with bf16, int4 or MXFP4
@@ -499,6 +591,7 @@ int moe_decoder_ffn_stats(moe_decoder_t* decoder, double* bytes, double* ms, int
 int moe_decoder_fills(const moe_decoder_t* decoder, int64_t* fills);
 int moe_decoder_cpu_runs(const moe_decoder_t* decoder, int64_t* runs);
 int moe_decoder_resize(moe_decoder_t* decoder, int S_new, void* slot_base, void* stream);
+int moe_decoder_set_gate(moe_decoder_t* decoder, const moe_gate_t* gate);
 
 /* ---------------------------------------------------------------------------
  * Prefill layer.
@@ -513,11 +606,15 @@ int moe_decoder_resize(moe_decoder_t* decoder, int S_new, void* slot_base, void*
  * caller's device buffers as for moe_decoder_create, sized for T tokens
  * (logits may be NULL); after the call they hold the layer's routing and
  * y_perm. Requirements and errors as moe_route and moe_ffn_grouped (bf16
- * activations; bf16 or MXFP4 experts).
+ * activations; bf16 or MXFP4 experts). int8 experts run moe_experts instead
+ * (its requirements; expert e in slot e); y_perm is then scratch.
  * ------------------------------------------------------------------------- */
 int moe_prefill_layer(const void* x, int dtype, const void* Wr, const float* bias, int T, int H, int E, int k,
                       int I, int wfmt, const void* layer_base, size_t blob_stride, const moe_decoder_buffers_t* b,
                       void* out, int out_dtype, void* stream);
+int moe_prefill_layer_scored(const void* x, int dtype, const void* Wr, const float* bias, const moe_gate_t* gate,
+                             int T, int H, int E, int k, int I, int wfmt, const void* layer_base, size_t blob_stride,
+                             const moe_decoder_buffers_t* b, void* out, int out_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
  * CPU execution of an expert (page "FreeToken-rtx-4090", component table row
@@ -538,7 +635,7 @@ int moe_prefill_layer(const void* x, int dtype, const void* Wr, const float* bia
  *   GPU. threads: participating threads (<= 0: all, see moe_cpu_threads);
  *   the library keeps one process-wide pool of worker threads, and calls from
  *   several host threads at once are serialised by the caller. Synchronous.
- *   Errors: EINVAL for null pointers, negative rows, fp32 weights, or H, I
+ *   Errors: EINVAL for null pointers, negative rows, fp32 or int8 weights, or H, I
  *   not multiples of 32 (bf16) or 128 (int4, MXFP4). Needs a CPU with
  *   AVX-512 BF16.
  * moe_cpu_threads: the number of threads moe_cpu_ffn can use (workers + the
@@ -584,7 +681,7 @@ int moe_cpu_threads(void);
  *   through into its slot as it goes (the fill; both projections run as one
  *   launch, numbered by the resolve's call counter, unless the down
  *   projection forms `out`);
- *   for fp32 experts a fill
+ *   for fp32 and int8 experts a fill
  *   kernel first copies the misses' blobs into their slots (returning at once
  *   when there are none) and the FFN then reads every item from its slot.
  *   It neither waits for the GPU nor allocates, so the same call can be
@@ -633,6 +730,7 @@ int moe_device_decoder_trace(const moe_device_decoder_t* decoder, moe_trace_t* o
 int moe_device_decoder_clear_trace(moe_device_decoder_t* decoder);
 int moe_device_decoder_slot_of(const moe_device_decoder_t* decoder, int key, int* slot);
 int moe_device_decoder_resize(moe_device_decoder_t* decoder, int S_new, void* slot_base, void* stream);
+int moe_device_decoder_set_gate(moe_device_decoder_t* decoder, const moe_gate_t* gate);
 
 int moe_graph_begin(void* stream);
 moe_graph_t* moe_graph_end(void* stream, int* status);

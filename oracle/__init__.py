@@ -12,3 +12,4 @@ from .moe import (  # noqa: F401
     expert_outputs, combine, dequant_int4, moe_layer, e2m1_value, E2M1, e8m0_value, dequant_mxfp4,
 )
 from .lru import SharedLRU, TraceRec  # noqa: F401
+from .scored import gate_scores, gate_select, quantise_rows, int8_expert  # noqa: F401

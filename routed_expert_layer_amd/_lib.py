@@ -14,7 +14,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_ECAPACITY, MOE_EHIP, MOE_ENOMEM, MOE_ESTATE = 0, -1, -2, -3, -4, -5
 MOE_DT_F32, MOE_DT_BF16 = 0, 1
-MOE_W_F32, MOE_W_BF16, MOE_W_INT4, MOE_W_MXFP4 = 0, 1, 2, 3
+MOE_W_F32, MOE_W_BF16, MOE_W_INT4, MOE_W_MXFP4, MOE_W_INT8 = 0, 1, 2, 3, 4
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_FFN_AUTO, MOE_FFN_DECODE, MOE_FFN_PREFILL = 0, 1, 2
 
 # Every symbol include/moe.h declares.
@@ -31,6 +32,8 @@ SYMBOLS = [
     "moe_graph_begin", "moe_graph_end", "moe_graph_launch", "moe_graph_destroy",
     "moe_cache_resize", "moe_cache_capacity", "moe_decoder_resize", "moe_device_decoder_resize",
     "moe_ffn_grouped", "moe_prefill_layer", "moe_route_noalloc",
+    "moe_select_workspace_size", "moe_select", "moe_route_scored", "moe_experts_workspace_size", "moe_experts",
+    "moe_prefill_layer_scored", "moe_decoder_set_gate", "moe_device_decoder_set_gate",
 ]
 
 
@@ -39,6 +42,22 @@ class DecoderBuffers(ctypes.Structure):
                 ("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("perm_src", ctypes.c_void_p),
                 ("perm_pos", ctypes.c_void_p), ("y_perm", ctypes.c_void_p), ("route_ws", ctypes.c_void_p),
                 ("route_ws_bytes", ctypes.c_size_t), ("ffn_ws", ctypes.c_void_p), ("ffn_ws_bytes", ctypes.c_size_t)]
+
+
+class Gate(ctypes.Structure):
+    """moe_gate_t: softmax or sigmoid scores, a balance bias for the choice alone (GPU fp32 tensor [E] or None, kept
+    alive here), groups of experts of which each token keeps topk_group, and the weights' renormalisation and scale."""
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("_balance", ctypes.c_void_p)]
+
+    def __init__(self, score="softmax", n_group=1, topk_group=1, group_top=1, renorm=True, scale=1.0, balance=None):
+        names = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+        if isinstance(score, str) and score not in names:
+            raise ValueError(f"unknown score {score!r}")
+        super().__init__(names.get(score, score), n_group, topk_group, group_top, int(bool(renorm)), scale,
+                         _dptr(_typed(balance, "float32", "balance")))
+        self.balance = balance
 
 
 class MoEError(RuntimeError):
@@ -71,6 +90,14 @@ _sig("moe_abi_version", I32)
 _sig("moe_route_workspace_size", SZ, I32, I32, I32, I32)
 _sig("moe_route", I32, P, I32, P, P, I32, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P)
 _sig("moe_route_noalloc", I32, P, I32, P, P, I32, I32, I32, I32, P, P, P, P, P, P, P, P)
+PG = ctypes.POINTER(Gate)
+_sig("moe_select_workspace_size", SZ, I32, I32, I32)
+_sig("moe_select", I32, P, PG, I32, I32, I32, P, P, P, P, P, P, P, SZ, P)
+_sig("moe_route_scored", I32, P, I32, P, P, PG, I32, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P)
+_sig("moe_experts_workspace_size", SZ, I32, I32, I32, I32, I32, I32)
+_sig("moe_experts", I32, P, I32, P, P, P, P, P, P, P, I32, I32, I32, I32, P, SZ, I32, I32, I32, P, I32, P, SZ, P)
+_sig("moe_decoder_set_gate", I32, P, PG)
+_sig("moe_device_decoder_set_gate", I32, P, PG)
 _sig("moe_expert_bytes", SZ, I32, I32, I32)
 _sig("moe_pack_expert", I32, I32, I32, I32, P, P, P, P, P, P, P, P)
 _sig("moe_pool_alloc", P, SZ, PI)
@@ -121,6 +148,8 @@ _sig("moe_cache_capacity", I32, P)
 _sig("moe_decoder_resize", I32, P, I32, P, P)
 _sig("moe_prefill_layer", I32, P, I32, P, P, I32, I32, I32, I32, I32, I32, P, SZ, ctypes.POINTER(DecoderBuffers), P,
      I32, P)
+_sig("moe_prefill_layer_scored", I32, P, I32, P, P, PG, I32, I32, I32, I32, I32, I32, P, SZ,
+     ctypes.POINTER(DecoderBuffers), P, I32, P)
 _sig("moe_device_decoder_resize", I32, P, I32, P, P)
 
 
@@ -151,6 +180,33 @@ def _dptr(t):
     if t is not None and not isinstance(t, int) and (isinstance(t, np.ndarray) or not t.is_cuda):
         raise ValueError("the library takes a GPU tensor for this argument")
     return _ptr(t)
+
+
+def _typed(t, dtype, name, shape=None):
+    """t, refused unless it has that torch dtype (by name) and, with `shape`, that shape. None passes."""
+    if t is not None and not isinstance(t, int):
+        if str(t.dtype) != "torch." + dtype:
+            raise ValueError(f"{name}: a {dtype} tensor is needed, not {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(shape)} is needed, not {tuple(t.shape)}")
+    return t
+
+
+def _routing_args(T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos):
+    """Addresses of a routing's arrays after a check of their types and sizes."""
+    if perm_src.numel() < T * k or str(perm_src.dtype) != "torch.int32":
+        raise ValueError(f"perm_src: int32 of at least {T * k} entries is needed")
+    return [_dptr(_typed(topk_idx, "int32", "topk_idx", (T, k))), _dptr(_typed(topk_w, "float32", "topk_w", (T, k))),
+            _dptr(_typed(counts, "int32", "counts", (E,))), _dptr(_typed(offsets, "int32", "offsets", (E + 1,))),
+            _dptr(perm_src), _dptr(_typed(perm_pos, "int32", "perm_pos", (T, k)))]
+
+
+def _gate_ref(gate, E=None):
+    if gate is None:
+        return None
+    if E is not None:
+        _typed(gate.balance, "float32", "balance", (E,))
+    return ctypes.byref(gate)
 
 
 def _nbytes(t):
@@ -203,6 +259,29 @@ def moe_route_noalloc(x, Wr, bias, k, topk_idx, topk_w, logits, counts, offsets,
     _check(_lib.moe_route_noalloc(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias), T, H, E, k, _dptr(topk_idx),
                                   _dptr(topk_w), _dptr(logits), _dptr(counts), _dptr(offsets), _dptr(perm_src),
                                   _dptr(perm_pos), _stream(stream)), "moe_route_noalloc")
+
+
+def moe_select_workspace_size(T, E, k):
+    return _lib.moe_select_workspace_size(T, E, k)
+
+
+def moe_select(logits, gate, k, topk_idx, topk_w, counts, offsets, perm_src, perm_pos, workspace, stream=None):
+    """logits: GPU fp32 [T, E]; gate: a Gate; outputs as moe_route's."""
+    T, E = logits.shape
+    idx, w, c, o, ps, pp = _routing_args(T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos)
+    _check(_lib.moe_select(_dptr(_typed(logits, "float32", "logits")), _gate_ref(gate, E), T, E, k, idx, w, c, o, ps, pp,
+                           _dptr(workspace), _nbytes(workspace), _stream(stream)), "moe_select")
+
+
+def moe_route_scored(x, Wr, bias, gate, k, topk_idx, topk_w, logits, counts, offsets, perm_src, perm_pos, workspace,
+                     stream=None):
+    """moe_route with the choice and the weights of a Gate."""
+    T, H = x.shape
+    E = Wr.shape[1]
+    _check(_lib.moe_route_scored(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias), _gate_ref(gate, E), T, H, E, k,
+                                 _dptr(topk_idx), _dptr(topk_w), _dptr(logits), _dptr(counts), _dptr(offsets),
+                                 _dptr(perm_src), _dptr(perm_pos), _dptr(workspace), _nbytes(workspace),
+                                 _stream(stream)), "moe_route_scored")
 
 
 # ---------------------------------------------------------------------------
@@ -336,6 +415,27 @@ def moe_ffn_grouped(x, perm_src, counts, offsets, slot_of, n_slots, rows_max, sl
            "moe_ffn_grouped")
 
 
+def moe_experts_workspace_size(T, k, E, H, I, wfmt):
+    return _lib.moe_experts_workspace_size(T, k, E, H, I, wfmt)
+
+
+def moe_experts(x, topk_idx, topk_w, perm_src, perm_pos, counts, offsets, slot_of, n_slots, slot_base, slot_stride,
+                wfmt, H, I, out, workspace, stream=None):
+    """The expert half of a layer with int8 experts: x bf16 [T, H] and a routing on the GPU to out [T, H]. slot_of:
+    int32 [E] or None (expert e in slot e); experts without a slot are left out of the sum."""
+    T, k = perm_pos.shape
+    E = counts.shape[0]
+    if tuple(x.shape) != (T, H) or tuple(out.shape) != (T, H):
+        raise ValueError(f"moe_experts: x and out must be [{T}, {H}]")
+    if not isinstance(slot_base, int) and slot_base.numel() * slot_base.element_size() < n_slots * slot_stride:
+        raise ValueError(f"moe_experts: slot_base holds fewer than {n_slots} slots of {slot_stride} bytes")
+    idx, w, c, o, ps, pp = _routing_args(T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos)
+    _check(_lib.moe_experts(_dptr(x), _dtype_code(x), idx, w, ps, pp, c, o,
+                            _dptr(_typed(slot_of, "int32", "slot_of", (E,))), T, k, E, n_slots, _dptr(slot_base),
+                            slot_stride, wfmt, H, I, _dptr(out), _dtype_code(out), _dptr(workspace),
+                            _nbytes(workspace), _stream(stream)), "moe_experts")
+
+
 def moe_combine(y_perm, perm_pos, topk_w, out, stream=None):
     T, k = perm_pos.shape
     H = y_perm.shape[1]
@@ -456,6 +556,26 @@ def moe_prefill_layer(x, Wr, bias, k, I, wfmt, layer_base, blob_stride, bufs, ou
     _check(_lib.moe_prefill_layer(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias), T, H, E, k, I, wfmt,
                                   _dptr(layer_base), blob_stride, ctypes.byref(bufs), _dptr(out), _dtype_code(out),
                                   _stream(stream)), "moe_prefill_layer")
+
+
+def moe_prefill_layer_scored(x, Wr, bias, gate, k, I, wfmt, layer_base, blob_stride, bufs, out, stream=None):
+    """moe_prefill_layer under a Gate."""
+    T, H = x.shape
+    E = Wr.shape[1]
+    _check(_lib.moe_prefill_layer_scored(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias), _gate_ref(gate, E), T, H, E,
+                                         k, I, wfmt, _dptr(layer_base), blob_stride, ctypes.byref(bufs), _dptr(out),
+                                         _dtype_code(out), _stream(stream)), "moe_prefill_layer_scored")
+
+
+def moe_decoder_set_gate(dec, gate):
+    """gate: a Gate (its balance tensor is kept alive with the decoder) or None for moe_route's softmax."""
+    _check(_lib.moe_decoder_set_gate(dec.h, _gate_ref(gate)), "moe_decoder_set_gate")
+    dec.gate = gate
+
+
+def moe_device_decoder_set_gate(dec, gate):
+    _check(_lib.moe_device_decoder_set_gate(dec.h, _gate_ref(gate)), "moe_device_decoder_set_gate")
+    dec.gate = gate
 
 
 def decoder_buffers(bufs):

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/moe.h"
+#include "int8_layout.hpp"
 #include "lru_policy.hpp"
 #include "moe_kernels.hpp"
 
@@ -121,21 +122,25 @@ static bool shape_ok(int wfmt, int H, int I) {
   if (wfmt == MOE_W_F32) return true;
   if (wfmt == MOE_W_BF16) return H % 32 == 0 && I % 32 == 0;
   if (wfmt == MOE_W_INT4 || wfmt == MOE_W_MXFP4) return H % 128 == 0 && I % 128 == 0;
+  if (wfmt == MOE_W_INT8) return moe::int8_shape_ok(H, I);
   return false;
 }
 
 size_t moe_expert_bytes(int wfmt, int H, int I) {
   if (!shape_ok(wfmt, H, I)) return 0;
-  return moe::blob_layout(wfmt, H, I).bytes;
+  return wfmt == MOE_W_INT8 ? moe::int8_layout(H, I).bytes : moe::blob_layout(wfmt, H, I).bytes;
 }
 
 int moe_pack_expert(int wfmt, int H, int I, const void* W1, const void* W3, const void* W2, const void* s1,
                     const void* s3, const void* s2, void* blob, void* stream) {
   if (!shape_ok(wfmt, H, I)) return fail(MOE_EINVAL, "moe_pack_expert: unsupported format/shape %d %dx%d", wfmt, H, I);
   if (!W1 || !W3 || !W2 || !blob) return fail(MOE_EINVAL, "moe_pack_expert: null pointer argument");
-  if ((wfmt == MOE_W_INT4 || wfmt == MOE_W_MXFP4) && (!s1 || !s3 || !s2))
-    return fail(MOE_EINVAL, "moe_pack_expert: int4 and MXFP4 need scales");
-  hipError_t e = moe::launch_pack(wfmt, H, I, W1, W3, W2, s1, s3, s2, blob, as_stream(stream));
+  if ((wfmt == MOE_W_INT4 || wfmt == MOE_W_MXFP4 || wfmt == MOE_W_INT8) && (!s1 || !s3 || !s2))
+    return fail(MOE_EINVAL, "moe_pack_expert: int4, MXFP4 and int8 need scales");
+  if (wfmt == MOE_W_INT8 && (reinterpret_cast<uintptr_t>(blob) & 15))
+    return fail(MOE_EINVAL, "moe_pack_expert: the blob must be 16-byte aligned");
+  hipError_t e = wfmt == MOE_W_INT8 ? moe::launch_pack_int8(H, I, W1, W3, W2, s1, s3, s2, blob, as_stream(stream))
+                                    : moe::launch_pack(wfmt, H, I, W1, W3, W2, s1, s3, s2, blob, as_stream(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_pack_expert");
 }
 
@@ -397,6 +402,7 @@ extern "C" {
 // ---------------------------------------------------------------------------
 size_t moe_ffn_workspace_size(int rows_total, int H, int I, int wfmt) {
   if (rows_total < 0 || !shape_ok(wfmt, H, I)) return 0;
+  if (wfmt == MOE_W_INT8) return moe::int8_ws(rows_total, rows_total, H, I).bytes;
   // h: one row of I per routed row, plus one 16-row tile of slack for the
   // prefill GEMM's tiled h layout
   const size_t hb = moe::align_up((size_t)(rows_total + 16) * I * (wfmt == MOE_W_F32 ? 4 : 2), 256);
@@ -413,7 +419,7 @@ int moe_ffn(const void* x, int dtype, const int32_t* perm_src, const moe_work_t*
     return fail(MOE_EINVAL, "moe_ffn: null pointer or negative count");
   if (mode < MOE_FFN_AUTO || mode > MOE_FFN_PREFILL) return fail(MOE_EINVAL, "moe_ffn: bad mode %d", mode);
   if (n_work == 0) return MOE_OK;
-  const size_t blob = moe::blob_layout(wfmt, H, I).bytes;
+  const size_t blob = moe_expert_bytes(wfmt, H, I);
   if (slot_stride < blob) return fail(MOE_EINVAL, "moe_ffn: slot_stride %zu < blob size %zu", slot_stride, blob);
   int rows_total = 0, max_rows = 0;
   for (int i = 0; i < n_work; ++i) {
@@ -426,15 +432,36 @@ int moe_ffn(const void* x, int dtype, const int32_t* perm_src, const moe_work_t*
   if (ws_bytes < moe_ffn_workspace_size(rows_total, H, I, wfmt))
     return fail(MOE_EINVAL, "moe_ffn: workspace too small for %d rows", rows_total);
   bool prefill = false;
-  const bool gemm_ok = wfmt == MOE_W_MXFP4 ? moe::prefill_mxfp4_supported(H, I) : moe::prefill_supported(wfmt, H, I);
+  const bool gemm_ok = wfmt == MOE_W_MXFP4  ? moe::prefill_mxfp4_supported(H, I)
+                       : wfmt == MOE_W_INT8 ? moe::int8_gemm_supported(H, I)
+                                            : moe::prefill_supported(wfmt, H, I);
   if (mode == MOE_FFN_PREFILL) {
     if (!gemm_ok)
       return fail(MOE_EINVAL,
-                  "moe_ffn: prefill GEMM needs bf16 weights with H %% 128 == 0 and I %% 64 == 0, or MXFP4 weights "
-                  "with H %% 256 == 0");
+                  "moe_ffn: prefill GEMM needs bf16 weights with H %% 128 == 0 and I %% 64 == 0, MXFP4 weights "
+                  "with H %% 256 == 0, or int8 weights with H %% 256 == 0 and I %% 128 == 0");
     prefill = true;
   } else if (mode == MOE_FFN_AUTO) {
     prefill = max_rows > 32 && gemm_ok;
+  }
+  if (wfmt == MOE_W_INT8) {
+    if (!moe::int8_rows_ok(rows_total, rows_total, H, I))
+      return fail(MOE_EINVAL, "moe_ffn: %d rows of int8 codes pass 32-bit offsets", rows_total);
+    if (!moe::aligned16(x, slot_base, y_perm, workspace) || slot_stride % 16 != 0)
+      return fail(MOE_EINVAL, "moe_ffn: int8 experts need 16-byte aligned buffers and slots");
+    try {
+      std::vector<int4> items;
+      items.reserve(n_work);
+      for (int i = 0; i < n_work; ++i)
+        if (work[i].rows > 0)
+          items.push_back(make_int4(work[i].slot, work[i].row_begin, work[i].rows, work[i].expert));
+      hipError_t e = moe::launch_ffn_int8_list(x, perm_src, items.data(), (int)items.size(), rows_total, prefill,
+                                               static_cast<const char*>(slot_base), slot_stride, H, I, y_perm,
+                                               workspace, as_stream(stream));
+      return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_ffn launch");
+    } catch (const std::bad_alloc&) {
+      return fail(MOE_ENOMEM, "moe_ffn: out of host memory");
+    }
   }
   char* ws = static_cast<char*>(workspace);
   void* hbuf = ws;
@@ -627,24 +654,57 @@ int moe_pipe_end_layer(moe_pipe_t* p, int layer, void* compute_stream) {
 // ---------------------------------------------------------------------------
 // Prefill layer: routing, grouped FFN over the device work list, combine
 // ---------------------------------------------------------------------------
-int moe_prefill_layer(const void* x, int dtype, const void* Wr, const float* bias, int T, int H, int E, int k, int I,
-                      int wfmt, const void* layer_base, size_t blob_stride, const moe_decoder_buffers_t* b, void* out,
-                      int out_dtype, void* stream) {
+static int prefill_layer(const void* x, int dtype, const void* Wr, const float* bias, const moe_gate_t* gate, int T,
+                         int H, int E, int k, int I, int wfmt, const void* layer_base, size_t blob_stride,
+                         const moe_decoder_buffers_t* b, void* out, int out_dtype, void* stream) {
   if (!b) return fail(MOE_EINVAL, "moe_prefill_layer: null buffers");
   if (T < 0 || H <= 0 || E <= 0 || k <= 0 || (long long)T * k > (1ll << 30))
     return fail(MOE_EINVAL, "moe_prefill_layer: bad sizes T=%d H=%d E=%d k=%d", T, H, E, k);
-  if (!moe::grouped_supported(wfmt, H, I) || dtype != MOE_DT_BF16)
-    return fail(MOE_EINVAL, "moe_prefill_layer: needs bf16 activations and bf16 or MXFP4 experts of a shape the "
-                            "grouped GEMM takes (format %d, %dx%d)", wfmt, H, I);
+  const bool int8 = wfmt == MOE_W_INT8;
+  if (!(int8 ? moe::int8_shape_ok(H, I) : moe::grouped_supported(wfmt, H, I)) || dtype != MOE_DT_BF16)
+    return fail(MOE_EINVAL, "moe_prefill_layer: needs bf16 activations and int8 experts, or bf16 or MXFP4 experts of "
+                            "a shape the grouped GEMM takes (format %d, %dx%d)", wfmt, H, I);
+  if (int8 && T > 0) {  // the expert half's own checks first: nothing is launched for a call that is refused
+    const int rc = moe::check_experts_int8("moe_prefill_layer", x, T, H, E, k, I, E, layer_base, blob_stride, out,
+                                           b->ffn_ws, b->ffn_ws_bytes, b->y_perm);
+    if (rc != MOE_OK) return rc;
+  }
   if (T > 0 && (!out || !b->y_perm || !layer_base)) return fail(MOE_EINVAL, "moe_prefill_layer: null pointer");
   if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16) return fail(MOE_EINVAL, "moe_prefill_layer: bad out dtype");
-  int rc = moe_route(x, dtype, Wr, bias, T, H, E, k, b->topk_idx, b->topk_w, b->logits, b->counts, b->offsets,
-                     b->perm_src, b->perm_pos, b->route_ws, b->route_ws_bytes, stream);
+  int rc = gate ? moe_route_scored(x, dtype, Wr, bias, gate, T, H, E, k, b->topk_idx, b->topk_w, b->logits, b->counts,
+                                   b->offsets, b->perm_src, b->perm_pos, b->route_ws, b->route_ws_bytes, stream)
+                : moe_route(x, dtype, Wr, bias, T, H, E, k, b->topk_idx, b->topk_w, b->logits, b->counts, b->offsets,
+                            b->perm_src, b->perm_pos, b->route_ws, b->route_ws_bytes, stream);
   if (rc != MOE_OK || T == 0) return rc;
+  if (int8) {
+    hipError_t e = moe::launch_experts_int8(x, T, k, E, b->topk_idx, b->topk_w, b->perm_src, b->perm_pos, b->counts,
+                                            b->offsets, nullptr, E, static_cast<const char*>(layer_base), blob_stride,
+                                            H, I, out, out_dtype == MOE_DT_BF16, b->ffn_ws, b->y_perm,
+                                            as_stream(stream));
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_prefill_layer");
+  }
   rc = moe_ffn_grouped(x, dtype, b->perm_src, b->counts, b->offsets, nullptr, E, E, T * k, layer_base, blob_stride,
                        wfmt, H, I, b->y_perm, b->ffn_ws, b->ffn_ws_bytes, stream);
   if (rc != MOE_OK) return rc;
   return moe_combine(b->y_perm, b->perm_pos, b->topk_w, T, k, H, out, out_dtype, stream);
+}
+
+int moe_prefill_layer(const void* x, int dtype, const void* Wr, const float* bias, int T, int H, int E, int k, int I,
+                      int wfmt, const void* layer_base, size_t blob_stride, const moe_decoder_buffers_t* b, void* out,
+                      int out_dtype, void* stream) {
+  return prefill_layer(x, dtype, Wr, bias, nullptr, T, H, E, k, I, wfmt, layer_base, blob_stride, b, out, out_dtype,
+                       stream);
+}
+
+int moe_prefill_layer_scored(const void* x, int dtype, const void* Wr, const float* bias, const moe_gate_t* gate,
+                             int T, int H, int E, int k, int I, int wfmt, const void* layer_base, size_t blob_stride,
+                             const moe_decoder_buffers_t* b, void* out, int out_dtype, void* stream) {
+  moe::GateArgs ga;
+  if (T < 0 || E <= 0 || k <= 0) return fail(MOE_EINVAL, "moe_prefill_layer_scored: bad sizes T=%d E=%d k=%d", T, E, k);
+  const int rc = moe::gate_args("moe_prefill_layer_scored", gate, E, k, &ga);
+  if (rc != MOE_OK) return rc;
+  return prefill_layer(x, dtype, Wr, bias, gate, T, H, E, k, I, wfmt, layer_base, blob_stride, b, out, out_dtype,
+                       stream);
 }
 
 int moe_clock_record(unsigned long long* sums) {

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "../../include/moe.h"
+#include "int8_layout.hpp"
 #include "moe_kernels.hpp"
 
 extern "C" const char* moe_last_error(void);
@@ -79,6 +80,8 @@ struct moe_decoder {
   uint64_t* ffn_flags = nullptr;   // device: hand-off flags of the one-launch FFN (zeroed at creation)
   uint64_t ffn_seq = 0;            // the last call's flag value
   int n_layers = 0;
+  moe::GateArgs gate{};  // with has_gate: the choice and weights of every step's routing
+  bool has_gate = false;
 };
 
 extern "C" {
@@ -111,6 +114,10 @@ moe_decoder_t* moe_decoder_create(moe_cache_t* cache, int T_max, int H, int I, i
   if (dtype != MOE_DT_F32 && dtype != MOE_DT_BF16) return bad(MOE_EINVAL, "bad activation dtype");
   const size_t blob = moe_expert_bytes(wfmt, H, I);
   if (blob == 0) return bad(MOE_EINVAL, "unsupported weight format or shape");
+  if (wfmt == MOE_W_INT8 && dtype != MOE_DT_BF16) return bad(MOE_EINVAL, "int8 experts need bf16 activations");
+  if (wfmt == MOE_W_INT8 && (!moe::aligned16(slot_base, buffers->y_perm, buffers->ffn_ws) || slot_stride % 16 != 0 ||
+                             !moe::int8_rows_ok((size_t)T_max * k, (size_t)T_max * k, H, I)))
+    return bad(MOE_EINVAL, "int8 experts need 16-byte aligned buffers and slots, and codes within 32-bit offsets");
   if (blob_stride < blob || slot_stride < blob) return bad(MOE_EINVAL, "stride smaller than an expert blob");
   const moe_decoder_buffers_t& b = *buffers;
   if (!b.topk_idx || !b.topk_w || !b.counts || !b.offsets || !b.perm_src || !b.perm_pos || !b.y_perm ||
@@ -294,12 +301,13 @@ int moe_decoder_step(moe_decoder_t* d, int step, int layer, const void* x, int T
   }
   hipError_t e = moe::launch_route(x, d->dtype == MOE_DT_BF16, Wr, bias, T, d->H, d->E, d->k, b.topk_idx, b.topk_w,
                                    b.logits, b.counts, b.offsets, b.perm_src, b.perm_pos, b.route_ws, s,
-                                   d->counts_dev, seq, early_hits ? &res : nullptr);
+                                   d->counts_dev, seq, early_hits ? &res : nullptr, nullptr,
+                                   d->has_gate ? &d->gate : nullptr);
   if (e == hipSuccess) d->pending.n = 0;
   const bool split = moe_cache_splits(d->cache);
   if (split && e == hipSuccess) {
     // misses may run on the CPU: it needs this step's activations and token order
-    if (d->dtype != MOE_DT_BF16 || d->wfmt == MOE_W_F32)
+    if (d->dtype != MOE_DT_BF16 || d->wfmt == MOE_W_F32 || d->wfmt == MOE_W_INT8)
       return dfail(MOE_EINVAL,
                    "moe_decoder_step: CPU execution of misses needs bf16 activations and bf16, int4 or MXFP4 weights");
     if (!d->x_host) {
@@ -351,7 +359,11 @@ int moe_decoder_step(moe_decoder_t* d, int step, int layer, const void* x, int T
       e = moe::launch_ffn_decode_fused(d->wfmt, x, b.perm_src, d->hit_n, d->hit_items, std::min(d->E, d->k * T),
                                        static_cast<const char*>(d->slot_base), d->slot_stride, d->H, d->I, b.ffn_ws,
                                        b.y_perm, d->ffn_flags, d->ffn_seq, s);
-    } else if (e == hipSuccess)
+    } else if (e == hipSuccess && d->wfmt == MOE_W_INT8)
+      e = moe::launch_ffn_int8_dev(x, T, b.perm_src, d->hit_n, d->hit_items, std::min(d->E, d->k * T), d->Tmax * d->k,
+                                   static_cast<const char*>(d->slot_base), d->slot_stride, d->H, d->I, b.y_perm,
+                                   b.ffn_ws, s);
+    else if (e == hipSuccess)
       e = moe::launch_ffn_decode_dev(d->wfmt, x, b.perm_src, d->hit_n, d->hit_items, std::min(d->E, d->k * T), T,
                                      static_cast<const char*>(d->slot_base), d->slot_stride, d->H, d->I, b.ffn_ws,
                                      b.y_perm, s);
@@ -420,7 +432,7 @@ int moe_decoder_step(moe_decoder_t* d, int step, int layer, const void* x, int T
     // then held all of them, so a fused launch has formed `out`)
     all_resident = nm == 0 && hits == n && n > 0;
     if (d->prof_every > 0 && all_resident && d->prof_calls++ % d->prof_every == 0 && prof_open) {
-      const double a = d->dtype == MOE_DT_BF16 ? 2.0 : 4.0, h = d->wfmt == MOE_W_F32 ? 4.0 : 2.0;
+      const double a = d->dtype == MOE_DT_BF16 ? 2.0 : 4.0, h = d->wfmt == MOE_W_F32 || d->wfmt == MOE_W_INT8 ? 4.0 : 2.0;
       d->ev_bytes[d->ev_used] = (double)hits * (double)d->blob_bytes +
                                 (double)rows * (d->H * a + 2.0 * d->I * h + d->H * 4.0) +
                                 (fused ? (double)T * d->H * (out_dtype == MOE_DT_BF16 ? 2.0 : 4.0) : 0.0);
@@ -517,7 +529,7 @@ int moe_decoder_step(moe_decoder_t* d, int step, int layer, const void* x, int T
                    d->wfmt, d->H, d->I, b.y_perm, b.ffn_ws, b.ffn_ws_bytes, MOE_FFN_AUTO, stream);
       if (rc != MOE_OK) return dfail(rc, "moe_decoder_step: %s", moe_last_error());
       if (prof) {
-        const double a = d->dtype == MOE_DT_BF16 ? 2.0 : 4.0, h = d->wfmt == MOE_W_F32 ? 4.0 : 2.0;
+        const double a = d->dtype == MOE_DT_BF16 ? 2.0 : 4.0, h = d->wfmt == MOE_W_F32 || d->wfmt == MOE_W_INT8 ? 4.0 : 2.0;
         const double bytes = (double)d->work.size() * (double)d->blob_bytes +
                              (double)rows * (d->H * a + 2.0 * d->I * h + d->H * 4.0);
         if (record_ffn_event(d, false, s, bytes) != MOE_OK)
@@ -546,6 +558,16 @@ int moe_decoder_step(moe_decoder_t* d, int step, int layer, const void* x, int T
     if (rc != MOE_OK) return dfail(rc, "moe_decoder_step: %s", moe_last_error());
   }
   if (n_miss) *n_miss = nm;
+  return MOE_OK;
+}
+
+int moe_decoder_set_gate(moe_decoder_t* d, const moe_gate_t* gate) {
+  if (!d) return dfail(MOE_EINVAL, "moe_decoder_set_gate: null decoder");
+  if (gate) {
+    const int rc = moe::gate_args("moe_decoder_set_gate", gate, d->E, d->k, &d->gate);
+    if (rc != MOE_OK) return rc;
+  }
+  d->has_gate = gate != nullptr;
   return MOE_OK;
 }
 

@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/moe.h"
+#include "int8_layout.hpp"
 #include "lru_policy.hpp"
 #include "moe_kernels.hpp"
 
@@ -35,6 +36,8 @@ struct moe_device_decoder {
   moe::DevCache c{};
   int max_items;
   uint64_t* ffn_flags = nullptr;  // hand-off flags of the one-launch FFN (zeroed at creation)
+  moe::GateArgs gate{};           // with has_gate: the choice and weights of every step's routing
+  bool has_gate = false;
 };
 
 namespace {
@@ -109,6 +112,9 @@ moe_device_decoder_t* moe_device_decoder_create(int L, int E, int S, int T_max, 
   if ((wfmt == MOE_W_F32) != (dtype == MOE_DT_F32)) return bad(MOE_EINVAL, "activation dtype does not match weights");
   const size_t blob = moe_expert_bytes(wfmt, H, I);
   if (blob == 0) return bad(MOE_EINVAL, "unsupported weight format or shape");
+  if (wfmt == MOE_W_INT8 && (!moe::aligned16(slot_base, buffers->y_perm, buffers->ffn_ws) || slot_stride % 16 != 0 ||
+                             !moe::int8_rows_ok((size_t)T_max * k, (size_t)T_max * k, H, I)))
+    return bad(MOE_EINVAL, "int8 experts need 16-byte aligned buffers and slots, and codes within 32-bit offsets");
   if (blob % 16 != 0) return bad(MOE_EINVAL, "expert blob size not a multiple of 16 bytes");
   if (blob_stride < blob || slot_stride < blob) return bad(MOE_EINVAL, "stride smaller than an expert blob");
   const moe_decoder_buffers_t& b = *buffers;
@@ -188,13 +194,16 @@ int moe_device_decoder_step(moe_device_decoder_t* d, int layer, const void* x, i
   const moe::DevStep dstep{d->c, layer};
   hipError_t e = moe::launch_route(x, d->dtype == MOE_DT_BF16, Wr, bias, T, d->H, d->E, d->k, b.topk_idx, b.topk_w,
                                    b.logits, b.counts, b.offsets, b.perm_src, b.perm_pos, b.route_ws, s, nullptr, 0,
-                                   nullptr, fused_resolve ? &dstep : nullptr);
+                                   nullptr, fused_resolve ? &dstep : nullptr, d->has_gate ? &d->gate : nullptr);
   if (e == hipSuccess && !fused_resolve) e = moe::launch_dev_resolve(b.counts, b.offsets, d->E, layer, d->c, s);
-  if (d->wfmt == MOE_W_F32) {
-    // fp32 experts: the misses are copied first, then every item runs from its slot
+  if (d->wfmt == MOE_W_F32 || d->wfmt == MOE_W_INT8) {
+    // fp32 and int8 experts: the misses are copied first, then every item runs from its slot
     if (e == hipSuccess)
       e = moe::launch_dev_fill(d->c, d->pool[layer], d->blob_stride, d->blob_bytes, d->slot_base, d->slot_stride, s);
-    if (e == hipSuccess)
+    if (e == hipSuccess && d->wfmt == MOE_W_INT8)
+      e = moe::launch_ffn_int8_dev(x, T, b.perm_src, d->c.n, d->c.work, items, d->Tmax * d->k, d->slot_base,
+                                   d->slot_stride, d->H, d->I, b.y_perm, b.ffn_ws, s);
+    else if (e == hipSuccess)
       e = moe::launch_ffn_decode_dev(d->wfmt, x, b.perm_src, d->c.n, d->c.work, items, T, d->slot_base,
                                      d->slot_stride, d->H, d->I, hbuf, b.y_perm, s);
   } else if (e == hipSuccess && fused_combine) {
@@ -216,6 +225,16 @@ int moe_device_decoder_step(moe_device_decoder_t* d, int layer, const void* x, i
   if (e == hipSuccess && !fused_combine)
     e = moe::launch_combine(b.y_perm, b.perm_pos, b.topk_w, T, d->k, d->H, out, out_dtype == MOE_DT_BF16, s);
   if (e != hipSuccess) return dd_fail(MOE_EHIP, "moe_device_decoder_step: %s", hipGetErrorString(e));
+  return MOE_OK;
+}
+
+int moe_device_decoder_set_gate(moe_device_decoder_t* d, const moe_gate_t* gate) {
+  if (!d) return dd_fail(MOE_EINVAL, "moe_device_decoder_set_gate: null decoder");
+  if (gate) {
+    const int rc = moe::gate_args("moe_device_decoder_set_gate", gate, d->E, d->k, &d->gate);
+    if (rc != MOE_OK) return rc;
+  }
+  d->has_gate = gate != nullptr;
   return MOE_OK;
 }
 

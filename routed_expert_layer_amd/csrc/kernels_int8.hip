@@ -1,0 +1,874 @@
+// Experts in 8-bit integers, a scale per token on one side and per output
+// channel on the other (MOE_W_INT8).
+//
+//   sx = max|x| / 127 over a token,  xq = rne(127 x / max|x|)
+//   g = (xq W1) sx s1,  u = (xq W3) sx s3,  h = silu(g) u
+//   sh, hq = the same of a row of h,  y = (hq W2) sh s2
+//
+// The integer products run on v_mfma_i32_16x16x64_i8 and are exact (32-bit
+// sums: |sum| <= 127^2 K, so K may reach 133000). A 16 x 64 operand fragment
+// is 1 KiB, as a 16 x 32 fragment in bf16 is, so the blobs, the streaming of
+// weights in decode steps and the staging of prefill tiles have the same byte
+// geometry as the bf16 experts at half the K.
+//
+// A row's scale needs the whole row of h, which no tile of the gate/up product
+// holds: h goes to memory in fp32 (a rounding to 16 bits here would move one
+// code in some hundreds by a step, more than all other roundings together)
+// and the down projection's side turns it into codes: decode blocks for
+// themselves, prefill in a pass of its own between the products.
+#include <algorithm>
+#include <cstring>
+
+#include "dev_common.hpp"
+#include "gemm_common.hpp"
+#include "int8_layout.hpp"
+#include "moe_kernels.hpp"
+
+namespace moe {
+namespace {
+
+using i32x4_t = int32_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ i32x4_t mfma_i8(u32x4_t a, u32x4_t b, i32x4_t c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0,
+                                               0);
+}
+
+// ---------------------------------------------------------------------------
+// Codes of a row.
+// ---------------------------------------------------------------------------
+// What a row's codes are formed with, from the largest magnitude (as bits, so
+// that infinities and NaN compare above every finite value).
+struct RowQuant {
+  float amax, up, inv;  // up: a power of two that keeps 127 / amax finite; inv = 127 / (amax up)
+  bool finite;
+  __device__ __forceinline__ explicit RowQuant(uint32_t amax_bits) {
+    finite = amax_bits < 0x7F800000u;
+    amax = __uint_as_float(amax_bits);
+    up = amax < 0x1p-100f ? 0x1p+100f : 1.f;
+    inv = (finite && amax > 0.f) ? 127.f / (amax * up) : 0.f;
+  }
+  // The scale: NaN for a row with an infinity or NaN (its products are then NaN), 0 for a row of zeros.
+  __device__ __forceinline__ float scale() const { return finite ? amax / 127.f : __uint_as_float(0x7FC00000u); }
+  // rne(127 v / amax). The fp32 quotient is off by less than 1e-4; where it is that near to a half, the exact side
+  // is taken from 127 v - (n + 1/2) amax, which 64 bits hold exactly (halves are common: v = amax / 2 gives 63.5).
+  __device__ __forceinline__ int code(float v) const {
+    const float t = (v * up) * inv;
+    float n = rintf(t);
+    if (__builtin_expect(fabsf(t - n) > 0.4999f, 0)) {
+      const float lo = floorf(t);
+      const double d = (double)v * 127.0 - ((double)lo + 0.5) * (double)amax;
+      n = d > 0.0 ? lo + 1.f : (d < 0.0 ? lo : 2.f * rintf(0.5f * (lo + 0.5f)));
+    }
+    return finite ? (int)n : 0;
+  }
+  __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) const {
+    return (uint32_t)(code(a) & 0xFF) | ((uint32_t)(code(b) & 0xFF) << 8) | ((uint32_t)(code(c) & 0xFF) << 16) |
+           ((uint32_t)code(d) << 24);
+  }
+};
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t o = __shfl_xor(v, d, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// One wave: the codes and the scale of a row of K bf16 values (K a multiple
+// of 16). NC: 16-value pieces a lane keeps in registers (K <= 1024 NC).
+template <int NC>
+__device__ __forceinline__ void quantise_row(const uint16_t* __restrict__ row, int K, uint8_t* __restrict__ codes,
+                                             float* __restrict__ scale, int lane) {
+  const int pieces = K / 16;
+  u32x4_t raw[NC][2];
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int p = lane + 64 * c;
+    raw[c][0] = raw[c][1] = u32x4_t{0u, 0u, 0u, 0u};
+    if (p < pieces) {
+      raw[c][0] = ld16(row + (size_t)p * 16);
+      raw[c][1] = ld16(row + (size_t)p * 16 + 8);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t lo = (raw[c][q][w] << 16) & 0x7FFFFFFFu, hi = raw[c][q][w] & 0x7FFF0000u;
+        m = lo > m ? lo : m;
+        m = hi > m ? hi : m;
+      }
+  const RowQuant rq(wave_max_u32(m));
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int p = lane + 64 * c;
+    if (p < pieces) {
+      u32x4_t o;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a = raw[c][w >> 1][2 * (w & 1)], b = raw[c][w >> 1][2 * (w & 1) + 1];
+        o[w] = rq.pack4(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
+                        __uint_as_float(b & 0xFFFF0000u));
+      }
+      *reinterpret_cast<u32x4_t*>(codes + (size_t)p * 16) = o;
+    }
+  }
+  if (lane == 0) *scale = rq.scale();
+}
+
+// Where a launch finds its work items {slot, row_begin, rows, expert}: in the kernel arguments or in device memory
+// (*n of them, the grid sized for the most there can be).
+struct ArgItems {
+  WorkArgs wa;
+  __device__ __forceinline__ bool get(int i, int4& it) const {
+    it = wa.item[i];
+    return true;
+  }
+};
+struct DevItems {
+  const int32_t* n;
+  const int4* items;
+  __device__ __forceinline__ bool get(int i, int4& it) const {
+    if (i >= *n) return false;
+    const int4 v = items[i];
+    it = make_int4(__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y),
+                   __builtin_amdgcn_readfirstlane(v.z), __builtin_amdgcn_readfirstlane(v.w));
+    return true;
+  }
+};
+
+// The experts with rows as work items, in ascending order, by one block of
+// 256 threads: what the decode kernels of a layer run over. Groups that reach
+// past rows_max and experts without a slot are left out.
+struct ItemPlan {
+  const int32_t *counts, *offsets, *slot_of;
+  int E, n_slots, rows_max;
+  int32_t* n;
+  int4* items;
+};
+
+__device__ __forceinline__ void plan_items(const ItemPlan& p) {
+  __shared__ int wsum[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int base = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 256) {
+    const int e = e0 + tid;
+    int4 it = make_int4(0, 0, 0, e);
+    bool ok = false;
+    if (e < p.E) {
+      it.z = p.counts[e];
+      it.y = p.offsets[e];
+      it.x = p.slot_of ? p.slot_of[e] : e;
+      ok = it.z > 0 && it.y >= 0 && (long long)it.y + it.z <= p.rows_max && it.x >= 0 && it.x < p.n_slots;
+    }
+    const uint64_t m = __ballot(ok);
+    if (lane == 0) wsum[wave] = __popcll(m);
+    __syncthreads();
+    int before = base, all = 0;
+    for (int w = 0; w < 4; ++w) {
+      before += w < wave ? wsum[w] : 0;
+      all += wsum[w];
+    }
+    if (ok) p.items[before + __popcll(m & ((1ull << lane) - 1ull))] = it;
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) *p.n = base;
+}
+
+// T token rows to codes, four rows a block (one a wave); with a plan, block 0
+// plans the layer's work items instead. Bound by memory: 2 bytes in, 1 out.
+template <int NC>
+__global__ __launch_bounds__(256) void quantise_tokens(const uint16_t* __restrict__ x, int T, int H,
+                                                       uint8_t* __restrict__ xq, float* __restrict__ sx,
+                                                       const ItemPlan plan) {
+  int block = blockIdx.x;
+  if (plan.n != nullptr) {
+    if (block == 0) {
+      plan_items(plan);
+      return;
+    }
+    --block;
+  }
+  const int r = block * 4 + (threadIdx.x >> 6);
+  if (r < T) quantise_row<NC>(x + (size_t)r * H, H, xq + (size_t)r * H, sx + r, threadIdx.x & 63);
+}
+
+// The rows of listed work items through perm_src: grouped row r of xq and sx.
+template <int NC>
+__global__ __launch_bounds__(256) void quantise_items(const uint16_t* __restrict__ x,
+                                                      const int32_t* __restrict__ perm_src, const ArgItems wk, int H,
+                                                      uint8_t* __restrict__ xq, float* __restrict__ sx) {
+  int4 it;
+  if (!wk.get(blockIdx.y, it)) return;
+  const int m = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (m >= it.z) return;
+  const size_t r = (size_t)(it.y + m);
+  quantise_row<NC>(x + (size_t)perm_src[r] * H, H, xq + r * H, sx + r, threadIdx.x & 63);
+}
+
+// ---------------------------------------------------------------------------
+// Packing: fragment order as in the bf16 blobs, 16 K bytes a lane.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void pack_int8_kernel(const int8_t* __restrict__ Q1, const int8_t* __restrict__ Q3,
+                                                        const int8_t* __restrict__ Q2, const float* __restrict__ S1,
+                                                        const float* __restrict__ S3, const float* __restrict__ S2,
+                                                        int H, int I, char* __restrict__ blob, const Int8Layout L) {
+  const size_t q = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const int KC1 = H / 64, KC2 = I / 64;
+  const size_t c1 = (size_t)(2 * I / 16) * KC1 * 64, c2 = (size_t)(H / 16) * KC2 * 64;
+  union {
+    int8_t b[16];
+    uint4 v;
+  } o;
+  if (q < c1) {
+    const int l = (int)(q % 64), c = (int)((q / 64) % KC1), t = (int)(q / (64 * (size_t)KC1));
+    int mat, i;
+    p1_row_source(16 * t + (l % 16), mat, i);
+    const int8_t* Q = mat ? Q3 : Q1;
+    const int k0 = 64 * c + 16 * (l / 16);
+    for (int j = 0; j < 16; ++j) o.b[j] = Q[(size_t)(k0 + j) * I + i];
+    *reinterpret_cast<uint4*>(blob + L.p1 + q * 16) = o.v;
+    return;
+  }
+  size_t r = q - c1;
+  if (r < c2) {
+    const int l = (int)(r % 64), c = (int)((r / 64) % KC2), t = (int)(r / (64 * (size_t)KC2));
+    const int n = 16 * t + (l % 16);
+    for (int j = 0; j < 16; ++j) o.b[j] = Q2[(size_t)int8_k2_source(c, l / 16, j) * H + n];
+    *reinterpret_cast<uint4*>(blob + L.p2 + r * 16) = o.v;
+    return;
+  }
+  r -= c2;
+  if (r < (size_t)2 * I) {
+    int mat, i;
+    p1_row_source((int)r, mat, i);
+    reinterpret_cast<float*>(blob + L.p1s)[r] = mat ? S3[i] : S1[i];
+    return;
+  }
+  r -= (size_t)2 * I;
+  if (r < (size_t)H) reinterpret_cast<float*>(blob + L.p2s)[r] = S2[r];
+}
+
+// ---------------------------------------------------------------------------
+// Decode: every weight byte is read once, straight from memory into matrix
+// instructions whose other operand holds up to 16 tokens' codes.
+// ---------------------------------------------------------------------------
+constexpr int kU8 = 8;  // weight fragments in flight a wave
+
+// A wave's sum over fragments [c0, c1) of a 16-row tile (1 KiB apart from wp) times the token fragments bload(c).
+template <typename BLoad>
+__device__ __forceinline__ i32x4_t int8_wave_dot(const char* wp, int c0, int c1, BLoad bload) {
+  i32x4_t acc = {0, 0, 0, 0};
+  int c = c0;
+  for (; c + kU8 <= c1; c += kU8) {
+    u32x4_t a[kU8], b[kU8];
+#pragma unroll
+    for (int u = 0; u < kU8; ++u) {
+      a[u] = ld16_nt(wp + (size_t)(c + u) * 1024);
+      b[u] = bload(c + u);
+    }
+#pragma unroll
+    for (int u = 0; u < kU8; ++u) acc = mfma_i8(a[u], b[u], acc);
+  }
+  const int n = c1 - c;
+  if (n > 0) {  // the last ones as one batch: slots past the end repeat the last fragment against zeros
+    u32x4_t a[kU8], b[kU8];
+#pragma unroll
+    for (int u = 0; u < kU8; ++u) {
+      const int cu = c + (u < n ? u : n - 1);
+      a[u] = ld16_nt(wp + (size_t)cu * 1024);
+      b[u] = bload(cu);
+      if (u >= n) b[u] = u32x4_t{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int u = 0; u < kU8; ++u) acc = mfma_i8(a[u], b[u], acc);
+  }
+  return acc;
+}
+
+// Gate/up: a block is one 16-row tile of P1 (8 gate and 8 up columns) of an
+// item, its four waves splitting K. src: the token of each grouped row
+// (nullptr: xq holds the grouped rows). h: fp32, row-major.
+template <typename W>
+__global__ __launch_bounds__(256) void int8_decode_up(const uint8_t* __restrict__ xq, const float* __restrict__ sx,
+                                                      const int32_t* __restrict__ src, const W wk,
+                                                      const char* __restrict__ slot_base, size_t slot_stride,
+                                                      const Int8Layout L, int H, int I, float* __restrict__ h) {
+  const int NT = I / 8;
+  const int item = blockIdx.x / NT, tile = blockIdx.x - item * NT;
+  int4 it;
+  if (!wk.get(item, it)) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int KC = H / 64, c0 = (KC * wave) >> 2, c1 = (KC * (wave + 1)) >> 2;
+  const char* blob = slot_base + (size_t)it.x * slot_stride;
+  const char* wp = blob + L.p1 + (size_t)tile * KC * 1024 + lane * 16;
+  __shared__ i32x4_t red[4][64];
+  for (int m0 = 0; m0 < it.z; m0 += 16) {
+    const int m = m0 + (lane & 15);
+    const bool valid = m < it.z;
+    // lanes past the group read its first row again: their columns are not stored
+    const int r = it.y + (valid ? m : 0), t = src ? src[r] : r;
+    const uint8_t* xr = xq + (size_t)t * H + 16 * (lane >> 4);
+    red[wave][lane] = int8_wave_dot(wp, c0, c1, [&](int c) { return ld16(xr + (size_t)c * 64); });
+    __syncthreads();
+    if (wave == 0 && valid) {
+      const i32x4_t s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
+      const f32x4_t sw = *reinterpret_cast<const f32x4_t*>(blob + L.p1s + (size_t)(16 * tile + 4 * (lane >> 4)) * 4);
+      const float st = sx[t];
+      const float g0 = (float)s[0] * (st * sw[0]), u0 = (float)s[1] * (st * sw[1]);
+      const float g1 = (float)s[2] * (st * sw[2]), u1 = (float)s[3] * (st * sw[3]);
+      *reinterpret_cast<float2*>(h + (size_t)r * I + 8 * tile + 2 * (lane >> 4)) =
+          make_float2(silu(g0) * u0, silu(g1) * u1);
+    }
+    __syncthreads();
+  }
+}
+
+// The codes of rows [r0, r0 + n) of h (n <= 16), by a block's waves, into LDS
+// in the order of P2's K (int8_k2_source): fragment c at 1024 c, lane
+// (column group, row) at 16 bytes each. Rows past n are zeroed.
+__device__ __forceinline__ void quantise_h_rows(const float* __restrict__ h, int r0, int n, int I, char* lds,
+                                                float* scales) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  for (int m = wave; m < 16; m += waves) {
+    if (m >= n) {
+      for (int c = lane; c < I / 16; c += 64)
+        *reinterpret_cast<u32x4_t*>(lds + (c >> 2) * 1024 + ((c & 3) * 16 + m) * 16) = u32x4_t{0u, 0u, 0u, 0u};
+      continue;
+    }
+    const float* row = h + (size_t)(r0 + m) * I;
+    uint32_t mx = 0;
+    for (int i = 4 * lane; i < I; i += 256) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + i);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mx = max(mx, abs_bits(v[w]));
+    }
+    const RowQuant rq(wave_max_u32(mx));
+    for (int i = 4 * lane; i < I; i += 256) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + i);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {  // columns i + 2p, i + 2p + 1: one column group, neighbouring bytes
+        const int col = i + 2 * p;
+        char* at = lds + (col >> 6) * 1024 + (((col >> 1) & 3) * 16 + m) * 16 + 2 * ((col >> 3) & 7);
+        *reinterpret_cast<uint16_t*>(at) =
+            (uint16_t)((rq.code(v[2 * p]) & 0xFF) | ((rq.code(v[2 * p + 1]) & 0xFF) << 8));
+      }
+    }
+    if (lane == 0) scales[m] = rq.scale();
+  }
+}
+
+// Down projection: a block is one 16-row tile of P2 (16 output columns) of an
+// item; it forms the codes of the item's rows of h itself.
+template <typename W>
+__global__ __launch_bounds__(256) void int8_decode_down(const float* __restrict__ h, const W wk,
+                                                        const char* __restrict__ slot_base, size_t slot_stride,
+                                                        const Int8Layout L, int H, int I, float* __restrict__ y) {
+  const int NT = H / 16;
+  const int item = blockIdx.x / NT, tile = blockIdx.x - item * NT;
+  int4 it;
+  if (!wk.get(item, it)) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int KC = I / 64, c0 = (KC * wave) >> 2, c1 = (KC * (wave + 1)) >> 2;
+  const char* blob = slot_base + (size_t)it.x * slot_stride;
+  const char* wp = blob + L.p2 + (size_t)tile * KC * 1024 + lane * 16;
+  extern __shared__ __attribute__((aligned(16))) char codes[];  // 16 rows of I bytes
+  __shared__ i32x4_t red[4][64];
+  __shared__ float sh[16];
+  for (int m0 = 0; m0 < it.z; m0 += 16) {
+    quantise_h_rows(h, it.y + m0, min(16, it.z - m0), I, codes, sh);
+    __syncthreads();
+    red[wave][lane] = int8_wave_dot(wp, c0, c1, [&](int c) { return ld16(codes + (size_t)c * 1024 + lane * 16); });
+    __syncthreads();
+    const int m = m0 + (lane & 15);
+    if (wave == 0 && m < it.z) {
+      const i32x4_t s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
+      const int n0 = 16 * tile + 4 * (lane >> 4);
+      const f32x4_t sw = *reinterpret_cast<const f32x4_t*>(blob + L.p2s + (size_t)n0 * 4);
+      const float st = sh[lane & 15];
+      f32x4_t o;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) o[w] = (float)s[w] * (st * sw[w]);
+      *reinterpret_cast<f32x4_t*>(y + (size_t)(it.y + m) * H + n0) = o;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Prefill: grouped GEMM, 256 weight rows x 128 or 256 tokens a block and 64 of
+// K a stage, both operands straight into LDS in fragment order; eight waves of
+// 64 x 64 (128 tokens) or 128 x 64.
+// ---------------------------------------------------------------------------
+// h of prefill: 16-row tiles, 8 columns a piece, the two columns of a lane
+// together: the gate/up product's store of a fragment is 512 contiguous bytes
+// and lane (q, row) of the pass below reads what it wrote.
+__device__ __forceinline__ size_t h_tile_at(size_t row, int piece, int q, int I) {
+  return ((row >> 4) * (size_t)(I / 8) + piece) * 128 + (q * 16 + (row & 15)) * 2;
+}
+
+template <int PHASE, int BM_T>
+__device__ __forceinline__ void int8_tile(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
+                                          const int32_t* __restrict__ src, const GemmTable* __restrict__ tab,
+                                          const char* __restrict__ slot_base, size_t slot_stride, size_t mat_off,
+                                          size_t scale_off, int N, int K, int H, int I, float* __restrict__ hout,
+                                          float* __restrict__ yout, const int sidx, const int w) {
+  constexpr int BN_T = 16;
+  constexpr int NS = BM_T == 16 ? 4 : 6;
+  constexpr int WN = BM_T == 16 ? 8 : 4;
+  constexpr int WM = 4;
+  constexpr int WAVES_N = BN_T / WN;
+  static_assert(WAVES_N * (BM_T / WM) == 8, "wave grid");
+  constexpr int FA = BN_T, FB = BM_T;
+  constexpr int FPW = (FA + FB) / 8;
+  constexpr int STAGE = (FA + FB) * 1024;
+  __shared__ __attribute__((aligned(1024))) char lds[NS][STAGE];
+
+  const int NTB = N / (16 * BN_T);
+  int lo = 0, hi = tab->n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tab->tile_prefix[mid] <= sidx) lo = mid; else hi = mid - 1;
+  }
+  const int4 it = tab->item[lo];
+  const int GM = it.w & 0xFF, GN = it.w >> 8;
+  if (w >= GM * GN) return;
+  const int ls = sidx - tab->tile_prefix[lo];
+  const int ngroups = NTB / GN;
+  const int mt = (ls / ngroups) * GM + w / GN;
+  const int nt = (ls % ngroups) * GN + (w % GN);
+  if (mt * 16 * BM_T >= it.z) return;
+  // the thread index passes through an empty asm so that nothing derived from it stays live over the loop of tiles
+  int tid = (int)threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int wave = tid >> 6, lane = tid & 63;
+  const int wn = wave % WAVES_N, wm = wave / WAVES_N;
+  const int KC = K / 64;
+  const char* blob = slot_base + (size_t)it.x * slot_stride;
+  const char* wbase = blob + mat_off;
+
+  constexpr int QW = FA / 8;  // weight fragments a wave loads per stage; the others are token fragments
+  uint32_t off[FPW], kstep[FPW];
+#pragma unroll
+  for (int q = 0; q < FPW; ++q) {
+    const int f = wave + 8 * q;
+    if (q < QW) {
+      off[q] = (uint32_t)((nt * BN_T + f) * KC) * 1024u + lane * 16;
+      kstep[q] = 1024;
+    } else {
+      int mloc = mt * (16 * BM_T) + (f - FA) * 16 + (lane & 15);
+      if (mloc >= it.z) mloc = it.z - 1;  // a valid row; its columns are not stored
+      if constexpr (PHASE == 2) {
+        const uint32_t row = (uint32_t)(it.y + mloc);
+        off[q] = (row >> 4) * (uint32_t)KC * 1024u + ((row & 15) + 16 * (lane >> 4)) * 16;
+        kstep[q] = 1024;
+      } else {
+        const uint32_t row = (uint32_t)(src ? src[it.y + mloc] : it.y + mloc);
+        off[q] = row * (uint32_t)H + (lane >> 4) * 16;
+        kstep[q] = 64;
+      }
+    }
+  }
+  auto issue = [&](int stage, int buf) {
+    char* base = lds[buf];
+#pragma unroll
+    for (int q = 0; q < FPW; ++q)
+      buffer_load_lds16(q < QW ? static_cast<const void*>(wbase) : static_cast<const void*>(bsrc),
+                        off[q] + (uint32_t)stage * kstep[q], base + (wave + 8 * q) * 1024);
+  };
+
+  i32x4_t acc[WN][WM];
+#pragma unroll
+  for (int i = 0; i < WN; ++i)
+#pragma unroll
+    for (int j = 0; j < WM; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  struct Frags {
+    u32x4_t a[WN], b[WM];
+  };
+  // JM: this wave's token fragments that hold rows of the group
+  auto k_loop = [&](auto jm_const) {
+    constexpr int JM = decltype(jm_const)::value;
+    auto read_stage = [&](int kt, Frags& f) {
+      const char* b = lds[kt % NS];
+#pragma unroll
+      for (int j = 0; j < JM; ++j) f.b[j] = ld16(b + (FA + wm * WM + j) * 1024 + lane * 16);
+      if constexpr (JM > 0) {
+#pragma unroll
+        for (int i = 0; i < WN; ++i) f.a[i] = ld16(b + (wn * WN + i) * 1024 + lane * 16);
+      }
+    };
+    auto compute = [&](const Frags& f) {
+#pragma unroll
+      for (int i = 0; i < WN; ++i)
+#pragma unroll
+        for (int j = 0; j < JM; ++j) acc[i][j] = mfma_i8(f.a[i], f.b[j], acc[i][j]);
+    };
+    // step kt computes on stage kt's registers while it reads stage kt + 1's fragments; after its barrier every
+    // wave has finished reading stage kt, whose buffer is then refilled with stage kt + NS
+    auto step = [&](int kt, Frags& cur, Frags& nxt) {
+      if (kt + NS - 1 < KC) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(FPW * (NS - 2)));
+      } else {
+        __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+      }
+      __builtin_amdgcn_s_waitcnt(lgkmcnt_only(0));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (kt + NS < KC) issue(kt + NS, kt % NS);
+      read_stage(min(kt + 1, KC - 1), nxt);
+      compute(cur);
+      if constexpr (JM > 0) {
+#pragma unroll
+        for (int q = 0; q < WN + JM; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, (WN * JM) / (WN + JM), 0);
+        }
+      }
+    };
+    for (int s0 = 0; s0 < NS && s0 < KC; ++s0) issue(s0, s0);
+    if (KC >= NS) {
+      __builtin_amdgcn_s_waitcnt(vmcnt_only(FPW * (NS - 1)));
+    } else {
+      __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    Frags f0, f1;
+    read_stage(0, f0);
+    int kt = 0;
+    for (; kt + 1 < KC; kt += 2) {
+      step(kt, f0, f1);
+      step(kt + 1, f1, f0);
+    }
+    if (kt < KC) step(kt, f0, f1);
+  };
+  static_assert(WM == 4, "the dispatch below covers 0 .. 4 fragments");
+  const int rows_here = it.z - (mt * 16 * BM_T + wm * WM * 16);
+  const int jm = rows_here <= 0 ? 0 : min(WM, (rows_here + 15) / 16);
+  switch (jm) {
+    case 0: k_loop(std::integral_constant<int, 0>{}); break;
+    case 1: k_loop(std::integral_constant<int, 1>{}); break;
+    case 2: k_loop(std::integral_constant<int, 2>{}); break;
+    case 3: k_loop(std::integral_constant<int, 3>{}); break;
+    default: k_loop(std::integral_constant<int, 4>{}); break;
+  }
+
+  const float* wscale = reinterpret_cast<const float*>(blob + scale_off);
+#pragma unroll
+  for (int j = 0; j < WM; ++j) {
+    const int mloc = mt * (16 * BM_T) + (wm * WM + j) * 16 + (lane & 15);
+    if (mloc >= it.z) continue;
+    const size_t row = (size_t)(it.y + mloc);
+    const float st = bscale[(PHASE == 1 && src) ? (size_t)src[row] : row];
+#pragma unroll
+    for (int i = 0; i < WN; ++i) {
+      const int ntile = nt * BN_T + wn * WN + i;
+      const i32x4_t s = acc[i][j];
+      const f32x4_t sw = *reinterpret_cast<const f32x4_t*>(wscale + 16 * ntile + 4 * (lane >> 4));
+      f32x4_t v;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = (float)s[c] * (st * sw[c]);
+      if constexpr (PHASE == 1)
+        *reinterpret_cast<float2*>(hout + h_tile_at(row, ntile, lane >> 4, I)) =
+            make_float2(silu(v[0]) * v[1], silu(v[2]) * v[3]);
+      else
+        *reinterpret_cast<f32x4_t*>(yout + row * H + 16 * ntile + 4 * (lane >> 4)) = v;
+    }
+  }
+}
+
+// Rounds of super-tiles as in the bf16 GEMM: block b works on super-tiles (b / 256) * 8 + b % 8, then that plus
+// 8 * (grid / 256), and so on, in slot (b / 8) % 32 of each. Every exit is uniform per block.
+template <int PHASE, int BM_T>
+__global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
+                                                    const int32_t* __restrict__ src,
+                                                    const GemmTable* __restrict__ tab,
+                                                    const char* __restrict__ slot_base, size_t slot_stride,
+                                                    size_t mat_off, size_t scale_off, int N, int K, int H, int I,
+                                                    float* __restrict__ hout, float* __restrict__ yout) {
+  const int first = (int)(blockIdx.x >> 8), rounds = (int)(gridDim.x >> 8);
+  const int total = tab->total_tiles;
+  for (int r = first;; r += rounds) {
+    const int sidx = r * 8 + (int)(blockIdx.x & 7);
+    if (sidx >= total) break;
+    if (r != first) __syncthreads();
+    int8_tile<PHASE, BM_T>(bsrc, bscale, src, tab, slot_base, slot_stride, mat_off, scale_off, N, K, H, I, hout, yout,
+                           sidx, (int)((blockIdx.x >> 3) & 31));
+  }
+}
+
+// h to codes between the products: a block is one 16-row tile; lane (q, row)
+// of a wave reads its two columns of each of a 64-wide piece's eight 8-wide
+// parts and has the 16 code bytes of its place in the token fragment (the
+// order P2 is packed in, int8_k2_source). Up to kHeld pieces a wave stay in
+// registers between the row maximum and the codes; wider rows are read again.
+constexpr int kHeld = 4, kReqWaves = 8;
+__global__ __launch_bounds__(64 * kReqWaves) void requantise_h(const float* __restrict__ h, int I,
+                                                               uint8_t* __restrict__ hq, float* __restrict__ sh) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const size_t tile = blockIdx.x;
+  const int pieces = I / 64;
+  const float* base = h + tile * 16 * (size_t)I + lane * 2;
+  __shared__ uint32_t mx[kReqWaves][16];
+  float2 v[kHeld][8];
+  uint32_t m = 0;
+  auto load = [&](int c, float2 (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = *reinterpret_cast<const float2*>(base + (size_t)(8 * c + j) * 128);
+  };
+  auto take = [&](const float2 (&o)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, max(abs_bits(o[j].x), abs_bits(o[j].y)));
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (wave + kReqWaves * u < pieces) {
+      load(wave + kReqWaves * u, v[u]);
+      take(v[u]);
+    }
+  for (int c = wave + kReqWaves * kHeld; c < pieces; c += kReqWaves) {
+    float2 o[8];
+    load(c, o);
+    take(o);
+  }
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+  if (lane < 16) mx[wave][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kReqWaves; ++w) m = max(m, mx[w][lane & 15]);
+  const RowQuant rq(m);
+  auto store = [&](int c, const float2 (&o)[8]) {
+    u32x4_t b;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) b[w] = rq.pack4(o[2 * w].x, o[2 * w].y, o[2 * w + 1].x, o[2 * w + 1].y);
+    *reinterpret_cast<u32x4_t*>(hq + (tile * pieces + c) * 1024 + lane * 16) = b;
+  };
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    if (wave + kReqWaves * u < pieces) store(wave + kReqWaves * u, v[u]);
+  for (int c = wave + kReqWaves * kHeld; c < pieces; c += kReqWaves) {
+    float2 o[8];
+    load(c, o);
+    store(c, o);
+  }
+  if (wave == 0 && lane < 16) sh[tile * 16 + lane] = rq.scale();
+}
+
+// out[t] = sum over j of w[t, j] y[pos[t, j]], j ascending, over the experts that have a slot.
+template <bool OUT_BF16>
+__global__ __launch_bounds__(256) void int8_combine(const float* __restrict__ y, const int32_t* __restrict__ perm_pos,
+                                                    const int32_t* __restrict__ topk_idx,
+                                                    const float* __restrict__ topk_w,
+                                                    const int32_t* __restrict__ slot_of, int n_slots, int k, int H,
+                                                    void* __restrict__ out) {
+  const size_t t = blockIdx.x;
+  const int n = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (n >= H) return;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < k; ++j) {
+    const int e = topk_idx[t * k + j];
+    const int slot = slot_of ? slot_of[e] : e;
+    if (slot < 0 || slot >= n_slots) continue;
+    const float wj = topk_w[t * k + j];
+    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(y + (size_t)perm_pos[t * k + j] * H + n);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = fmaf(wj, v[c], acc[c]);
+  }
+  if constexpr (OUT_BF16) {
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + t * H + n) =
+        make_uint2((uint32_t)f32_to_bf16(acc[0]) | ((uint32_t)f32_to_bf16(acc[1]) << 16),
+                   (uint32_t)f32_to_bf16(acc[2]) | ((uint32_t)f32_to_bf16(acc[3]) << 16));
+  } else {
+    *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + t * H + n) = acc;
+  }
+}
+
+// Workgroup rounds of a grouped launch, as for the bf16 GEMM (see launch_ffn_grouped).
+dim3 gemm_grid(int N, int gm_min) {
+  int shape = 0;
+  supertiles_of(gm_min * 128, N, 128, shape);
+  const int fill = (shape & 0xFF) * (shape >> 8);
+  return dim3(256 * 8 * (fill >= 32 ? 1 : 32 / fill));
+}
+
+hipError_t launch_quantise_tokens(const uint16_t* x, int T, int H, uint8_t* xq, float* sx, const ItemPlan& plan,
+                                  hipStream_t s) {
+  const dim3 grid((T + 3) / 4 + (plan.n != nullptr ? 1 : 0));
+  if (H <= 1024) hipLaunchKernelGGL(quantise_tokens<1>, grid, dim3(256), 0, s, x, T, H, xq, sx, plan);
+  else if (H <= 2048) hipLaunchKernelGGL(quantise_tokens<2>, grid, dim3(256), 0, s, x, T, H, xq, sx, plan);
+  else if (H <= 4096) hipLaunchKernelGGL(quantise_tokens<4>, grid, dim3(256), 0, s, x, T, H, xq, sx, plan);
+  else if (H <= 8192) hipLaunchKernelGGL(quantise_tokens<8>, grid, dim3(256), 0, s, x, T, H, xq, sx, plan);
+  else hipLaunchKernelGGL(quantise_tokens<16>, grid, dim3(256), 0, s, x, T, H, xq, sx, plan);
+  return hipGetLastError();
+}
+
+template <typename W>
+hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const float* sx, const int32_t* src,
+                           const char* slot_base, size_t slot_stride, int H, int I, float* h, float* y,
+                           hipStream_t s) {
+  const Int8Layout L = int8_layout(H, I);
+  hipLaunchKernelGGL(int8_decode_up<W>, dim3(n_items * (I / 8)), dim3(256), 0, s, xq, sx, src, wk, slot_base,
+                     slot_stride, L, H, I, h);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(int8_decode_down<W>, dim3(n_items * (H / 16)), dim3(256), (size_t)16 * I, s, h, wk, slot_base,
+                     slot_stride, L, H, I, y);
+  return hipGetLastError();
+}
+
+// The two products and the pass between them over tables the planners wrote; launch shapes for a host plan (tot:
+// super-tiles of each part and projection) or, with tot null, for a plan made on the device.
+hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src, int rows, const char* tables,
+                         const int (*tot)[2], const char* slot_base, size_t slot_stride, int H, int I, float* h,
+                         uint8_t* hq, float* sh, float* y, hipStream_t s) {
+  const Int8Layout L = int8_layout(H, I);
+  const GemmTable* tab[2][2];
+  for (int p = 0; p < 2; ++p)
+    for (int ph = 0; ph < 2; ++ph)
+      tab[p][ph] = reinterpret_cast<const GemmTable*>(tables + (2 * p + ph) * kTableBytes);
+  const auto grid = [&](int p, int ph) {
+    return tot ? dim3(supertile_blocks(tot[p][ph])) : gemm_grid(ph ? H : 2 * I, p == 0 ? 2 : 1);
+  };
+  const auto any = [&](int p, int ph) { return !tot || tot[p][ph] > 0; };
+  if (any(0, 0))
+    hipLaunchKernelGGL((int8_gemm<1, 16>), grid(0, 0), dim3(512), 0, s, xq, sx, src, tab[0][0], slot_base,
+                       slot_stride, L.p1, L.p1s, 2 * I, H, H, I, h, y);
+  if (any(1, 0))
+    hipLaunchKernelGGL((int8_gemm<1, 8>), grid(1, 0), dim3(512), 0, s, xq, sx, src, tab[1][0], slot_base, slot_stride,
+                       L.p1, L.p1s, 2 * I, H, H, I, h, y);
+  hipLaunchKernelGGL(requantise_h, dim3((rows + 15) / 16), dim3(64 * kReqWaves), 0, s, h, I, hq, sh);
+  if (any(0, 1))
+    hipLaunchKernelGGL((int8_gemm<2, 16>), grid(0, 1), dim3(512), 0, s, hq, sh, nullptr, tab[0][1], slot_base,
+                       slot_stride, L.p2, L.p2s, H, I, H, I, h, y);
+  if (any(1, 1))
+    hipLaunchKernelGGL((int8_gemm<2, 8>), grid(1, 1), dim3(512), 0, s, hq, sh, nullptr, tab[1][1], slot_base,
+                       slot_stride, L.p2, L.p2s, H, I, H, I, h, y);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_pack_int8(int H, int I, const void* Q1, const void* Q3, const void* Q2, const void* S1,
+                            const void* S3, const void* S2, void* blob, hipStream_t s) {
+  const size_t n = (size_t)(2 * I / 16) * (H / 64) * 64 + (size_t)(H / 16) * (I / 64) * 64 + (size_t)2 * I + H;
+  hipLaunchKernelGGL(pack_int8_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                     static_cast<const int8_t*>(Q1), static_cast<const int8_t*>(Q3), static_cast<const int8_t*>(Q2),
+                     static_cast<const float*>(S1), static_cast<const float*>(S3), static_cast<const float*>(S2), H, I,
+                     static_cast<char*>(blob), int8_layout(H, I));
+  return hipGetLastError();
+}
+
+hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const int4* items, int n, int rows_total,
+                                bool gemm, const char* slot_base, size_t slot_stride, int H, int I, float* y, void* ws,
+                                hipStream_t s) {
+  if (n <= 0) return hipSuccess;
+  const Int8Ws w = int8_ws(rows_total, rows_total, H, I);
+  char* b = static_cast<char*>(ws);
+  uint8_t* xq = reinterpret_cast<uint8_t*>(b + w.xq);
+  float *sx = reinterpret_cast<float*>(b + w.sx), *h = reinterpret_cast<float*>(b + w.h);
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  WorkArgs wa;
+  for (int base = 0; base < n; base += kMaxItems) {
+    std::memset(&wa, 0, sizeof wa);
+    wa.n = std::min(kMaxItems, n - base);
+    int most = 0;
+    for (int i = 0; i < wa.n; ++i) {
+      wa.item[i] = items[base + i];
+      most = std::max(most, wa.item[i].z);
+    }
+    const dim3 grid((most + 3) / 4, wa.n);
+    const ArgItems wk{wa};
+    if (H <= 1024) hipLaunchKernelGGL(quantise_items<1>, grid, dim3(256), 0, s, xb, perm_src, wk, H, xq, sx);
+    else if (H <= 2048) hipLaunchKernelGGL(quantise_items<2>, grid, dim3(256), 0, s, xb, perm_src, wk, H, xq, sx);
+    else if (H <= 4096) hipLaunchKernelGGL(quantise_items<4>, grid, dim3(256), 0, s, xb, perm_src, wk, H, xq, sx);
+    else if (H <= 8192) hipLaunchKernelGGL(quantise_items<8>, grid, dim3(256), 0, s, xb, perm_src, wk, H, xq, sx);
+    else hipLaunchKernelGGL(quantise_items<16>, grid, dim3(256), 0, s, xb, perm_src, wk, H, xq, sx);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && !gemm)
+      e = decode_products(wk, wa.n, xq, sx, nullptr, slot_base, slot_stride, H, I, h, y, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!gemm) return hipSuccess;
+  char* tables = b + w.tables;
+  for (int base = 0; base < n; base += kTableItems) {
+    const int m = std::min(kTableItems, n - base);
+    // 128-token tiles throughout (part 1 of the four tables)
+    int tot[2][2] = {{0, 0}, {0, 0}};
+    hipError_t e = plan_gemm_tables(items + base, m, H, I, 128, reinterpret_cast<GemmTable*>(tables + 2 * kTableBytes),
+                                    reinterpret_cast<GemmTable*>(tables + 3 * kTableBytes), tot[1], s);
+    if (e == hipSuccess)
+      e = gemm_products(xq, sx, nullptr, rows_total, tables, tot, slot_base, slot_stride, H, I, h,
+                        reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_ffn_int8_dev(const void* x, int T, const int32_t* perm_src, const int32_t* n_items,
+                               const int4* items, int max_items, int rows_total, const char* slot_base,
+                               size_t slot_stride, int H, int I, float* y, void* ws, hipStream_t s) {
+  if (max_items <= 0 || T <= 0) return hipSuccess;
+  const Int8Ws w = int8_ws(rows_total, rows_total, H, I);
+  char* b = static_cast<char*>(ws);
+  uint8_t* xq = reinterpret_cast<uint8_t*>(b + w.xq);
+  float* sx = reinterpret_cast<float*>(b + w.sx);
+  hipError_t e = launch_quantise_tokens(static_cast<const uint16_t*>(x), T, H, xq, sx, ItemPlan{}, s);
+  if (e != hipSuccess) return e;
+  return decode_products(DevItems{n_items, items}, max_items, xq, sx, perm_src, slot_base, slot_stride, H, I,
+                         reinterpret_cast<float*>(b + w.h), y, s);
+}
+
+hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t* topk_idx, const float* topk_w,
+                               const int32_t* perm_src, const int32_t* perm_pos, const int32_t* counts,
+                               const int32_t* offsets, const int32_t* slot_of, int n_slots, const char* slot_base,
+                               size_t slot_stride, int H, int I, void* out, bool out_bf16, void* ws, float* y,
+                               hipStream_t s) {
+  if (T <= 0) return hipSuccess;
+  const int rows = T * k;
+  const Int8Ws w = int8_ws(rows, T, H, I);
+  char* b = static_cast<char*>(ws);
+  uint8_t* xq = reinterpret_cast<uint8_t*>(b + w.xq);
+  float *sx = reinterpret_cast<float*>(b + w.sx), *h = reinterpret_cast<float*>(b + w.h);
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  // Few rows an expert: weights streamed once per 16 rows; else the tiled GEMM where the shape allows it.
+  const bool gemm = int8_gemm_supported(H, I) && T > 32;
+  hipError_t e;
+  if (!gemm) {
+    const int max_items = std::min(E, rows);
+    // the decode work list takes the place of the GEMMs' tables
+    int32_t* n = reinterpret_cast<int32_t*>(b + w.tables);
+    int4* items = reinterpret_cast<int4*>(b + w.tables + 256);
+    static_assert(kTableItems * sizeof(int4) + 256 <= 4 * kTableBytes, "the list fits the tables");
+    e = launch_quantise_tokens(xb, T, H, xq, sx, ItemPlan{counts, offsets, slot_of, E, n_slots, rows, n, items}, s);
+    if (e == hipSuccess)
+      e = decode_products(DevItems{n, items}, max_items, xq, sx, perm_src, slot_base, slot_stride, H, I, h, y, s);
+  } else {
+    char* tables = b + w.tables;
+    e = launch_plan_tables(counts, offsets, slot_of, E, n_slots, rows, 2 * I, H, 256, 256, 128, tables, s);
+    if (e == hipSuccess) e = launch_quantise_tokens(xb, T, H, xq, sx, ItemPlan{}, s);
+    if (e == hipSuccess)
+      e = gemm_products(xq, sx, perm_src, rows, tables, nullptr, slot_base, slot_stride, H, I, h,
+                        reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
+  }
+  if (e != hipSuccess) return e;
+  const dim3 grid(T, (H + 1023) / 1024);
+  if (out_bf16)
+    hipLaunchKernelGGL(int8_combine<true>, grid, dim3(256), 0, s, y, perm_pos, topk_idx, topk_w, slot_of, n_slots, k,
+                       H, out);
+  else
+    hipLaunchKernelGGL(int8_combine<false>, grid, dim3(256), 0, s, y, perm_pos, topk_idx, topk_w, slot_of, n_slots, k,
+                       H, out);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -8,6 +8,7 @@
 // softmax weights renormalised over the selected k.
 #include "dev_common.hpp"
 #include "dev_resolve.hpp"
+#include "dev_select.hpp"
 #include "moe_kernels.hpp"
 
 namespace moe {
@@ -371,6 +372,8 @@ __device__ __forceinline__ float sum_partials(const float* __restrict__ p, size_
 
 // One block: logits = sum of the partials + bias (fixed order), top-k of
 // every token by one wave each, then the grouping of the <= 16 tokens.
+// GATED: the choice and the weights of select_token under `gate`.
+template <bool GATED>
 __global__ __launch_bounds__(1024) void route_finish_small(const float* __restrict__ partial, int nsplit,
                                                            const float* __restrict__ bias, int T, int E, int k,
                                                            int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
@@ -379,7 +382,8 @@ __global__ __launch_bounds__(1024) void route_finish_small(const float* __restri
                                                            int32_t* __restrict__ perm_src,
                                                            int32_t* __restrict__ perm_pos,
                                                            int32_t* __restrict__ counts_mirror, int32_t mirror_seq,
-                                                           const ResidentList res, const DevStep dev) {
+                                                           const ResidentList res, const DevStep dev,
+                                                           const GateArgs gate) {
   __shared__ float lg[kSmallT * kSmallE];
   __shared__ int32_t sidx[kSmallT * 16];
   __shared__ unsigned long long bm[kSmallE];
@@ -423,33 +427,45 @@ __global__ __launch_bounds__(1024) void route_finish_small(const float* __restri
   __syncthreads();
   if (wave < T) {
     const int t = wave;
-    uint64_t key[kSmallE / 64];
-#pragma unroll
-    for (int v = 0; v < kSmallE / 64; ++v) {
-      const int e = v * 64 + lane;
-      key[v] = e < E ? (((uint64_t)float_key(lg[t * E + e]) << 32) | (uint32_t)(~(uint32_t)e)) : 0ull;
-    }
-    float v0 = 0.f, den = 0.f, my_v = 0.f;
     int my_e = 0;
-    for (int j = 0; j < k; ++j) {
-      uint64_t local = 0;
+    float my_w;
+    if constexpr (GATED) {
+      float l[kSmallE / 64];
 #pragma unroll
-      for (int v = 0; v < kSmallE / 64; ++v) local = key[v] > local ? key[v] : local;
-      const uint64_t best = wave_max_u64(local);
-#pragma unroll
-      for (int v = 0; v < kSmallE / 64; ++v)
-        if (key[v] == best) key[v] = 0;
-      const float val = key_float((uint32_t)(best >> 32));
-      if (j == 0) v0 = val;
-      den += expf(val - v0);
-      if (lane == j) {
-        my_e = (int)(~(uint32_t)best);
-        my_v = val;
+      for (int v = 0; v < kSmallE / 64; ++v) {
+        const int e = lane * (kSmallE / 64) + v;
+        l[v] = e < E ? lg[t * E + e] : 0.f;
       }
+      select_token(l, E, k, gate, lane, my_e, my_w);
+    } else {
+      uint64_t key[kSmallE / 64];
+#pragma unroll
+      for (int v = 0; v < kSmallE / 64; ++v) {
+        const int e = v * 64 + lane;
+        key[v] = e < E ? (((uint64_t)float_key(lg[t * E + e]) << 32) | (uint32_t)(~(uint32_t)e)) : 0ull;
+      }
+      float v0 = 0.f, den = 0.f, my_v = 0.f;
+      for (int j = 0; j < k; ++j) {
+        uint64_t local = 0;
+#pragma unroll
+        for (int v = 0; v < kSmallE / 64; ++v) local = key[v] > local ? key[v] : local;
+        const uint64_t best = wave_max_u64(local);
+#pragma unroll
+        for (int v = 0; v < kSmallE / 64; ++v)
+          if (key[v] == best) key[v] = 0;
+        const float val = key_float((uint32_t)(best >> 32));
+        if (j == 0) v0 = val;
+        den += expf(val - v0);
+        if (lane == j) {
+          my_e = (int)(~(uint32_t)best);
+          my_v = val;
+        }
+      }
+      my_w = expf(my_v - v0) / den;
     }
     if (lane < k) {
       topk_idx[t * k + lane] = my_e;
-      topk_w[t * k + lane] = expf(my_v - v0) / den;
+      topk_w[t * k + lane] = my_w;
       sidx[t * k + lane] = my_e;
       atomicOr(&bm[my_e], 1ull << t);
     }
@@ -564,7 +580,7 @@ size_t route_workspace_bytes(int T, int H, int E, int k) {
 hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* bias, int T, int H, int E, int k,
                         int32_t* topk_idx, float* topk_w, float* logits, int32_t* counts, int32_t* offsets,
                         int32_t* perm_src, int32_t* perm_pos, void* ws, hipStream_t s, int32_t* counts_mirror,
-                        int32_t mirror_seq, const ResidentList* resident, const DevStep* dev) {
+                        int32_t mirror_seq, const ResidentList* resident, const DevStep* dev, const GateArgs* gate) {
   const RoutePlan p = plan_route(T, H, E, bf16);
   ResidentList res{};
   if (resident != nullptr) {
@@ -590,9 +606,14 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
         hipLaunchKernelGGL(router_small_partial<false>, dim3(p.nsplit), dim3(256), 0, s, x, Wr, T, H, E, partial);
       if ((err = hipGetLastError()) != hipSuccess) return err;
     }
-    hipLaunchKernelGGL(route_finish_small, dim3(1), dim3(1024), 0, s, partial, T > 0 ? p.nsplit : 0, bias, T, E, k,
-                       topk_idx, topk_w, logits, counts, offsets, perm_src, perm_pos, counts_mirror, mirror_seq, res,
-                       dv);
+    if (gate != nullptr)
+      hipLaunchKernelGGL(route_finish_small<true>, dim3(1), dim3(1024), 0, s, partial, T > 0 ? p.nsplit : 0, bias, T,
+                         E, k, topk_idx, topk_w, logits, counts, offsets, perm_src, perm_pos, counts_mirror, mirror_seq,
+                         res, dv, *gate);
+    else
+      hipLaunchKernelGGL(route_finish_small<false>, dim3(1), dim3(1024), 0, s, partial, T > 0 ? p.nsplit : 0, bias, T,
+                         E, k, topk_idx, topk_w, logits, counts, offsets, perm_src, perm_pos, counts_mirror, mirror_seq,
+                         res, dv, GateArgs{});
     return hipGetLastError();
   }
   if (p.mode == 1) {
@@ -607,6 +628,9 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
       hipLaunchKernelGGL(router_partial_kernel<false>, grid, dim3(256), 0, s, x, Wr, T, H, E, p.hchunk, partial);
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
+  if (gate != nullptr)
+    return launch_select(partial, p.nsplit, bias, logits, *gate, T, E, k, topk_idx, topk_w, counts, offsets, perm_src,
+                         perm_pos, w + p.hist_off, s, counts_mirror);
   hipLaunchKernelGGL(topk_kernel, dim3((T + 3) / 4), dim3(256), 0, s, partial, p.nsplit, bias,
                      T, E, k, topk_idx, topk_w, logits);
   if ((err = hipGetLastError()) != hipSuccess) return err;
@@ -616,8 +640,16 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
                        hist);
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
+  return launch_group_rows(topk_idx, T, E, k, bits, hist, counts, offsets, perm_src, perm_pos, counts_mirror, s);
+}
+
+hipError_t launch_group_rows(const int32_t* topk_idx, int T, int E, int k, uint64_t* bits, int32_t* hist,
+                             int32_t* counts, int32_t* offsets, int32_t* perm_src, int32_t* perm_pos,
+                             int32_t* counts_mirror, hipStream_t s) {
+  const int nchunks = (T + 63) / 64;
   hipLaunchKernelGGL(expert_scan_kernel, dim3(E), dim3(256), 0, s, hist, nchunks, counts, counts_mirror);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
   hipLaunchKernelGGL(positions_kernel, dim3(nchunks > 0 ? nchunks : 1), dim3(256), (size_t)E * 4, s, topk_idx, T, E, k,
                      nchunks, counts, bits, hist, offsets, perm_src, perm_pos);
   return hipGetLastError();

@@ -134,6 +134,23 @@ struct ResidentList {
   int4* items;          // [E]
   SlotUpdates updates;  // applied to slot_of before the list is made
 };
+// A gate other than the plain softmax over the chosen logits (moe_gate_t).
+struct GateArgs {
+  int score, n_group, topk_group, group_top, renorm;  // score 0: softmax, 1: sigmoid
+  float scale;
+  const float* balance;  // device [E] or nullptr
+};
+// The choice under a gate from logits [T, E], or from nsplit slabs of partial sums (added in order, plus bias [E]; the
+// sums go to `keep` when it is set), and the grouping. ws: select_workspace_bytes.
+size_t select_workspace_bytes(int T, int E);
+hipError_t launch_select(const float* logits, int nsplit, const float* bias, float* keep, const GateArgs& g, int T,
+                         int E, int k, int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* offsets,
+                         int32_t* perm_src, int32_t* perm_pos, void* ws, hipStream_t s,
+                         int32_t* counts_mirror = nullptr);
+// The grouping's last two kernels, from each 64-token chunk's masks bits[chunk][E] and counts hist[E][chunk].
+hipError_t launch_group_rows(const int32_t* topk_idx, int T, int E, int k, uint64_t* bits, int32_t* hist,
+                             int32_t* counts, int32_t* offsets, int32_t* perm_src, int32_t* perm_pos,
+                             int32_t* counts_mirror, hipStream_t s);
 hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* bias, int T, int H, int E, int k,
                         int32_t* topk_idx, float* topk_w, float* logits, int32_t* counts, int32_t* offsets,
                         int32_t* perm_src, int32_t* perm_pos, void* ws, hipStream_t s,
@@ -145,7 +162,9 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
                         const ResidentList* resident = nullptr,
                         // optional, decode-size path only: the device-resident cache's resolve of this layer-step
                         // (as launch_dev_resolve), run at the end of the last routing kernel
-                        const DevStep* dev = nullptr);
+                        const DevStep* dev = nullptr,
+                        // optional: choice and weights under this gate
+                        const GateArgs* gate = nullptr);
 // Whether launch_route takes the decode-size path (and tags its counts mirror).
 bool route_small_path(int T, int E);
 
@@ -251,6 +270,14 @@ hipError_t launch_ffn_grouped(int wfmt, const void* x, const int32_t* perm_src, 
                               const int32_t* offsets, const int32_t* slot_of, int E, int n_slots, int rows_max,
                               const char* slot_base, size_t slot_stride, int H, int I, void* hbuf, float* y,
                               void* tables, hipStream_t s);
+// The planners of those work lists alone: the host planner's tables of n items (gate/up N = 2I, down N = H, tiles of
+// tile_tokens rows; tot receives the super-tile counts), and the device planner's four tables (groups of more than
+// `split` rows in part 0, tiles of tt0 rows, the others in part 1, tiles of tt1; projections of N1 and N2 columns).
+hipError_t plan_gemm_tables(const int4* items, int n, int H, int I, int tile_tokens, GemmTable* t1, GemmTable* t2,
+                            int (&tot)[2], hipStream_t s);
+hipError_t launch_plan_tables(const int32_t* counts, const int32_t* offsets, const int32_t* slot_of, int E,
+                              int n_slots, int rows_max, int N1, int N2, int split, int tt0, int tt1, void* tables,
+                              hipStream_t s);
 int router_gemm2_splits(int T, int H, int E);
 hipError_t launch_router_gemm2(const void* x, const void* wrt, int T, int H, int E, float* partial, int nsplit,
                                hipStream_t s);

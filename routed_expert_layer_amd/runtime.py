@@ -21,7 +21,8 @@ import torch
 
 from . import _lib as L
 
-WFMT = {"f32": L.MOE_W_F32, "bf16": L.MOE_W_BF16, "int4": L.MOE_W_INT4, "mxfp4": L.MOE_W_MXFP4}
+WFMT = {"f32": L.MOE_W_F32, "bf16": L.MOE_W_BF16, "int4": L.MOE_W_INT4, "mxfp4": L.MOE_W_MXFP4,
+        "int8": L.MOE_W_INT8}
 
 
 def _align(v, a):
@@ -68,8 +69,9 @@ class ExpertStore:
         """Pack every expert of physical layer `layer` into the pool.
 
         make_expert(e) returns canonical device tensors: (W1, W3, W2) for fp32/bf16,
-        a dict with q1, q3, q2 (int8) and s1, s3, s2 (fp16) for int4, or a dict with
-        c1, c3, c2 (uint8 FP4 codes) and s1, s3, s2 (uint8 E8M0 scales) for MXFP4.
+        a dict with q1, q3, q2 (int8) and s1, s3, s2 (fp16) for int4, the same with fp32
+        scales per output channel for int8, or a dict with c1, c3, c2 (uint8 FP4 codes)
+        and s1, s3, s2 (uint8 E8M0 scales) for MXFP4.
         """
         assert 0 <= layer < self.P
         stage = torch.empty(batch * self.stride, dtype=torch.uint8, device=device)
@@ -79,7 +81,7 @@ class ExpertStore:
             for j in range(n):
                 w = make_expert(e0 + j)
                 dst = stage[j * self.stride:]
-                if self.wfmt == L.MOE_W_INT4:
+                if self.wfmt in (L.MOE_W_INT4, L.MOE_W_INT8):
                     L.moe_pack_expert(self.wfmt, self.H, self.I, w["q1"], w["q3"], w["q2"], w["s1"], w["s3"],
                                       w["s2"], dst)
                 elif self.wfmt == L.MOE_W_MXFP4:
@@ -115,9 +117,15 @@ class RouteBuffers:
         self.counts_host = torch.empty(E, dtype=torch.int32, pin_memory=True)
         self.offsets_host = torch.empty(E + 1, dtype=torch.int32, pin_memory=True)
 
-    def route(self, x, Wr, bias, stream=None):
+    def route(self, x, Wr, bias, stream=None, gate=None):
+        """Routing of x [T, H] into the buffers; with a Gate, its choice and weights."""
         T = x.shape[0]
         assert T <= self.T
+        if gate is not None:
+            L.moe_route_scored(x, Wr, bias, gate, self.k, self.topk_idx[:T], self.topk_w[:T],
+                               None if self.logits is None else self.logits[:T], self.counts, self.offsets,
+                               self.perm_src, self.perm_pos[:T], self.ws, stream)
+            return
         L.moe_route(x, Wr, bias, self.k, self.topk_idx[:T], self.topk_w[:T],
                     None if self.logits is None else self.logits[:T], self.counts, self.offsets, self.perm_src,
                     self.perm_pos[:T], self.ws, stream)
@@ -185,6 +193,12 @@ class DecodeLayer:
         """Divide misses between GPU fills and CPU execution in the ratio of the rates (e.g. MB/s of pinned
         fills and of the host expert kernel, see measure_rates); rate_cpu = 0 fills every miss."""
         L.moe_cache_set_split(self.cache, rate_gpu, rate_cpu)
+
+    def set_gate(self, gate):
+        """Later steps choose experts under this Gate (None: softmax over the chosen logits)."""
+        if gate is not None:
+            L._typed(gate.balance, "float32", "balance", (self.E,))
+        L.moe_decoder_set_gate(self.dec, gate)
 
     def measure_rates(self, layer=0, n=4, rows=None):
         """(fill MB/s, CPU expert MB/s) on this machine: n pinned blobs of `layer` copied to a scratch device
@@ -268,6 +282,13 @@ class DeviceDecodeLayer:
         L.moe_device_decoder_step(self.dec, layer, x, Wr, bias, o, s)
         return o
 
+    def set_gate(self, gate):
+        """Later steps choose experts under this Gate (None: softmax over the chosen logits); a captured graph keeps
+        the gate it was captured with."""
+        if gate is not None:
+            L._typed(gate.balance, "float32", "balance", (self.E,))
+        L.moe_device_decoder_set_gate(self.dec, gate)
+
     @staticmethod
     def capture(enqueue, stream):
         """Record the work `enqueue()` puts on `stream` (a torch.cuda.Stream) into a graph; nothing runs."""
@@ -299,9 +320,10 @@ class DeviceDecodeLayer:
 class PrefillLayer:
     """Prefill path over a layer whose experts are all resident (blob of expert e at base + e*stride): one
     moe_prefill_layer call enqueues routing, the grouped GEMM over the work list planned on the GPU and the
-    combine; nothing waits for the GPU."""
+    combine; nothing waits for the GPU. With `gate` (a Gate), its choice and weights; int8 experts run moe_experts."""
 
-    def __init__(self, H, I, E, k, T, stride, device="cuda", keep_logits=False, wfmt=L.MOE_W_BF16):
+    def __init__(self, H, I, E, k, T, stride, device="cuda", keep_logits=False, wfmt=L.MOE_W_BF16, gate=None):
+        self.gate = gate
         self.H, self.I, self.E, self.k, self.stride, self.wfmt = H, I, E, k, stride, wfmt
         self.rb = RouteBuffers(T, H, E, k, device, keep_logits)
         rows = T * k
@@ -317,6 +339,12 @@ class PrefillLayer:
         s = stream or torch.cuda.current_stream()
         T = x.shape[0]
         rb = self.rb
+        if self.gate is not None:
+            if timer is not None:
+                raise ValueError("the timed form of the layer takes no gate")
+            L.moe_prefill_layer_scored(x, Wr, bias, self.gate, self.k, self.I, self.wfmt, layer_base, self.stride,
+                                       self.bufs, self.out[:T], s)
+            return self.out[:T]
         if timer is None:
             L.moe_prefill_layer(x, Wr, bias, self.k, self.I, self.wfmt, layer_base, self.stride, self.bufs,
                                 self.out[:T], s)

@@ -1,0 +1,44 @@
+"""Inputs and derived tolerances of the int8 expert tests."""
+import numpy as np
+import torch
+
+import oracle
+from tests.parity import np64
+
+
+def expert(H, I, seed, device="cpu"):
+    """Canonical int8 expert: codes over the whole range [-128, 127] at the edges, scales spread over a factor of 4."""
+    g = torch.Generator().manual_seed(seed)
+    d = {}
+    for n, shape in (("q1", (H, I)), ("q3", (H, I)), ("q2", (I, H))):
+        d[n] = (torch.randn(shape, generator=g) * 40).round().clamp(-128, 127).to(torch.int8)
+        d[n][0, 0], d[n][-1, -1] = -128, 127
+    for n, size, fan in (("s1", I, H), ("s3", I, H), ("s2", H, I)):
+        d[n] = (0.25 + 0.75 * torch.rand(size, generator=g)) / (32 * fan ** 0.5)
+    return {k: v.to(device) for k, v in d.items()}
+
+
+def reference(X, w):
+    """(y, tol) of an expert on rows X in 64 bits. The kernel's h carries fp32 roundings: the integer sum and its two
+    scales 3 half steps, g's share through silu at most (1 + |g|) of that again, exp and the quotient and the product
+    6 more: below 2^-24 (16 + 2 |g|) relative, 2^-19 for |g| < 8 and 2^-18 for |g| < 24. As code units that is at most
+    127 * 2^-18; an h whose 127 h / max|h| lies nearer than that to a half may get either code, which moves y by one
+    step of its scale times its weight. Beside that y carries 2^-18 relative of the row's scale and the final
+    products' roundings, over the sum of magnitudes."""
+    r = oracle.int8_expert(X, *(np64(w[n]) for n in ("q1", "q3", "q2", "s1", "s3", "s2")))
+    amax = np.abs(r["h"]).max(1, keepdims=True)
+    t = np.abs(r["h"]) * 127.0 / np.where(amax > 0, amax, 1.0)
+    near = np.abs(t - np.floor(t) - 0.5) < 127 * 2.0 ** -18
+    W2 = np.abs(np64(w["q2"])) * np64(w["s2"])[None, :]
+    step = r["sh"][:, None]
+    tol = (near * step) @ W2 * (1 + 1e-3) + 2.0 ** -17 * (np.abs(r["hq"]) * step) @ W2 + 1e-30
+    return r["y"], tol
+
+
+def check(got, y, tol, what, out_bf16=False):
+    got = np.asarray(got, np.float64)
+    assert got.shape == y.shape and np.all(np.isfinite(got)), what
+    if out_bf16:
+        tol = tol + 2.0 ** -8 * (np.abs(y) + tol)
+    bad = np.abs(got - y) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.max(np.abs(got - y) / tol):.2f} of its tolerance"
