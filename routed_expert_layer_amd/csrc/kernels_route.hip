@@ -372,8 +372,8 @@ __device__ __forceinline__ float sum_partials(const float* __restrict__ p, size_
 
 // One block: logits = sum of the partials + bias (fixed order), top-k of
 // every token by one wave each, then the grouping of the <= 16 tokens.
-// GATED: the choice and the weights of select_token under `gate`.
-template <bool GATED>
+// VE > 0: the choice and the weights of select_token<VE> under `gate`.
+template <int VE>
 __global__ __launch_bounds__(1024) void route_finish_small(const float* __restrict__ partial, int nsplit,
                                                            const float* __restrict__ bias, int T, int E, int k,
                                                            int32_t* __restrict__ topk_idx, float* __restrict__ topk_w,
@@ -383,7 +383,7 @@ __global__ __launch_bounds__(1024) void route_finish_small(const float* __restri
                                                            int32_t* __restrict__ perm_pos,
                                                            int32_t* __restrict__ counts_mirror, int32_t mirror_seq,
                                                            const ResidentList res, const DevStep dev,
-                                                           const GateArgs gate) {
+                                                           const GateArgs gate, int gate_lanes) {
   __shared__ float lg[kSmallT * kSmallE];
   __shared__ int32_t sidx[kSmallT * 16];
   __shared__ unsigned long long bm[kSmallE];
@@ -427,16 +427,10 @@ __global__ __launch_bounds__(1024) void route_finish_small(const float* __restri
   __syncthreads();
   if (wave < T) {
     const int t = wave;
-    int my_e = 0;
+    int my_e = 0, my_at = lane;
     float my_w;
-    if constexpr (GATED) {
-      float l[kSmallE / 64];
-#pragma unroll
-      for (int v = 0; v < kSmallE / 64; ++v) {
-        const int e = lane * (kSmallE / 64) + v;
-        l[v] = e < E ? lg[t * E + e] : 0.f;
-      }
-      select_token(l, E, k, gate, lane, my_e, my_w);
+    if constexpr (VE > 0) {
+      select_token<VE>(lg + t * E, gate.balance, E / gate.n_group, k, gate, gate_lanes, lane, my_e, my_w, my_at);
     } else {
       uint64_t key[kSmallE / 64];
 #pragma unroll
@@ -464,9 +458,9 @@ __global__ __launch_bounds__(1024) void route_finish_small(const float* __restri
       my_w = expf(my_v - v0) / den;
     }
     if (lane < k) {
-      topk_idx[t * k + lane] = my_e;
-      topk_w[t * k + lane] = my_w;
-      sidx[t * k + lane] = my_e;
+      topk_idx[t * k + my_at] = my_e;
+      topk_w[t * k + my_at] = my_w;
+      sidx[t * k + my_at] = my_e;
       atomicOr(&bm[my_e], 1ull << t);
     }
   }
@@ -560,8 +554,9 @@ RoutePlan plan_route(int T, int H, int E, bool bf16) {
     p.partial_bytes = align_up((size_t)p.nsplit * T * E * sizeof(float), 256);
   }
   p.hist_off = p.partial_bytes;
-  p.bits_off = align_up(p.hist_off + (size_t)nchunks * E * sizeof(int32_t), 256);
-  p.wrt_off = align_up(p.bits_off + (size_t)nchunks * E * sizeof(uint64_t), 256);
+  const int E4 = (E + 3) / 4 * 4;  // a scored gate counts four experts to a word
+  p.bits_off = align_up(p.hist_off + (size_t)nchunks * E4 * sizeof(int32_t), 256);
+  p.wrt_off = align_up(p.bits_off + (size_t)nchunks * E4 * sizeof(uint64_t), 256);
   p.total = p.wrt_off + (p.mode == 1 ? align_up((size_t)H * E * 2, 256) : 0) + 256;
   return p;
 }
@@ -606,14 +601,21 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
         hipLaunchKernelGGL(router_small_partial<false>, dim3(p.nsplit), dim3(256), 0, s, x, Wr, T, H, E, partial);
       if ((err = hipGetLastError()) != hipSuccess) return err;
     }
-    if (gate != nullptr)
-      hipLaunchKernelGGL(route_finish_small<true>, dim3(1), dim3(1024), 0, s, partial, T > 0 ? p.nsplit : 0, bias, T,
-                         E, k, topk_idx, topk_w, logits, counts, offsets, perm_src, perm_pos, counts_mirror, mirror_seq,
-                         res, dv, *gate);
-    else
-      hipLaunchKernelGGL(route_finish_small<false>, dim3(1), dim3(1024), 0, s, partial, T > 0 ? p.nsplit : 0, bias, T,
-                         E, k, topk_idx, topk_w, logits, counts, offsets, perm_src, perm_pos, counts_mirror, mirror_seq,
-                         res, dv, GateArgs{});
+    const SelectShape sh = gate != nullptr ? select_shape(E, gate->n_group) : SelectShape{64, 0};
+    const GateArgs ga = gate != nullptr ? *gate : GateArgs{};
+    const auto finish = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(1), dim3(1024), 0, s, partial, T > 0 ? p.nsplit : 0, bias, T, E, k, topk_idx,
+                         topk_w, logits, counts, offsets, perm_src, perm_pos, counts_mirror, mirror_seq, res, dv, ga,
+                         sh.lanes);
+    };
+    switch (sh.ve) {
+      case 0: finish(route_finish_small<0>); break;
+      case 1: finish(route_finish_small<1>); break;
+      case 2: finish(route_finish_small<2>); break;
+      case 4: finish(route_finish_small<4>); break;
+      case 8: finish(route_finish_small<8>); break;
+      default: finish(route_finish_small<16>); break;  // 512 experts: at most 16 a lane
+    }
     return hipGetLastError();
   }
   if (p.mode == 1) {
