@@ -384,19 +384,14 @@ __device__ __forceinline__ void select_token(const float* logits, const float* b
   my_w = (float)(s * (double)g.scale);
 }
 
-// A row of 16 lanes a token, four tokens to a wave. logits: the lane's token's, in memory; pick, score: LDS of the wave
-// (64 each); bal: the balance in LDS, without NaN. Lane r < k of a row holds one choice, my_at its place. False: the
-// row's token is one that 32-bit scores do not decide (select_token then does).
+// The logits of a row's lanes (-inf past the experts); vec: whole pieces of four, 16-byte aligned.
 template <int VE>
-__device__ __forceinline__ bool select_row(const float* __restrict__ logits, bool vec, const float* bal, int per, int k,
-                                           const GateArgs& g, int lanes, int lane, int* pick, double* score, int& my_e,
-                                           float& my_w, int& my_at) {
-  const int r = lane & 15, row = lane & 48;
-  const int group = r / lanes, sub = r & (lanes - 1);
+__device__ __forceinline__ void load_row(const float* __restrict__ logits, bool vec, int per, int n_group, int lanes,
+                                         int lane, float (&l)[VE]) {
+  const int r = lane & 15, group = r / lanes, sub = r & (lanes - 1);
   const int base = group * per + sub * VE;
-  const int ok = group < g.n_group ? min(max(per - sub * VE, 0), VE) : 0;
-  float l[VE];
-  if (VE % 4 == 0 && vec) {  // whole pieces of four, 16-byte aligned
+  const int ok = group < n_group ? min(max(per - sub * VE, 0), VE) : 0;
+  if (VE % 4 == 0 && vec) {
 #pragma unroll
     for (int v = 0; v < VE; v += 4) {
       f32x4_t q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -411,6 +406,19 @@ __device__ __forceinline__ bool select_row(const float* __restrict__ logits, boo
       if (v < ok) l[v] = logits[base + v];
     }
   }
+}
+
+// A row of 16 lanes a token, four tokens to a wave. l: load_row's; logits: the lane's token's, in memory; pick, score: LDS of the wave
+// (64 each); bal: the balance in LDS, without NaN. Lane r < k of a row holds one choice, my_at its place. False: the
+// row's token is one that 32-bit scores do not decide (select_token then does).
+template <int VE>
+__device__ __forceinline__ bool select_row(float (&l)[VE], const float* __restrict__ logits, const float* bal, int per,
+                                           int k, const GateArgs& g, int lanes, int lane, int* pick, double* score, int& my_e,
+                                           float& my_w, int& my_at) {
+  const int r = lane & 15, row = lane & 48;
+  const int group = r / lanes, sub = r & (lanes - 1);
+  const int base = group * per + sub * VE;
+  const int ok = group < g.n_group ? min(max(per - sub * VE, 0), VE) : 0;
   float most = -INFINITY;
 #pragma unroll
   for (int v = 0; v < VE; ++v) {
@@ -469,10 +477,17 @@ __device__ __forceinline__ bool select_row(const float* __restrict__ logits, boo
     float above, below;
     rank_bounds(rank, by_c, g.score, m, above, below);
     int sure = 0, may = -1;
-    for (int i = 0; i < g.n_group; ++i) {
-      const float o = __shfl(rank, row + i * lanes, 64);
-      sure += o > above ? 1 : 0;
-      may += o >= below ? 1 : 0;
+    // four at a time, so that their exchanges are in flight together
+    for (int i = 0; i < g.n_group; i += 4) {
+      float o[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o[u] = __shfl(rank, row + min(i + u, g.n_group - 1) * lanes, 64);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u < g.n_group) {
+          sure += o[u] > above ? 1 : 0;
+          may += o[u] >= below ? 1 : 0;
+        }
     }
     kept = may < g.topk_group;
     unsure = !kept && sure < g.topk_group;
@@ -491,7 +506,8 @@ __device__ __forceinline__ bool select_row(const float* __restrict__ logits, boo
     return n;
   };
   float hi = row_max(top), lo = below_all(-row_max(top > -INFINITY ? -top : -INFINITY), hi);
-  bool open = hi < INFINITY && row_sum(unsure ? 1 : 0) == 0;  // still looking for the token's threshold
+  const int doubts = row_sum(unsure ? 1 : 0);
+  bool open = hi < INFINITY && doubts == 0;  // still looking for the token's threshold
   float T = lo;
   int mine = reach(T), n = row_sum(mine);
   if (__ballot(open && n < k) != 0) {
@@ -520,11 +536,17 @@ __device__ __forceinline__ bool select_row(const float* __restrict__ logits, boo
   }
   // the chosen to lanes 0 .. k - 1 of the row
   int at = mine;
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) {
-    const int o = __shfl_up(at, d, 16);
-    at += r >= d ? o : 0;
-  }
+  // prefix over the row, by shifts of 1, 2, 4 and 8 lanes, each taken by every lane before it is used by some (inside a
+  // conditional expression the lanes that are read could be inactive)
+  const auto shifted_add = [&](int o, int d) { at += r >= d ? o : 0; };
+  const int o1 = (int)dpp_u32<0x111>((uint32_t)at);
+  shifted_add(o1, 1);
+  const int o2 = (int)dpp_u32<0x112>((uint32_t)at);
+  shifted_add(o2, 2);
+  const int o4 = (int)dpp_u32<0x114>((uint32_t)at);
+  shifted_add(o4, 4);
+  const int o8 = (int)dpp_u32<0x118>((uint32_t)at);
+  shifted_add(o8, 8);
   at += row - mine;
   if (found) {
 #pragma unroll
@@ -552,10 +574,17 @@ __device__ __forceinline__ bool select_row(const float* __restrict__ logits, boo
   score[lane] = cs;
   __builtin_amdgcn_wave_barrier();
   my_at = 0;
-  for (int i = 0; i < k; ++i) {
-    const double oc = score[row + i];
-    const int oe = pick[row + i];
-    my_at += (oc > cs || (oc == cs && oe < my_e)) ? 1 : 0;
+  for (int i = 0; i < k; i += 4) {
+    double oc[4];
+    int oe[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      oc[u] = score[row + min(i + u, k - 1)];
+      oe[u] = pick[row + min(i + u, k - 1)];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (i + u < k) my_at += (oc[u] > cs || (oc[u] == cs && oe[u] < my_e)) ? 1 : 0;
   }
   __builtin_amdgcn_wave_barrier();
   if (g.renorm) {

@@ -108,6 +108,13 @@ __device__ __forceinline__ void choose_rows(const float* __restrict__ logits, co
   __shared__ double score[16][64];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int per = E / g.n_group;
+  // a row past the end repeats the last token, and writes nothing
+  const int i = min(4 * wave + (lane >> 4), n - 1);
+  const bool here = 4 * wave + (lane >> 4) < n;
+  const size_t t = (size_t)(t0 + i);
+  float l[RVE];
+  load_row<RVE>(logits + t * E, ((reinterpret_cast<uintptr_t>(logits) & 15) | (E & 3) | (per & 3)) == 0, per, g.n_group,
+                row_lanes, lane, l);
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     s.masks[e] = 0ull;
     if (g.balance != nullptr) s.balance[e] = fmaxf(g.balance[e], -INFINITY);  // a NaN is -inf
@@ -115,14 +122,10 @@ __device__ __forceinline__ void choose_rows(const float* __restrict__ logits, co
   __syncthreads();
   const float* bal = g.balance != nullptr ? s.balance : nullptr;
   if (4 * wave < n) {
-    const int i = min(4 * wave + (lane >> 4), n - 1);  // a row past the end repeats the last token, and writes nothing
-    const bool here = 4 * wave + (lane >> 4) < n;
-    const size_t t = (size_t)(t0 + i);
-    const bool vec = ((reinterpret_cast<uintptr_t>(logits) & 15) | (E & 3) | (per & 3)) == 0;
     int e, at;
     float w;
-    const bool sure = select_row<RVE>(logits + t * E, vec, bal, per, k, g, row_lanes, lane, pick[wave], score[wave], e,
-                                      w, at);
+    const bool sure = select_row<RVE>(l, logits + t * E, bal, per, k, g, row_lanes, lane, pick[wave], score[wave], e, w,
+                                      at);
     if (sure && here && (lane & 15) < k) {
       topk_idx[t * k + at] = e;
       topk_w[t * k + at] = w;
