@@ -56,7 +56,7 @@ class Gate(ctypes.Structure):
         if isinstance(score, str) and score not in names:
             raise ValueError(f"unknown score {score!r}")
         super().__init__(names.get(score, score), n_group, topk_group, group_top, int(bool(renorm)), scale,
-                         _dptr(_typed(balance, "float32", "balance")))
+                         None if balance is None else _gpu(balance, _device(balance, "balance"), "float32", "balance"))
         self.balance = balance
 
 
@@ -182,30 +182,71 @@ def _dptr(t):
     return _ptr(t)
 
 
-def _typed(t, dtype, name, shape=None):
-    """t, refused unless it has that torch dtype (by name) and, with `shape`, that shape. None passes."""
-    if t is not None and not isinstance(t, int):
-        if str(t.dtype) != "torch." + dtype:
-            raise ValueError(f"{name}: a {dtype} tensor is needed, not {t.dtype}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: shape {tuple(shape)} is needed, not {tuple(t.shape)}")
-    return t
+# torch's own raw query takes a tenth of the time of torch.cuda.current_stream() (3 us, as long as a short launch)
+_raw_stream = None
 
 
-def _routing_args(T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos):
-    """Addresses of a routing's arrays after a check of their types and sizes."""
-    if perm_src.numel() < T * k or str(perm_src.dtype) != "torch.int32":
-        raise ValueError(f"perm_src: int32 of at least {T * k} entries is needed")
-    return [_dptr(_typed(topk_idx, "int32", "topk_idx", (T, k))), _dptr(_typed(topk_w, "float32", "topk_w", (T, k))),
-            _dptr(_typed(counts, "int32", "counts", (E,))), _dptr(_typed(offsets, "int32", "offsets", (E + 1,))),
-            _dptr(perm_src), _dptr(_typed(perm_pos, "int32", "perm_pos", (T, k)))]
+def _current_stream():
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
-def _gate_ref(gate, E=None):
+def _device(t, name):
+    """The index of the GPU that tensor t is on; refused unless it is the current one, which the call launches on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: the library takes a GPU tensor for this argument")
+    import torch
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: on GPU {dev}, while GPU {torch.cuda.current_device()} is the current one")
+    return dev
+
+
+def _gpu(t, dev, dtype, name, shape=None):
+    """Address of a contiguous tensor on GPU `dev`, refused unless it has that torch dtype (by name; None: any) and,
+    with `shape`, that shape."""
+    if dtype is not None and t.dtype is not _torch_dtype(dtype):
+        raise ValueError(f"{name}: a {dtype} tensor is needed, not {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} is needed, not {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: a tensor on GPU {dev} is needed, not one on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: the library takes contiguous tensors")
+    return t.data_ptr()
+
+
+_dtypes = {}
+
+
+def _torch_dtype(name):
+    d = _dtypes.get(name)
+    if d is None:
+        import torch
+        d = _dtypes[name] = getattr(torch, name)
+    return d
+
+
+def _routing_args(dev, T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos):
+    """Addresses of a routing's arrays after a check of their types, sizes and device."""
+    if perm_src.numel() < T * k:
+        raise ValueError(f"perm_src: at least {T * k} entries are needed")
+    tk = (T, k)
+    return (_gpu(topk_idx, dev, "int32", "topk_idx", tk), _gpu(topk_w, dev, "float32", "topk_w", tk),
+            _gpu(counts, dev, "int32", "counts", (E,)), _gpu(offsets, dev, "int32", "offsets", (E + 1,)),
+            _gpu(perm_src, dev, "int32", "perm_src"), _gpu(perm_pos, dev, "int32", "perm_pos", tk))
+
+
+def _gate_ref(gate, E=None, dev=None):
     if gate is None:
         return None
-    if E is not None:
-        _typed(gate.balance, "float32", "balance", (E,))
+    b = gate.balance
+    if b is not None and ((E is not None and b.shape != (E,)) or (dev is not None and b.get_device() != dev)):
+        raise ValueError(f"balance: {E} entries on the call's GPU are needed, not {tuple(b.shape)} on {b.device}")
     return ctypes.byref(gate)
 
 
@@ -215,18 +256,16 @@ def _nbytes(t):
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
 
 
 def _dtype_code(t):
-    import torch
-    if t.dtype == torch.float32:
+    if t.dtype is _torch_dtype("float32"):
         return MOE_DT_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is _torch_dtype("bfloat16"):
         return MOE_DT_BF16
     raise ValueError(f"unsupported activation dtype {t.dtype}")
 
@@ -268,9 +307,11 @@ def moe_select_workspace_size(T, E, k):
 def moe_select(logits, gate, k, topk_idx, topk_w, counts, offsets, perm_src, perm_pos, workspace, stream=None):
     """logits: GPU fp32 [T, E]; gate: a Gate; outputs as moe_route's."""
     T, E = logits.shape
-    idx, w, c, o, ps, pp = _routing_args(T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos)
-    _check(_lib.moe_select(_dptr(_typed(logits, "float32", "logits")), _gate_ref(gate, E), T, E, k, idx, w, c, o, ps, pp,
-                           _dptr(workspace), _nbytes(workspace), _stream(stream)), "moe_select")
+    dev = _device(logits, "logits")
+    idx, w, c, o, ps, pp = _routing_args(dev, T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos)
+    _check(_lib.moe_select(_gpu(logits, dev, "float32", "logits"), _gate_ref(gate, E, dev), T, E, k, idx, w, c, o, ps,
+                           pp, _gpu(workspace, dev, None, "workspace"), _nbytes(workspace), _stream(stream)),
+           "moe_select")
 
 
 def moe_route_scored(x, Wr, bias, gate, k, topk_idx, topk_w, logits, counts, offsets, perm_src, perm_pos, workspace,
@@ -425,15 +466,17 @@ def moe_experts(x, topk_idx, topk_w, perm_src, perm_pos, counts, offsets, slot_o
     int32 [E] or None (expert e in slot e); experts without a slot are left out of the sum."""
     T, k = perm_pos.shape
     E = counts.shape[0]
-    if tuple(x.shape) != (T, H) or tuple(out.shape) != (T, H):
-        raise ValueError(f"moe_experts: x and out must be [{T}, {H}]")
-    if not isinstance(slot_base, int) and slot_base.numel() * slot_base.element_size() < n_slots * slot_stride:
-        raise ValueError(f"moe_experts: slot_base holds fewer than {n_slots} slots of {slot_stride} bytes")
-    idx, w, c, o, ps, pp = _routing_args(T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos)
-    _check(_lib.moe_experts(_dptr(x), _dtype_code(x), idx, w, ps, pp, c, o,
-                            _dptr(_typed(slot_of, "int32", "slot_of", (E,))), T, k, E, n_slots, _dptr(slot_base),
-                            slot_stride, wfmt, H, I, _dptr(out), _dtype_code(out), _dptr(workspace),
-                            _nbytes(workspace), _stream(stream)), "moe_experts")
+    dev = _device(x, "x")
+    if not isinstance(slot_base, int):
+        if _nbytes(slot_base) < n_slots * slot_stride:
+            raise ValueError(f"moe_experts: slot_base holds fewer than {n_slots} slots of {slot_stride} bytes")
+        slot_base = _gpu(slot_base, dev, None, "slot_base")
+    idx, w, c, o, ps, pp = _routing_args(dev, T, k, E, topk_idx, topk_w, counts, offsets, perm_src, perm_pos)
+    _check(_lib.moe_experts(_gpu(x, dev, None, "x", (T, H)), _dtype_code(x), idx, w, ps, pp, c, o,
+                            None if slot_of is None else _gpu(slot_of, dev, "int32", "slot_of", (E,)), T, k, E, n_slots,
+                            slot_base, slot_stride, wfmt, H, I, _gpu(out, dev, None, "out", (T, H)), _dtype_code(out),
+                            _gpu(workspace, dev, None, "workspace"), _nbytes(workspace), _stream(stream)),
+           "moe_experts")
 
 
 def moe_combine(y_perm, perm_pos, topk_w, out, stream=None):
@@ -567,14 +610,15 @@ def moe_prefill_layer_scored(x, Wr, bias, gate, k, I, wfmt, layer_base, blob_str
                                          _dtype_code(out), _stream(stream)), "moe_prefill_layer_scored")
 
 
-def moe_decoder_set_gate(dec, gate):
-    """gate: a Gate (its balance tensor is kept alive with the decoder) or None for moe_route's softmax."""
-    _check(_lib.moe_decoder_set_gate(dec.h, _gate_ref(gate)), "moe_decoder_set_gate")
+def moe_decoder_set_gate(dec, gate, E=None):
+    """gate: a Gate (its balance tensor, of E entries when given, is kept alive with the decoder) or None for moe_route's
+    softmax."""
+    _check(_lib.moe_decoder_set_gate(dec.h, _gate_ref(gate, E)), "moe_decoder_set_gate")
     dec.gate = gate
 
 
-def moe_device_decoder_set_gate(dec, gate):
-    _check(_lib.moe_device_decoder_set_gate(dec.h, _gate_ref(gate)), "moe_device_decoder_set_gate")
+def moe_device_decoder_set_gate(dec, gate, E=None):
+    _check(_lib.moe_device_decoder_set_gate(dec.h, _gate_ref(gate, E)), "moe_device_decoder_set_gate")
     dec.gate = gate
 
 

@@ -196,9 +196,7 @@ class DecodeLayer:
 
     def set_gate(self, gate):
         """Later steps choose experts under this Gate (None: softmax over the chosen logits)."""
-        if gate is not None:
-            L._typed(gate.balance, "float32", "balance", (self.E,))
-        L.moe_decoder_set_gate(self.dec, gate)
+        L.moe_decoder_set_gate(self.dec, gate, self.E)
 
     def measure_rates(self, layer=0, n=4, rows=None):
         """(fill MB/s, CPU expert MB/s) on this machine: n pinned blobs of `layer` copied to a scratch device
@@ -285,9 +283,7 @@ class DeviceDecodeLayer:
     def set_gate(self, gate):
         """Later steps choose experts under this Gate (None: softmax over the chosen logits); a captured graph keeps
         the gate it was captured with."""
-        if gate is not None:
-            L._typed(gate.balance, "float32", "balance", (self.E,))
-        L.moe_device_decoder_set_gate(self.dec, gate)
+        L.moe_device_decoder_set_gate(self.dec, gate, self.E)
 
     @staticmethod
     def capture(enqueue, stream):
