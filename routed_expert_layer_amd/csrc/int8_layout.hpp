@@ -48,9 +48,9 @@ inline bool aligned16(const P*... p) {
 __host__ __device__ inline int int8_k2_source(int c, int q, int j) { return 64 * c + 8 * (j >> 1) + 2 * q + (j & 1); }
 
 // Workspace of the products: token codes and scales, h (fp32), its codes and
-// scales, the GEMMs' tables.
+// scales, the plan (a count, then an entry for each group or 128-row tile).
 struct Int8Ws {
-  size_t xq, sx, h, hq, sh, tables, bytes;
+  size_t xq, sx, h, hq, sh, plan, bytes;
 };
 inline Int8Ws int8_ws(size_t rows, size_t tokens, int H, int I) {
   Int8Ws w{};
@@ -60,8 +60,8 @@ inline Int8Ws int8_ws(size_t rows, size_t tokens, int H, int I) {
   w.h = align_up(w.sx + tokens * 4, 256);
   w.hq = align_up(w.h + padded * I * 4, 256);
   w.sh = align_up(w.hq + padded * I, 256);
-  w.tables = align_up(w.sh + padded * 4, 256);
-  w.bytes = w.tables + 4 * kTableBytes;
+  w.plan = align_up(w.sh + padded * 4, 256);
+  w.bytes = w.plan + 256 + align_up((rows / 128 + kTableItems + 1) * 16, 256);
   return w;
 }
 hipError_t launch_pack_int8(int H, int I, const void* Q1, const void* Q3, const void* Q2, const void* S1,

@@ -145,22 +145,68 @@ struct DevItems {
   }
 };
 
-// The experts with rows as work items, in ascending order, by one block of
-// 256 threads: what the decode kernels of a layer run over. Groups that reach
-// past rows_max and experts without a slot are left out.
-struct ItemPlan {
+// What a layer's kernels run over, planned by one block of 256 threads from a
+// routing's counts and offsets, or from a listed group a thread. Groups that
+// reach past rows_max and experts without a slot are left out.
+//   tile_rows 0: decode, the groups with rows as items {slot, row_begin, rows,
+//     expert}, in ascending order, and their number;
+//   else: prefill, an entry for each tile of tile_rows rows, and their number.
+//     Up to kSuper tiles of a group make a super-row; an entry is {slot, first
+//     row of the super-row, its rows, tiles in it | this one's index << 8}.
+constexpr int kSuper = 8;
+struct Plan {
   const int32_t *counts, *offsets, *slot_of;
-  int E, n_slots, rows_max;
-  int32_t* n;
+  int E, n_slots, rows_max, tile_rows;
+  int32_t* n;  // nullptr: no plan
   int4* items;
 };
 
-__device__ __forceinline__ void plan_items(const ItemPlan& p) {
-  __shared__ int wsum[4];
+// Thread's group `it` of a list of 256 (`base` entries before it); returns the new number of entries. E, lds: LDS.
+__device__ __forceinline__ int plan_groups(int4 it, bool ok, int base, int tile_rows, int4* items, int (*lds)[256],
+                                           int4* group) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int mine = !ok ? 0 : tile_rows ? (it.z + tile_rows - 1) / tile_rows : 1;
+  int x = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(x, d, 64);
+    if (lane >= d) x += o;
+  }
+  if (lane == 63) lds[0][wave] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < 4; ++w) {
+    before += w < wave ? lds[0][w] : 0;
+    all += lds[0][w];
+  }
+  lds[1][tid] = before + x;  // inclusive
+  group[tid] = it;
+  __syncthreads();
+  for (int q = tid; q < all; q += 256) {
+    int lo = 0, hi = 255;  // the group of entry q: the first whose inclusive count is above q
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (lds[1][mid] > q) hi = mid; else lo = mid + 1;
+    }
+    const int4 g = group[lo];
+    int4 e = g;
+    if (tile_rows) {
+      const int tiles = (g.z + tile_rows - 1) / tile_rows, t = q - (lds[1][lo] - tiles), s0 = t / kSuper * kSuper;
+      const int in = min(kSuper, tiles - s0);
+      e = make_int4(g.x, g.y + s0 * tile_rows, min(g.z - s0 * tile_rows, kSuper * tile_rows), in | (t - s0) << 8);
+    }
+    items[base + q] = e;
+  }
+  __syncthreads();
+  return base + all;
+}
+
+__device__ __forceinline__ void run_plan(const Plan& p) {
+  __shared__ int lds[2][256];
+  __shared__ int4 group[256];
   int base = 0;
   for (int e0 = 0; e0 < p.E; e0 += 256) {
-    const int e = e0 + tid;
+    const int e = e0 + (int)threadIdx.x;
     int4 it = make_int4(0, 0, 0, e);
     bool ok = false;
     if (e < p.E) {
@@ -169,19 +215,19 @@ __device__ __forceinline__ void plan_items(const ItemPlan& p) {
       it.x = p.slot_of ? p.slot_of[e] : e;
       ok = it.z > 0 && it.y >= 0 && (long long)it.y + it.z <= p.rows_max && it.x >= 0 && it.x < p.n_slots;
     }
-    const uint64_t m = __ballot(ok);
-    if (lane == 0) wsum[wave] = __popcll(m);
-    __syncthreads();
-    int before = base, all = 0;
-    for (int w = 0; w < 4; ++w) {
-      before += w < wave ? wsum[w] : 0;
-      all += wsum[w];
-    }
-    if (ok) p.items[before + __popcll(m & ((1ull << lane) - 1ull))] = it;
-    base += all;
-    __syncthreads();
+    base = plan_groups(it, ok, base, p.tile_rows, p.items, lds, group);
   }
-  if (tid == 0) *p.n = base;
+  if (threadIdx.x == 0) *p.n = base;
+}
+
+// Prefill entries of up to kMaxItems groups listed on the host.
+__global__ __launch_bounds__(256) void plan_list(const ArgItems wk, int tile_rows, int32_t* __restrict__ n,
+                                                 int4* __restrict__ items) {
+  __shared__ int lds[2][256];
+  __shared__ int4 group[256];
+  const bool ok = (int)threadIdx.x < wk.wa.n;
+  const int all = plan_groups(ok ? wk.wa.item[threadIdx.x] : make_int4(0, 0, 0, 0), ok, 0, tile_rows, items, lds, group);
+  if (threadIdx.x == 0) *n = all;
 }
 
 // T token rows to codes, four rows a block (one a wave); with a plan, block 0
@@ -189,11 +235,11 @@ __device__ __forceinline__ void plan_items(const ItemPlan& p) {
 template <int NC>
 __global__ __launch_bounds__(256) void quantise_tokens(const uint16_t* __restrict__ x, int T, int H,
                                                        uint8_t* __restrict__ xq, float* __restrict__ sx,
-                                                       const ItemPlan plan) {
+                                                       const Plan plan) {
   int block = blockIdx.x;
   if (plan.n != nullptr) {
     if (block == 0) {
-      plan_items(plan);
+      run_plan(plan);
       return;
     }
     --block;
@@ -262,43 +308,64 @@ __global__ __launch_bounds__(256) void pack_int8_kernel(const int8_t* __restrict
 // Decode: every weight byte is read once, straight from memory into matrix
 // instructions whose other operand holds up to 16 tokens' codes.
 // ---------------------------------------------------------------------------
-constexpr int kU8 = 8;  // weight fragments in flight a wave
-
-// A wave's sum over fragments [c0, c1) of a 16-row tile (1 KiB apart from wp) times the token fragments bload(c).
-template <typename BLoad>
-__device__ __forceinline__ i32x4_t int8_wave_dot(const char* wp, int c0, int c1, BLoad bload) {
-  i32x4_t acc = {0, 0, 0, 0};
-  int c = c0;
-  for (; c + kU8 <= c1; c += kU8) {
-    u32x4_t a[kU8], b[kU8];
+// A wave's fragments [c0, c1) of a 16-row tile, 1 KiB apart. Up to NF of them
+// are held: loaded before anything that they wait for (a down projection's
+// codes), and used again for every 16 rows of a group, so weights are read
+// once however long the group is. Past NF (MORE) they are streamed, kStream in
+// flight.
+constexpr int kStream = 8;
+template <int NF, bool MORE>
+struct Held {
+  u32x4_t a[NF];
+  int n;  // fragments held: the first n
+  __device__ __forceinline__ void load(const char* wp, int c0, int c1) {
+    n = min(NF, c1 - c0);
+    if (n == NF) {
 #pragma unroll
-    for (int u = 0; u < kU8; ++u) {
-      a[u] = ld16_nt(wp + (size_t)(c + u) * 1024);
-      b[u] = bload(c + u);
+      for (int u = 0; u < NF; ++u) a[u] = ld16_nt(wp + (size_t)(c0 + u) * 1024);
+    } else {
+#pragma unroll
+      for (int u = 0; u < NF; ++u) {
+        a[u] = u32x4_t{0u, 0u, 0u, 0u};
+        if (u < n) a[u] = ld16_nt(wp + (size_t)(c0 + u) * 1024);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kU8; ++u) acc = mfma_i8(a[u], b[u], acc);
   }
-  const int n = c1 - c;
-  if (n > 0) {  // the last ones as one batch: slots past the end repeat the last fragment against zeros
-    u32x4_t a[kU8], b[kU8];
+  // the sum over all of [c0, c1) times the token fragments bload(c)
+  template <typename BLoad>
+  __device__ __forceinline__ i32x4_t dot(const char* wp, int c0, int c1, BLoad bload) const {
+    i32x4_t acc = {0, 0, 0, 0};
 #pragma unroll
-    for (int u = 0; u < kU8; ++u) {
-      const int cu = c + (u < n ? u : n - 1);
-      a[u] = ld16_nt(wp + (size_t)cu * 1024);
-      b[u] = bload(cu);
-      if (u >= n) b[u] = u32x4_t{0u, 0u, 0u, 0u};
+    for (int u0 = 0; u0 < NF; u0 += kStream) {
+      u32x4_t b[kStream];
+#pragma unroll
+      for (int u = 0; u < kStream; ++u)
+        if (u0 + u < NF) b[u] = bload(min(c0 + u0 + u, c1 - 1));  // past n: against zeros
+#pragma unroll
+      for (int u = 0; u < kStream; ++u)
+        if (u0 + u < NF) acc = mfma_i8(a[u0 + u], b[u], acc);
     }
+    if constexpr (!MORE) return acc;
+    for (int c = c0 + NF; c < c1; c += kStream) {
+      u32x4_t w[kStream], b[kStream];
 #pragma unroll
-    for (int u = 0; u < kU8; ++u) acc = mfma_i8(a[u], b[u], acc);
+      for (int u = 0; u < kStream; ++u) {
+        const int cu = min(c + u, c1 - 1);
+        w[u] = ld16_nt(wp + (size_t)cu * 1024);
+        b[u] = bload(cu);
+        if (c + u >= c1) b[u] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int u = 0; u < kStream; ++u) acc = mfma_i8(w[u], b[u], acc);
+    }
+    return acc;
   }
-  return acc;
-}
+};
 
 // Gate/up: a block is one 16-row tile of P1 (8 gate and 8 up columns) of an
 // item, its four waves splitting K. src: the token of each grouped row
 // (nullptr: xq holds the grouped rows). h: fp32, row-major.
-template <typename W>
+template <typename W, int NF, bool MORE>
 __global__ __launch_bounds__(256) void int8_decode_up(const uint8_t* __restrict__ xq, const float* __restrict__ sx,
                                                       const int32_t* __restrict__ src, const W wk,
                                                       const char* __restrict__ slot_base, size_t slot_stride,
@@ -307,10 +374,12 @@ __global__ __launch_bounds__(256) void int8_decode_up(const uint8_t* __restrict_
   const int item = blockIdx.x / NT, tile = blockIdx.x - item * NT;
   int4 it;
   if (!wk.get(item, it)) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
   const int KC = H / 64, c0 = (KC * wave) >> 2, c1 = (KC * (wave + 1)) >> 2;
   const char* blob = slot_base + (size_t)it.x * slot_stride;
   const char* wp = blob + L.p1 + (size_t)tile * KC * 1024 + lane * 16;
+  Held<NF, MORE> w;
+  w.load(wp, c0, c1);
   __shared__ i32x4_t red[4][64];
   for (int m0 = 0; m0 < it.z; m0 += 16) {
     const int m = m0 + (lane & 15);
@@ -318,7 +387,7 @@ __global__ __launch_bounds__(256) void int8_decode_up(const uint8_t* __restrict_
     // lanes past the group read its first row again: their columns are not stored
     const int r = it.y + (valid ? m : 0), t = src ? src[r] : r;
     const uint8_t* xr = xq + (size_t)t * H + 16 * (lane >> 4);
-    red[wave][lane] = int8_wave_dot(wp, c0, c1, [&](int c) { return ld16(xr + (size_t)c * 64); });
+    red[wave][lane] = c0 < c1 ? w.dot(wp, c0, c1, [&](int c) { return ld16(xr + (size_t)c * 64); }) : i32x4_t{0, 0, 0, 0};
     __syncthreads();
     if (wave == 0 && valid) {
       const i32x4_t s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
@@ -333,71 +402,114 @@ __global__ __launch_bounds__(256) void int8_decode_up(const uint8_t* __restrict_
   }
 }
 
-// The codes of rows [r0, r0 + n) of h (n <= 16), by a block's waves, into LDS
-// in the order of P2's K (int8_k2_source): fragment c at 1024 c, lane
-// (column group, row) at 16 bytes each. Rows past n are zeroed.
-__device__ __forceinline__ void quantise_h_rows(const float* __restrict__ h, int r0, int n, int I, char* lds,
-                                                float* scales) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  for (int m = wave; m < 16; m += waves) {
-    if (m >= n) {
-      for (int c = lane; c < I / 16; c += 64)
-        *reinterpret_cast<u32x4_t*>(lds + (c >> 2) * 1024 + ((c & 3) * 16 + m) * 16) = u32x4_t{0u, 0u, 0u, 0u};
-      continue;
-    }
-    const float* row = h + (size_t)(r0 + m) * I;
-    uint32_t mx = 0;
-    for (int i = 4 * lane; i < I; i += 256) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + i);
+// Four columns of row m's codes into LDS in the order of P2's K (int8_k2_source): fragment c at 1024 c, lane (column
+// group, row) at 16 bytes each, columns 2q and 2q + 1 of every 8 beside each other.
+__device__ __forceinline__ void put_h_codes(char* lds, int m, int col, const RowQuant& rq, const f32x4_t& v) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) mx = max(mx, abs_bits(v[w]));
-    }
-    const RowQuant rq(wave_max_u32(mx));
-    for (int i = 4 * lane; i < I; i += 256) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + i);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {  // columns i + 2p, i + 2p + 1: one column group, neighbouring bytes
-        const int col = i + 2 * p;
-        char* at = lds + (col >> 6) * 1024 + (((col >> 1) & 3) * 16 + m) * 16 + 2 * ((col >> 3) & 7);
-        *reinterpret_cast<uint16_t*>(at) =
-            (uint16_t)((rq.code(v[2 * p]) & 0xFF) | ((rq.code(v[2 * p + 1]) & 0xFF) << 8));
-      }
-    }
-    if (lane == 0) scales[m] = rq.scale();
+  for (int p = 0; p < 2; ++p) {
+    const int c = col + 2 * p;
+    *reinterpret_cast<uint16_t*>(lds + (c >> 6) * 1024 + (((c >> 1) & 3) * 16 + m) * 16 + 2 * ((c >> 3) & 7)) =
+        (uint16_t)((rq.code(v[2 * p]) & 0xFF) | ((rq.code(v[2 * p + 1]) & 0xFF) << 8));
   }
 }
 
-// Down projection: a block is one 16-row tile of P2 (16 output columns) of an
-// item; it forms the codes of the item's rows of h itself.
-template <typename W>
+// The codes of rows [r0, r0 + n) of h (n <= 16) into LDS by a block of 256
+// threads: a row's maximum over the block, then its codes, kQuantRows rows at a
+// time in registers (rows of up to 2048; longer ones are read twice). Columns
+// of rows past n are left as they are: they are other tokens' columns of the
+// products, which are not stored. mx: LDS of 16 x 4 words.
+constexpr int kQuantRows = 4;
+__device__ __forceinline__ void quantise_h_rows(const float* __restrict__ h, int r0, int n, int I, char* lds,
+                                                float* scales, uint32_t (*mx)[4]) {
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  for (int m0 = 0; m0 < n; m0 += kQuantRows) {
+    f32x4_t v[kQuantRows][2];
+#pragma unroll
+    for (int r = 0; r < kQuantRows; ++r) {
+      const float* row = h + (size_t)(r0 + min(m0 + r, n - 1)) * I;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int i = 4 * tid + 1024 * p;
+        v[r][p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (i < I) v[r][p] = *reinterpret_cast<const f32x4_t*>(row + i);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kQuantRows; ++r) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = max(m, abs_bits(v[r][p][w]));
+      if (I > 2048) {
+        const float* row = h + (size_t)(r0 + min(m0 + r, n - 1)) * I;
+        for (int i = 4 * tid + 2048; i < I; i += 1024) {
+          const f32x4_t q = *reinterpret_cast<const f32x4_t*>(row + i);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) m = max(m, abs_bits(q[w]));
+        }
+      }
+      m = wave_max_u32(m);
+      if (lane == 0 && m0 + r < n) mx[m0 + r][wave] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kQuantRows; ++r) {
+      if (m0 + r >= n) break;
+      const RowQuant rq(max(max(mx[m0 + r][0], mx[m0 + r][1]), max(mx[m0 + r][2], mx[m0 + r][3])));
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (4 * tid + 1024 * p < I) put_h_codes(lds, m0 + r, 4 * tid + 1024 * p, rq, v[r][p]);
+      if (I > 2048) {
+        const float* row = h + (size_t)(r0 + m0 + r) * I;
+        for (int i = 4 * tid + 2048; i < I; i += 1024)
+          put_h_codes(lds, m0 + r, i, rq, *reinterpret_cast<const f32x4_t*>(row + i));
+      }
+      if (tid == 0) scales[m0 + r] = rq.scale();
+    }
+  }
+}
+
+// Down projection: a block is R 16-row tiles of P2 (16 R output columns) of an
+// item; it forms the codes of the item's rows of h itself, while its weights
+// are on their way.
+template <typename W, int NF, bool MORE, int R>
 __global__ __launch_bounds__(256) void int8_decode_down(const float* __restrict__ h, const W wk,
                                                         const char* __restrict__ slot_base, size_t slot_stride,
                                                         const Int8Layout L, int H, int I, float* __restrict__ y) {
-  const int NT = H / 16;
-  const int item = blockIdx.x / NT, tile = blockIdx.x - item * NT;
+  const int NB = H / (16 * R);
+  const int item = blockIdx.x / NB, tile0 = (blockIdx.x - item * NB) * R;
   int4 it;
   if (!wk.get(item, it)) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
   const int KC = I / 64, c0 = (KC * wave) >> 2, c1 = (KC * (wave + 1)) >> 2;
   const char* blob = slot_base + (size_t)it.x * slot_stride;
-  const char* wp = blob + L.p2 + (size_t)tile * KC * 1024 + lane * 16;
+  const char* wp = blob + L.p2 + (size_t)tile0 * KC * 1024 + lane * 16;
+  Held<NF, MORE> w[R];
+#pragma unroll
+  for (int t = 0; t < R; ++t) w[t].load(wp + (size_t)t * KC * 1024, c0, c1);
   extern __shared__ __attribute__((aligned(16))) char codes[];  // 16 rows of I bytes
-  __shared__ i32x4_t red[4][64];
+  __shared__ i32x4_t red[4][R][64];
   __shared__ float sh[16];
+  __shared__ uint32_t mx[16][4];
   for (int m0 = 0; m0 < it.z; m0 += 16) {
-    quantise_h_rows(h, it.y + m0, min(16, it.z - m0), I, codes, sh);
+    quantise_h_rows(h, it.y + m0, min(16, it.z - m0), I, codes, sh, mx);
     __syncthreads();
-    red[wave][lane] = int8_wave_dot(wp, c0, c1, [&](int c) { return ld16(codes + (size_t)c * 1024 + lane * 16); });
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+      red[wave][t][lane] = c0 < c1 ? w[t].dot(wp + (size_t)t * KC * 1024, c0, c1,
+                                              [&](int c) { return ld16(codes + (size_t)c * 1024 + lane * 16); })
+                                   : i32x4_t{0, 0, 0, 0};
     __syncthreads();
     const int m = m0 + (lane & 15);
-    if (wave == 0 && m < it.z) {
-      const i32x4_t s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
-      const int n0 = 16 * tile + 4 * (lane >> 4);
+    if (wave < R && m < it.z) {
+      const i32x4_t s = red[0][wave][lane] + red[1][wave][lane] + red[2][wave][lane] + red[3][wave][lane];
+      const int n0 = 16 * (tile0 + wave) + 4 * (lane >> 4);
       const f32x4_t sw = *reinterpret_cast<const f32x4_t*>(blob + L.p2s + (size_t)n0 * 4);
       const float st = sh[lane & 15];
       f32x4_t o;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) o[w] = (float)s[w] * (st * sw[w]);
+      for (int c = 0; c < 4; ++c) o[c] = (float)s[c] * (st * sw[c]);
       *reinterpret_cast<f32x4_t*>(y + (size_t)(it.y + m) * H + n0) = o;
     }
     __syncthreads();
@@ -416,12 +528,18 @@ __device__ __forceinline__ size_t h_tile_at(size_t row, int piece, int q, int I)
   return ((row >> 4) * (size_t)(I / 8) + piece) * 128 + (q * 16 + (row & 15)) * 2;
 }
 
+// Tile t of the launch: entry t / NTB's super-row, in which the tiles go in
+// groups of kGroupN weight tiles over all its token tiles, so that the blocks
+// that run together on an XCD share 8 x 4 tiles' operands in its L2.
+constexpr int kGroupN = 4;
+
 template <int PHASE, int BM_T>
-__device__ __forceinline__ void int8_tile(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
-                                          const int32_t* __restrict__ src, const GemmTable* __restrict__ tab,
-                                          const char* __restrict__ slot_base, size_t slot_stride, size_t mat_off,
-                                          size_t scale_off, int N, int K, int H, int I, float* __restrict__ hout,
-                                          float* __restrict__ yout, const int sidx, const int w) {
+__global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
+                                                    const int32_t* __restrict__ src, const int32_t* __restrict__ n_entries,
+                                                    const int4* __restrict__ entries,
+                                                    const char* __restrict__ slot_base, size_t slot_stride,
+                                                    size_t mat_off, size_t scale_off, int N, int K, int H, int I,
+                                                    float* __restrict__ hout, float* __restrict__ yout) {
   constexpr int BN_T = 16;
   constexpr int NS = BM_T == 16 ? 4 : 6;
   constexpr int WN = BM_T == 16 ? 8 : 4;
@@ -433,24 +551,22 @@ __device__ __forceinline__ void int8_tile(const uint8_t* __restrict__ bsrc, cons
   constexpr int STAGE = (FA + FB) * 1024;
   __shared__ __attribute__((aligned(1024))) char lds[NS][STAGE];
 
-  const int NTB = N / (16 * BN_T);
-  int lo = 0, hi = tab->n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tab->tile_prefix[mid] <= sidx) lo = mid; else hi = mid - 1;
-  }
-  const int4 it = tab->item[lo];
-  const int GM = it.w & 0xFF, GN = it.w >> 8;
-  if (w >= GM * GN) return;
-  const int ls = sidx - tab->tile_prefix[lo];
-  const int ngroups = NTB / GN;
-  const int mt = (ls / ngroups) * GM + w / GN;
-  const int nt = (ls % ngroups) * GN + (w % GN);
-  if (mt * 16 * BM_T >= it.z) return;
-  // the thread index passes through an empty asm so that nothing derived from it stays live over the loop of tiles
-  int tid = (int)threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const int wave = tid >> 6, lane = tid & 63;
+  // an eighth of the tiles for each XCD (blocks b with the same b % 8), in order
+  const int NTB = N / (16 * BN_T), total = *n_entries * NTB, share = (total + 7) / 8;
+  const int in_share = (int)(blockIdx.x >> 3), t = (int)(blockIdx.x & 7) * share + in_share;
+  if (in_share >= share || t >= total) return;
+  const int ent = t / NTB;
+  const int4 en = entries[ent];
+  const int gm = en.w & 0xFF;
+  const int li = (en.w >> 8) * NTB + (t - ent * NTB);
+  const int whole = NTB / kGroupN * kGroupN * gm;  // tiles in whole groups of weight tiles
+  const int width = li < whole ? kGroupN : NTB % kGroupN, lg = li < whole ? li : li - whole;
+  const int ng = lg / (gm * width), rem = lg - ng * gm * width;
+  const int mt = rem / width, nt = (li < whole ? ng * kGroupN : NTB / kGroupN * kGroupN) + rem % width;
+  const int4 it = make_int4(__builtin_amdgcn_readfirstlane(en.x), __builtin_amdgcn_readfirstlane(en.y),
+                            __builtin_amdgcn_readfirstlane(en.z), 0);
+  const int tid = (int)threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int wn = wave % WAVES_N, wm = wave / WAVES_N;
   const int KC = K / 64;
   const char* blob = slot_base + (size_t)it.x * slot_stride;
@@ -586,26 +702,6 @@ __device__ __forceinline__ void int8_tile(const uint8_t* __restrict__ bsrc, cons
   }
 }
 
-// Rounds of super-tiles as in the bf16 GEMM: block b works on super-tiles (b / 256) * 8 + b % 8, then that plus
-// 8 * (grid / 256), and so on, in slot (b / 8) % 32 of each. Every exit is uniform per block.
-template <int PHASE, int BM_T>
-__global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
-                                                    const int32_t* __restrict__ src,
-                                                    const GemmTable* __restrict__ tab,
-                                                    const char* __restrict__ slot_base, size_t slot_stride,
-                                                    size_t mat_off, size_t scale_off, int N, int K, int H, int I,
-                                                    float* __restrict__ hout, float* __restrict__ yout) {
-  const int first = (int)(blockIdx.x >> 8), rounds = (int)(gridDim.x >> 8);
-  const int total = tab->total_tiles;
-  for (int r = first;; r += rounds) {
-    const int sidx = r * 8 + (int)(blockIdx.x & 7);
-    if (sidx >= total) break;
-    if (r != first) __syncthreads();
-    int8_tile<PHASE, BM_T>(bsrc, bscale, src, tab, slot_base, slot_stride, mat_off, scale_off, N, K, H, I, hout, yout,
-                           sidx, (int)((blockIdx.x >> 3) & 31));
-  }
-}
-
 // h to codes between the products: a block is one 16-row tile; lane (q, row)
 // of a wave reads its two columns of each of a 64-wide piece's eight 8-wide
 // parts and has the 16 code bytes of its place in the token fragment (the
@@ -693,15 +789,7 @@ __global__ __launch_bounds__(256) void int8_combine(const float* __restrict__ y,
   }
 }
 
-// Workgroup rounds of a grouped launch, as for the bf16 GEMM (see launch_ffn_grouped).
-dim3 gemm_grid(int N, int gm_min) {
-  int shape = 0;
-  supertiles_of(gm_min * 128, N, 128, shape);
-  const int fill = (shape & 0xFF) * (shape >> 8);
-  return dim3(256 * 8 * (fill >= 32 ? 1 : 32 / fill));
-}
-
-hipError_t launch_quantise_tokens(const uint16_t* x, int T, int H, uint8_t* xq, float* sx, const ItemPlan& plan,
+hipError_t launch_quantise_tokens(const uint16_t* x, int T, int H, uint8_t* xq, float* sx, const Plan& plan,
                                   hipStream_t s) {
   const dim3 grid((T + 3) / 4 + (plan.n != nullptr ? 1 : 0));
   if (H <= 1024) hipLaunchKernelGGL(quantise_tokens<1>, grid, dim3(256), 0, s, x, T, H, xq, sx, plan);
@@ -712,48 +800,59 @@ hipError_t launch_quantise_tokens(const uint16_t* x, int T, int H, uint8_t* xq, 
   return hipGetLastError();
 }
 
+template <typename W, int NF, bool MORE>
+hipError_t decode_down(const W& wk, int n_items, const char* slot_base, size_t slot_stride, int H, int I,
+                       const float* h, float* y, hipStream_t s) {
+  constexpr int R = 2;  // H is a multiple of 64
+  hipLaunchKernelGGL((int8_decode_down<W, NF, MORE, R>), dim3(n_items * (H / (16 * R))), dim3(256), (size_t)16 * I, s, h, wk,
+                     slot_base, slot_stride, int8_layout(H, I), H, I, y);
+  return hipGetLastError();
+}
+
 template <typename W>
 hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const float* sx, const int32_t* src,
                            const char* slot_base, size_t slot_stride, int H, int I, float* h, float* y,
                            hipStream_t s) {
   const Int8Layout L = int8_layout(H, I);
-  hipLaunchKernelGGL(int8_decode_up<W>, dim3(n_items * (I / 8)), dim3(256), 0, s, xq, sx, src, wk, slot_base,
-                     slot_stride, L, H, I, h);
+  const auto up = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(n_items * (I / 8)), dim3(256), 0, s, xq, sx, src, wk, slot_base, slot_stride, L, H,
+                       I, h);
+  };
+  // Held fragments a wave: a quarter of K / 64, up to 8. (H 4096: 16 held took 40 us a token's call and 128 us of eight
+  // tokens, 8 held and 8 streamed 37.5 and 121, having more waves resident.)
+  if (H <= 1024) up(int8_decode_up<W, 4, false>);
+  else if (H <= 2048) up(int8_decode_up<W, 8, false>);
+  else up(int8_decode_up<W, 8, true>);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(int8_decode_down<W>, dim3(n_items * (H / 16)), dim3(256), (size_t)16 * I, s, h, wk, slot_base,
-                     slot_stride, L, H, I, y);
-  return hipGetLastError();
+  if (I <= 1024) return decode_down<W, 4, false>(wk, n_items, slot_base, slot_stride, H, I, h, y, s);
+  if (I <= 2048) return decode_down<W, 8, false>(wk, n_items, slot_base, slot_stride, H, I, h, y, s);
+  return decode_down<W, 8, true>(wk, n_items, slot_base, slot_stride, H, I, h, y, s);
 }
 
-// The two products and the pass between them over tables the planners wrote; launch shapes for a host plan (tot:
-// super-tiles of each part and projection) or, with tot null, for a plan made on the device.
-hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src, int rows, const char* tables,
-                         const int (*tot)[2], const char* slot_base, size_t slot_stride, int H, int I, float* h,
-                         uint8_t* hq, float* sh, float* y, hipStream_t s) {
+// Rows a prefill tile holds: 256 when groups have that many on average (16384 tokens over 64 experts: the 128-row tile
+// reads each weight tile twice as often from L2), else 128 (a 96-row group leaves half of a 256-row tile's waves idle).
+int tile_rows_for(int rows, int groups) { return (long long)rows >= 256ll * groups ? 256 : 128; }
+
+// The two products and the pass between them over planned entries (at most rows / tile + groups).
+hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src, int rows, int groups, int tile_rows,
+                         const int32_t* n, const int4* entries, const char* slot_base, size_t slot_stride, int H, int I,
+                         float* h, uint8_t* hq, float* sh, float* y, hipStream_t s) {
   const Int8Layout L = int8_layout(H, I);
-  const GemmTable* tab[2][2];
-  for (int p = 0; p < 2; ++p)
-    for (int ph = 0; ph < 2; ++ph)
-      tab[p][ph] = reinterpret_cast<const GemmTable*>(tables + (2 * p + ph) * kTableBytes);
-  const auto grid = [&](int p, int ph) {
-    return tot ? dim3(supertile_blocks(tot[p][ph])) : gemm_grid(ph ? H : 2 * I, p == 0 ? 2 : 1);
+  const auto grid = [&](int N) { return dim3((unsigned)(((size_t)(rows / tile_rows + groups) * (N / 256) + 7) / 8 * 8)); };
+  const auto product = [&](auto kernel, int N, int K, const uint8_t* b, const float* bs, const int32_t* from, size_t mat,
+                           size_t scales) {
+    hipLaunchKernelGGL(kernel, grid(N), dim3(512), 0, s, b, bs, from, n, entries, slot_base, slot_stride, mat, scales, N,
+                       K, H, I, h, y);
+    return hipGetLastError();
   };
-  const auto any = [&](int p, int ph) { return !tot || tot[p][ph] > 0; };
-  if (any(0, 0))
-    hipLaunchKernelGGL((int8_gemm<1, 16>), grid(0, 0), dim3(512), 0, s, xq, sx, src, tab[0][0], slot_base,
-                       slot_stride, L.p1, L.p1s, 2 * I, H, H, I, h, y);
-  if (any(1, 0))
-    hipLaunchKernelGGL((int8_gemm<1, 8>), grid(1, 0), dim3(512), 0, s, xq, sx, src, tab[1][0], slot_base, slot_stride,
-                       L.p1, L.p1s, 2 * I, H, H, I, h, y);
+  hipError_t e = tile_rows == 256 ? product(int8_gemm<1, 16>, 2 * I, H, xq, sx, src, L.p1, L.p1s)
+                                  : product(int8_gemm<1, 8>, 2 * I, H, xq, sx, src, L.p1, L.p1s);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(requantise_h, dim3((rows + 15) / 16), dim3(64 * kReqWaves), 0, s, h, I, hq, sh);
-  if (any(0, 1))
-    hipLaunchKernelGGL((int8_gemm<2, 16>), grid(0, 1), dim3(512), 0, s, hq, sh, nullptr, tab[0][1], slot_base,
-                       slot_stride, L.p2, L.p2s, H, I, H, I, h, y);
-  if (any(1, 1))
-    hipLaunchKernelGGL((int8_gemm<2, 8>), grid(1, 1), dim3(512), 0, s, hq, sh, nullptr, tab[1][1], slot_base,
-                       slot_stride, L.p2, L.p2s, H, I, H, I, h, y);
-  return hipGetLastError();
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return tile_rows == 256 ? product(int8_gemm<2, 16>, H, I, hq, sh, nullptr, L.p2, L.p2s)
+                          : product(int8_gemm<2, 8>, H, I, hq, sh, nullptr, L.p2, L.p2s);
 }
 
 }  // namespace
@@ -781,10 +880,11 @@ hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const in
   for (int base = 0; base < n; base += kMaxItems) {
     std::memset(&wa, 0, sizeof wa);
     wa.n = std::min(kMaxItems, n - base);
-    int most = 0;
+    int most = 0, rows = 0;
     for (int i = 0; i < wa.n; ++i) {
       wa.item[i] = items[base + i];
       most = std::max(most, wa.item[i].z);
+      rows += wa.item[i].z;
     }
     const dim3 grid((most + 3) / 4, wa.n);
     const ArgItems wk{wa};
@@ -794,21 +894,19 @@ hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const in
     else if (H <= 8192) hipLaunchKernelGGL(quantise_items<8>, grid, dim3(256), 0, s, xb, perm_src, wk, H, xq, sx);
     else hipLaunchKernelGGL(quantise_items<16>, grid, dim3(256), 0, s, xb, perm_src, wk, H, xq, sx);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && !gemm)
-      e = decode_products(wk, wa.n, xq, sx, nullptr, slot_base, slot_stride, H, I, h, y, s);
     if (e != hipSuccess) return e;
-  }
-  if (!gemm) return hipSuccess;
-  char* tables = b + w.tables;
-  for (int base = 0; base < n; base += kTableItems) {
-    const int m = std::min(kTableItems, n - base);
-    // 128-token tiles throughout (part 1 of the four tables)
-    int tot[2][2] = {{0, 0}, {0, 0}};
-    hipError_t e = plan_gemm_tables(items + base, m, H, I, 128, reinterpret_cast<GemmTable*>(tables + 2 * kTableBytes),
-                                    reinterpret_cast<GemmTable*>(tables + 3 * kTableBytes), tot[1], s);
-    if (e == hipSuccess)
-      e = gemm_products(xq, sx, nullptr, rows_total, tables, tot, slot_base, slot_stride, H, I, h,
-                        reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
+    if (!gemm) {
+      e = decode_products(wk, wa.n, xq, sx, nullptr, slot_base, slot_stride, H, I, h, y, s);
+    } else {
+      const int tile = tile_rows_for(rows, wa.n);
+      int32_t* count = reinterpret_cast<int32_t*>(b + w.plan);
+      int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
+      hipLaunchKernelGGL(plan_list, dim3(1), dim3(256), 0, s, wk, tile, count, entries);
+      if ((e = hipGetLastError()) == hipSuccess)
+        // rows_total: the pass between the products covers every row of the workspace, listed or not
+        e = gemm_products(xq, sx, nullptr, rows_total, wa.n, tile, count, entries, slot_base, slot_stride, H, I, h,
+                          reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
+    }
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -822,7 +920,7 @@ hipError_t launch_ffn_int8_dev(const void* x, int T, const int32_t* perm_src, co
   char* b = static_cast<char*>(ws);
   uint8_t* xq = reinterpret_cast<uint8_t*>(b + w.xq);
   float* sx = reinterpret_cast<float*>(b + w.sx);
-  hipError_t e = launch_quantise_tokens(static_cast<const uint16_t*>(x), T, H, xq, sx, ItemPlan{}, s);
+  hipError_t e = launch_quantise_tokens(static_cast<const uint16_t*>(x), T, H, xq, sx, Plan{}, s);
   if (e != hipSuccess) return e;
   return decode_products(DevItems{n_items, items}, max_items, xq, sx, perm_src, slot_base, slot_stride, H, I,
                          reinterpret_cast<float*>(b + w.h), y, s);
@@ -842,24 +940,17 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   const uint16_t* xb = static_cast<const uint16_t*>(x);
   // Few rows an expert: weights streamed once per 16 rows; else the tiled GEMM where the shape allows it.
   const bool gemm = int8_gemm_supported(H, I) && T > 32;
-  hipError_t e;
-  if (!gemm) {
-    const int max_items = std::min(E, rows);
-    // the decode work list takes the place of the GEMMs' tables
-    int32_t* n = reinterpret_cast<int32_t*>(b + w.tables);
-    int4* items = reinterpret_cast<int4*>(b + w.tables + 256);
-    static_assert(kTableItems * sizeof(int4) + 256 <= 4 * kTableBytes, "the list fits the tables");
-    e = launch_quantise_tokens(xb, T, H, xq, sx, ItemPlan{counts, offsets, slot_of, E, n_slots, rows, n, items}, s);
-    if (e == hipSuccess)
-      e = decode_products(DevItems{n, items}, max_items, xq, sx, perm_src, slot_base, slot_stride, H, I, h, y, s);
-  } else {
-    char* tables = b + w.tables;
-    e = launch_plan_tables(counts, offsets, slot_of, E, n_slots, rows, 2 * I, H, 256, 256, 128, tables, s);
-    if (e == hipSuccess) e = launch_quantise_tokens(xb, T, H, xq, sx, ItemPlan{}, s);
-    if (e == hipSuccess)
-      e = gemm_products(xq, sx, perm_src, rows, tables, nullptr, slot_base, slot_stride, H, I, h,
-                        reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
-  }
+  const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups) : 0;
+  int32_t* n = reinterpret_cast<int32_t*>(b + w.plan);
+  int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
+  hipError_t e = launch_quantise_tokens(xb, T, H, xq, sx,
+                                        Plan{counts, offsets, slot_of, E, n_slots, rows, tile, n, entries}, s);
+  if (e != hipSuccess) return e;
+  if (gemm)
+    e = gemm_products(xq, sx, perm_src, rows, groups, tile, n, entries, slot_base, slot_stride, H, I, h,
+                      reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
+  else
+    e = decode_products(DevItems{n, entries}, groups, xq, sx, perm_src, slot_base, slot_stride, H, I, h, y, s);
   if (e != hipSuccess) return e;
   const dim3 grid(T, (H + 1023) / 1024);
   if (out_bf16)
