@@ -68,6 +68,12 @@ struct RowQuant {
   }
 };
 
+// bf16 of any value: a NaN stays one (f32_to_bf16 takes finite values).
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+  const uint32_t u = __float_as_uint(f);
+  return isnan(f) ? (u >> 16 | 0x40u) : (uint32_t)f32_to_bf16(f);
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
@@ -304,6 +310,23 @@ __global__ __launch_bounds__(256) void pack_int8_kernel(const int8_t* __restrict
   if (r < (size_t)H) reinterpret_cast<float*>(blob + L.p2s)[r] = S2[r];
 }
 
+// The power of two 2^u with |sum * scale * 2^u| <= 2^15 for any codes (|sum| <= 127 * 128 I) and the expert's scales.
+__global__ __launch_bounds__(256) void pack_int8_unit(const float* __restrict__ S2, int H, int I,
+                                                      float* __restrict__ unit) {
+  __shared__ uint32_t wmax[4];
+  uint32_t m = 0;
+  for (int n = threadIdx.x; n < H; n += 256) m = max(m, abs_bits(S2[n]));
+  m = wave_max_u32(m);
+  if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  const float most = __uint_as_float(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]))) * (127.f * 128.f * (float)I);
+  // exponents within what fp32 holds; scales of 0, or not finite, need none
+  int e = 0;
+  if (most > 0.f && most < INFINITY) e = min(max(14 - ilogbf(most), -120), 120);
+  *unit = ldexpf(1.f, e);
+}
+
 // ---------------------------------------------------------------------------
 // Decode: every weight byte is read once, straight from memory into matrix
 // instructions whose other operand holds up to 16 tokens' codes.
@@ -533,13 +556,20 @@ __device__ __forceinline__ size_t h_tile_at(size_t row, int piece, int q, int I)
 // that run together on an XCD share 8 x 4 tiles' operands in its L2.
 constexpr int kGroupN = 4;
 
-template <int PHASE, int BM_T>
+// What a prefill down projection leaves of its rows: fp32 rows of y; or, for a
+// bf16 layer output, fp16 rows (11 bits) in units of their row factor (below),
+// since a token's sum of them is rounded to 8 bits right after: their error is
+// an eighth of that rounding's, and y's traffic, read back by the combine, is
+// as long as the weights' (16384 tokens x 6 of 64 experts: 1.6 GB written and
+// read in fp32).
+template <int PHASE, int BM_T, bool HALF>
 __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
                                                     const int32_t* __restrict__ src, const int32_t* __restrict__ n_entries,
                                                     const int4* __restrict__ entries,
                                                     const char* __restrict__ slot_base, size_t slot_stride,
                                                     size_t mat_off, size_t scale_off, int N, int K, int H, int I,
-                                                    float* __restrict__ hout, float* __restrict__ yout) {
+                                                    float* __restrict__ hout, void* __restrict__ yout,
+                                                    float* __restrict__ factor) {
   constexpr int BN_T = 16;
   constexpr int NS = BM_T == 16 ? 4 : 6;
   constexpr int WN = BM_T == 16 ? 8 : 4;
@@ -679,12 +709,16 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
   }
 
   const float* wscale = reinterpret_cast<const float*>(blob + scale_off);
+  const float unit = (PHASE == 2 && HALF) ? wscale[N] : 1.f;
 #pragma unroll
   for (int j = 0; j < WM; ++j) {
     const int mloc = mt * (16 * BM_T) + (wm * WM + j) * 16 + (lane & 15);
     if (mloc >= it.z) continue;
     const size_t row = (size_t)(it.y + mloc);
-    const float st = bscale[(PHASE == 1 && src) ? (size_t)src[row] : row];
+    const float bs = bscale[(PHASE == 1 && src) ? (size_t)src[row] : row];
+    const float st = (PHASE == 2 && HALF) ? unit : bs;
+    // the row's factor, once (several blocks and lanes of a row store the same)
+    if (PHASE == 2 && HALF && nt == 0 && wn == 0 && lane < 16) factor[row] = bs / unit;
 #pragma unroll
     for (int i = 0; i < WN; ++i) {
       const int ntile = nt * BN_T + wn * WN + i;
@@ -696,8 +730,12 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
       if constexpr (PHASE == 1)
         *reinterpret_cast<float2*>(hout + h_tile_at(row, ntile, lane >> 4, I)) =
             make_float2(silu(v[0]) * v[1], silu(v[2]) * v[3]);
+      else if constexpr (HALF)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(yout) + row * H + 16 * ntile + 4 * (lane >> 4)) =
+            make_uint2(f32_to_f16_bits(v[0]) | (uint32_t)f32_to_f16_bits(v[1]) << 16,
+                       f32_to_f16_bits(v[2]) | (uint32_t)f32_to_f16_bits(v[3]) << 16);
       else
-        *reinterpret_cast<f32x4_t*>(yout + row * H + 16 * ntile + 4 * (lane >> 4)) = v;
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(yout) + row * H + 16 * ntile + 4 * (lane >> 4)) = v;
     }
   }
 }
@@ -760,32 +798,64 @@ __global__ __launch_bounds__(64 * kReqWaves) void requantise_h(const float* __re
   if (wave == 0 && lane < 16) sh[tile * 16 + lane] = rq.scale();
 }
 
-// out[t] = sum over j of w[t, j] y[pos[t, j]], j ascending, over the experts that have a slot.
-template <bool OUT_BF16>
-__global__ __launch_bounds__(256) void int8_combine(const float* __restrict__ y, const int32_t* __restrict__ perm_pos,
+// out[t] = sum over j of w[t, j] y[pos[t, j]], j ascending, over the experts that have a slot. HALF: fp16 rows with a
+// factor each. A thread takes 8 columns, all of a token's rows in flight together (up to kAhead of them).
+constexpr int kAhead = 8;
+template <bool OUT_BF16, bool HALF>
+__global__ __launch_bounds__(256) void int8_combine(const void* __restrict__ y, const float* __restrict__ factor,
+                                                    const int32_t* __restrict__ perm_pos,
                                                     const int32_t* __restrict__ topk_idx,
                                                     const float* __restrict__ topk_w,
                                                     const int32_t* __restrict__ slot_of, int n_slots, int k, int H,
-                                                    void* __restrict__ out) {
-  const size_t t = blockIdx.x;
-  const int n = (blockIdx.y * 256 + threadIdx.x) * 4;
-  if (n >= H) return;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < k; ++j) {
-    const int e = topk_idx[t * k + j];
-    const int slot = slot_of ? slot_of[e] : e;
-    if (slot < 0 || slot >= n_slots) continue;
-    const float wj = topk_w[t * k + j];
-    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(y + (size_t)perm_pos[t * k + j] * H + n);
+                                                    int T, void* __restrict__ out) {
+  const int per = H / 8;  // threads a token; a block may hold several tokens, or a part of one
+  const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t t = id / per;
+  const int n = (int)(id - t * per) * 8;
+  if (t >= (size_t)T) return;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < k; j0 += kAhead) {
+    u32x4_t v[kAhead][HALF ? 1 : 2];
+    float w[kAhead];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = fmaf(wj, v[c], acc[c]);
+    for (int u = 0; u < kAhead; ++u) {
+      w[u] = 0.f;
+#pragma unroll
+      for (int p = 0; p < (HALF ? 1 : 2); ++p) v[u][p] = u32x4_t{0u, 0u, 0u, 0u};
+      if (j0 + u >= k) continue;
+      const int e = topk_idx[t * k + j0 + u];
+      const int slot = slot_of ? slot_of[e] : e;
+      if (slot < 0 || slot >= n_slots) continue;
+      const size_t row = (size_t)perm_pos[t * k + j0 + u];
+      w[u] = topk_w[t * k + j0 + u];
+      if constexpr (HALF) {
+        w[u] *= factor[row];
+        v[u][0] = ld16(static_cast<const uint16_t*>(y) + row * H + n);
+      } else {
+        v[u][0] = ld16(static_cast<const float*>(y) + row * H + n);
+        v[u][1] = ld16(static_cast<const float*>(y) + row * H + n + 4);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (j0 + u < k) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float x = HALF ? f16_bits_to_f32(v[u][0][c >> 1] >> (16 * (c & 1)) & 0xFFFFu)
+                               : __uint_as_float(v[u][HALF ? 0 : c >> 2][c & 3]);
+          acc[c] = fmaf(w[u], x, acc[c]);
+        }
+      }
   }
   if constexpr (OUT_BF16) {
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + t * H + n) =
-        make_uint2((uint32_t)f32_to_bf16(acc[0]) | ((uint32_t)f32_to_bf16(acc[1]) << 16),
-                   (uint32_t)f32_to_bf16(acc[2]) | ((uint32_t)f32_to_bf16(acc[3]) << 16));
+    u32x4_t o;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = bf16_bits(acc[2 * c]) | bf16_bits(acc[2 * c + 1]) << 16;
+    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(out) + t * H + n) = o;
   } else {
-    *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + t * H + n) = acc;
+    float* o = static_cast<float*>(out) + t * H + n;
+    *reinterpret_cast<f32x4_t*>(o) = f32x4_t{acc[0], acc[1], acc[2], acc[3]};
+    *reinterpret_cast<f32x4_t*>(o + 4) = f32x4_t{acc[4], acc[5], acc[6], acc[7]};
   }
 }
 
@@ -834,36 +904,45 @@ hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const fl
 // reads each weight tile twice as often from L2), else 128 (a 96-row group leaves half of a 256-row tile's waves idle).
 int tile_rows_for(int rows, int groups) { return (long long)rows >= 256ll * groups ? 256 : 128; }
 
-// The two products and the pass between them over planned entries (at most rows / tile + groups).
+// The two products and the pass between them over planned entries (at most rows / tile + groups). factor: y's rows are
+// left in fp16 with one each; nullptr: fp32 rows.
 hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src, int rows, int groups, int tile_rows,
                          const int32_t* n, const int4* entries, const char* slot_base, size_t slot_stride, int H, int I,
-                         float* h, uint8_t* hq, float* sh, float* y, hipStream_t s) {
+                         float* h, uint8_t* hq, float* sh, void* y, float* factor, hipStream_t s) {
   const Int8Layout L = int8_layout(H, I);
   const auto grid = [&](int N) { return dim3((unsigned)(((size_t)(rows / tile_rows + groups) * (N / 256) + 7) / 8 * 8)); };
   const auto product = [&](auto kernel, int N, int K, const uint8_t* b, const float* bs, const int32_t* from, size_t mat,
                            size_t scales) {
     hipLaunchKernelGGL(kernel, grid(N), dim3(512), 0, s, b, bs, from, n, entries, slot_base, slot_stride, mat, scales, N,
-                       K, H, I, h, y);
+                       K, H, I, h, y, factor);
     return hipGetLastError();
   };
-  hipError_t e = tile_rows == 256 ? product(int8_gemm<1, 16>, 2 * I, H, xq, sx, src, L.p1, L.p1s)
-                                  : product(int8_gemm<1, 8>, 2 * I, H, xq, sx, src, L.p1, L.p1s);
+  hipError_t e = tile_rows == 256 ? product(int8_gemm<1, 16, false>, 2 * I, H, xq, sx, src, L.p1, L.p1s)
+                                  : product(int8_gemm<1, 8, false>, 2 * I, H, xq, sx, src, L.p1, L.p1s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(requantise_h, dim3((rows + 15) / 16), dim3(64 * kReqWaves), 0, s, h, I, hq, sh);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  return tile_rows == 256 ? product(int8_gemm<2, 16>, H, I, hq, sh, nullptr, L.p2, L.p2s)
-                          : product(int8_gemm<2, 8>, H, I, hq, sh, nullptr, L.p2, L.p2s);
+  if (factor != nullptr)
+    return tile_rows == 256 ? product(int8_gemm<2, 16, true>, H, I, hq, sh, nullptr, L.p2, L.p2s)
+                            : product(int8_gemm<2, 8, true>, H, I, hq, sh, nullptr, L.p2, L.p2s);
+  return tile_rows == 256 ? product(int8_gemm<2, 16, false>, H, I, hq, sh, nullptr, L.p2, L.p2s)
+                          : product(int8_gemm<2, 8, false>, H, I, hq, sh, nullptr, L.p2, L.p2s);
 }
 
 }  // namespace
 
 hipError_t launch_pack_int8(int H, int I, const void* Q1, const void* Q3, const void* Q2, const void* S1,
                             const void* S3, const void* S2, void* blob, hipStream_t s) {
+  const Int8Layout L = int8_layout(H, I);
   const size_t n = (size_t)(2 * I / 16) * (H / 64) * 64 + (size_t)(H / 16) * (I / 64) * 64 + (size_t)2 * I + H;
   hipLaunchKernelGGL(pack_int8_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
                      static_cast<const int8_t*>(Q1), static_cast<const int8_t*>(Q3), static_cast<const int8_t*>(Q2),
                      static_cast<const float*>(S1), static_cast<const float*>(S3), static_cast<const float*>(S2), H, I,
-                     static_cast<char*>(blob), int8_layout(H, I));
+                     static_cast<char*>(blob), L);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(pack_int8_unit, dim3(1), dim3(256), 0, s, static_cast<const float*>(S2), H, I,
+                     reinterpret_cast<float*>(static_cast<char*>(blob) + L.unit));
   return hipGetLastError();
 }
 
@@ -905,7 +984,7 @@ hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const in
       if ((e = hipGetLastError()) == hipSuccess)
         // rows_total: the pass between the products covers every row of the workspace, listed or not
         e = gemm_products(xq, sx, nullptr, rows_total, wa.n, tile, count, entries, slot_base, slot_stride, H, I, h,
-                          reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
+                          reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, nullptr, s);
     }
     if (e != hipSuccess) return e;
   }
@@ -940,6 +1019,8 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   const uint16_t* xb = static_cast<const uint16_t*>(x);
   // Few rows an expert: weights streamed once per 16 rows; else the tiled GEMM where the shape allows it.
   const bool gemm = int8_gemm_supported(H, I) && T > 32;
+  const bool half = gemm && out_bf16;
+  float* factor = half ? h : nullptr;  // over h, which is codes by then
   const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups) : 0;
   int32_t* n = reinterpret_cast<int32_t*>(b + w.plan);
   int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
@@ -948,18 +1029,18 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   if (e != hipSuccess) return e;
   if (gemm)
     e = gemm_products(xq, sx, perm_src, rows, groups, tile, n, entries, slot_base, slot_stride, H, I, h,
-                      reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
+                      reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, factor, s);
   else
     e = decode_products(DevItems{n, entries}, groups, xq, sx, perm_src, slot_base, slot_stride, H, I, h, y, s);
   if (e != hipSuccess) return e;
-  const dim3 grid(T, (H + 1023) / 1024);
-  if (out_bf16)
-    hipLaunchKernelGGL(int8_combine<true>, grid, dim3(256), 0, s, y, perm_pos, topk_idx, topk_w, slot_of, n_slots, k,
-                       H, out);
-  else
-    hipLaunchKernelGGL(int8_combine<false>, grid, dim3(256), 0, s, y, perm_pos, topk_idx, topk_w, slot_of, n_slots, k,
-                       H, out);
-  return hipGetLastError();
+  const dim3 grid((unsigned)(((size_t)T * (H / 8) + 255) / 256));
+  const auto combine = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, y, factor, perm_pos, topk_idx, topk_w, slot_of, n_slots, k, H, T,
+                       out);
+    return hipGetLastError();
+  };
+  if (half) return combine(int8_combine<true, true>);
+  return out_bf16 ? combine(int8_combine<true, false>) : combine(int8_combine<false, false>);
 }
 
 }  // namespace moe

@@ -18,13 +18,16 @@ def expert(H, I, seed, device="cpu"):
     return {k: v.to(device) for k, v in d.items()}
 
 
-def reference(X, w):
+def reference(X, w, half=False):
     """(y, tol) of an expert on rows X in 64 bits. The kernel's h carries fp32 roundings: the integer sum and its two
     scales 3 half steps, g's share through silu at most (1 + |g|) of that again, exp and the quotient and the product
     6 more: below 2^-24 (16 + 2 |g|) relative, 2^-19 for |g| < 8 and 2^-18 for |g| < 24. As code units that is at most
     127 * 2^-18; an h whose 127 h / max|h| lies nearer than that to a half may get either code, which moves y by one
     step of its scale times its weight. Beside that y carries 2^-18 relative of the row's scale and the final
-    products' roundings, over the sum of magnitudes."""
+    products' roundings, over the sum of magnitudes.
+    half: the layer's prefill form keeps rows that go into a bf16 output in fp16, scaled by a power of two u with
+    2^14 <= 127 * 128 I max(s2) u < 2^15: half a step is 2^-11 of y, or of the smallest subnormal 2^-25 / u of the row's
+    scale, at most 2^-39 * 127 * 128 I max(s2) sh."""
     r = oracle.int8_expert(X, *(np64(w[n]) for n in ("q1", "q3", "q2", "s1", "s3", "s2")))
     amax = np.abs(r["h"]).max(1, keepdims=True)
     t = np.abs(r["h"]) * 127.0 / np.where(amax > 0, amax, 1.0)
@@ -32,6 +35,9 @@ def reference(X, w):
     W2 = np.abs(np64(w["q2"])) * np64(w["s2"])[None, :]
     step = r["sh"][:, None]
     tol = (near * step) @ W2 * (1 + 1e-3) + 2.0 ** -17 * (np.abs(r["hq"]) * step) @ W2 + 1e-30
+    if half:
+        I = W2.shape[0]
+        tol = tol + 2.0 ** -11 * (np.abs(r["y"]) + tol) + 2.0 ** -39 * 127 * 128 * I * float(np64(w["s2"]).max()) * step
     return r["y"], tol
 
 

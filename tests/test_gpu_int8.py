@@ -52,8 +52,8 @@ def routing(T, E, k, seed, skew=0.0, never=()):
                          counts=t(counts), offsets=t(offsets)))
 
 
-def expected(x, experts, rt, slot_of, n_slots):
-    """(out, tol) of the layer's expert half in 64 bits, over the experts that have a slot."""
+def expected(x, experts, rt, slot_of, n_slots, half=False):
+    """(out, tol) of the layer's expert half in 64 bits, over the experts that have a slot; half: as in reference()."""
     x64, T, H = np64(x), x.shape[0], x.shape[1]
     out, tol = np.zeros((T, H)), np.zeros((T, H))
     for e, w in enumerate(experts):
@@ -61,7 +61,7 @@ def expected(x, experts, rt, slot_of, n_slots):
         if n == 0 or not 0 <= slot_of[e] < n_slots:
             continue
         rows = rt["src"][rt["offsets"][e]:rt["offsets"][e] + n]
-        y, ty = ic.reference(x64[rows], w)
+        y, ty = ic.reference(x64[rows], w, half)
         wt = np.array([rt["w"][t][list(rt["idx"][t]).index(e)] for t in rows], np.float64)[:, None]
         np.add.at(out, rows, wt * y)
         # the sum of k products in fp32: k roundings of at most the sum of magnitudes
@@ -113,7 +113,7 @@ def test_experts_parity(L, case, bf16):
     x, rt = tokens(T, H, T), routing(T, E, k, T + E, skew)
     out = run(L, x, rt, slots, stride, slot_of, E + 2, H, I, torch.bfloat16 if bf16 else torch.float32)
     torch.cuda.synchronize()
-    ic.check(np64(out), *expected(x, experts, rt, slot_of, E + 2), str(case), bf16)
+    ic.check(np64(out), *expected(x, experts, rt, slot_of, E + 2, half=bf16), str(case), bf16)
 
 
 @pytest.mark.parametrize("T", [5, 200])

@@ -70,7 +70,8 @@ def test_experts_refusals(L):
 
 def test_int8_format_refusals(L):
     f = L.MOE_W_INT8
-    assert L.moe_expert_bytes(f, 4096, 2048) == 3 * 4096 * 2048 + 4 * (2 * 2048 + 4096)
+    least = 3 * 4096 * 2048 + 4 * (2 * 2048 + 4096 + 1)  # codes, scales and one word more
+    assert least <= L.moe_expert_bytes(f, 4096, 2048) < least + 4 * 256
     for H, I in ((32, 64), (64, 32), (16448, 64), (64, 8256), (0, 64)):
         assert L.moe_expert_bytes(f, H, I) == 0
     lib = L._lib
