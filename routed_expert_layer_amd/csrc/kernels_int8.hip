@@ -34,6 +34,13 @@ __device__ __forceinline__ i32x4_t mfma_i8(u32x4_t a, u32x4_t b, i32x4_t c) {
                                                0);
 }
 
+// silu(g) u for g, u a few roundings off already: the hardware's exponential and
+// reciprocal (a step each) add 1.5 |g| + 5 half steps (the exponent's argument
+// carries |g| of them), which is below what g's own error does to it.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
 // ---------------------------------------------------------------------------
 // Codes of a row.
 // ---------------------------------------------------------------------------
@@ -419,7 +426,7 @@ __global__ __launch_bounds__(256) void int8_decode_up(const uint8_t* __restrict_
       const float g0 = (float)s[0] * (st * sw[0]), u0 = (float)s[1] * (st * sw[1]);
       const float g1 = (float)s[2] * (st * sw[2]), u1 = (float)s[3] * (st * sw[3]);
       *reinterpret_cast<float2*>(h + (size_t)r * I + 8 * tile + 2 * (lane >> 4)) =
-          make_float2(silu(g0) * u0, silu(g1) * u1);
+          make_float2(swiglu(g0, u0), swiglu(g1, u1));
     }
     __syncthreads();
   }
@@ -710,26 +717,37 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
 
   const float* wscale = reinterpret_cast<const float*>(blob + scale_off);
   const float unit = (PHASE == 2 && HALF) ? wscale[N] : 1.f;
+  // every scale first, so that their loads are in flight together
+  f32x4_t sw[WN];
+#pragma unroll
+  for (int i = 0; i < WN; ++i)
+    sw[i] = *reinterpret_cast<const f32x4_t*>(wscale + 16 * (nt * BN_T + wn * WN + i) + 4 * (lane >> 4));
+  float st[WM];
+#pragma unroll
+  for (int j = 0; j < WM; ++j) {
+    const int mloc = mt * (16 * BM_T) + (wm * WM + j) * 16 + (lane & 15);
+    const size_t row = (size_t)(it.y + min(mloc, it.z - 1));
+    st[j] = bscale[(PHASE == 1 && src) ? (size_t)src[row] : row];
+    if constexpr (PHASE == 2 && HALF) {
+      if (mloc < it.z && nt == 0 && wn == 0 && lane < 16) factor[row] = st[j] / unit;  // once a row
+      st[j] = unit;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < WM; ++j) {
     const int mloc = mt * (16 * BM_T) + (wm * WM + j) * 16 + (lane & 15);
     if (mloc >= it.z) continue;
     const size_t row = (size_t)(it.y + mloc);
-    const float bs = bscale[(PHASE == 1 && src) ? (size_t)src[row] : row];
-    const float st = (PHASE == 2 && HALF) ? unit : bs;
-    // the row's factor, once (several blocks and lanes of a row store the same)
-    if (PHASE == 2 && HALF && nt == 0 && wn == 0 && lane < 16) factor[row] = bs / unit;
 #pragma unroll
     for (int i = 0; i < WN; ++i) {
       const int ntile = nt * BN_T + wn * WN + i;
       const i32x4_t s = acc[i][j];
-      const f32x4_t sw = *reinterpret_cast<const f32x4_t*>(wscale + 16 * ntile + 4 * (lane >> 4));
       f32x4_t v;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = (float)s[c] * (st * sw[c]);
+      for (int c = 0; c < 4; ++c) v[c] = (float)s[c] * (st[j] * sw[i][c]);
       if constexpr (PHASE == 1)
         *reinterpret_cast<float2*>(hout + h_tile_at(row, ntile, lane >> 4, I)) =
-            make_float2(silu(v[0]) * v[1], silu(v[2]) * v[3]);
+            make_float2(swiglu(v[0], v[1]), swiglu(v[2], v[3]));
       else if constexpr (HALF)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(yout) + row * H + 16 * ntile + 4 * (lane >> 4)) =
             make_uint2(f32_to_f16_bits(v[0]) | (uint32_t)f32_to_f16_bits(v[1]) << 16,
@@ -801,7 +819,7 @@ __global__ __launch_bounds__(64 * kReqWaves) void requantise_h(const float* __re
 // out[t] = sum over j of w[t, j] y[pos[t, j]], j ascending, over the experts that have a slot. HALF: fp16 rows with a
 // factor each. A thread takes 8 columns, all of a token's rows in flight together (up to kAhead of them).
 constexpr int kAhead = 8;
-template <bool OUT_BF16, bool HALF>
+template <bool OUT_BF16, bool HALF, bool UNIFORM>
 __global__ __launch_bounds__(256) void int8_combine(const void* __restrict__ y, const float* __restrict__ factor,
                                                     const int32_t* __restrict__ perm_pos,
                                                     const int32_t* __restrict__ topk_idx,
@@ -810,8 +828,9 @@ __global__ __launch_bounds__(256) void int8_combine(const void* __restrict__ y, 
                                                     int T, void* __restrict__ out) {
   const int per = H / 8;  // threads a token; a block may hold several tokens, or a part of one
   const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
-  const size_t t = id / per;
+  size_t t = id / per;
   const int n = (int)(id - t * per) * 8;
+  if constexpr (UNIFORM) t = (size_t)__builtin_amdgcn_readfirstlane((int)t);  // a wave is within one token: scalar loads
   if (t >= (size_t)T) return;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 < k; j0 += kAhead) {
@@ -1039,8 +1058,8 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
                        out);
     return hipGetLastError();
   };
-  if (half) return combine(int8_combine<true, true>);
-  return out_bf16 ? combine(int8_combine<true, false>) : combine(int8_combine<false, false>);
+  if (half) return H % 512 == 0 ? combine(int8_combine<true, true, true>) : combine(int8_combine<true, true, false>);
+  return out_bf16 ? combine(int8_combine<true, false, false>) : combine(int8_combine<false, false, false>);
 }
 
 }  // namespace moe
