@@ -423,6 +423,9 @@ int moe_ffn_grouped(const void* x, int dtype, const int32_t* perm_src, const int
  *   workspace device scratch, >= moe_experts_workspace_size(...) bytes
  * x, slots, out and workspace 16-byte aligned. Limits: E <= 1024; the codes of
  * the tokens and of the T*k rows within 4 GiB each.
+ * With a bf16 `out` the rows of more than 32 tokens (where the shape runs the
+ * tiled GEMM) are kept in 11 bits before the sum; a column whose channel scale
+ * s2 is below 2^-20 of its expert's largest keeps fewer.
  * Errors: MOE_EINVAL (null, sizes, formats, alignment), MOE_EHIP.
  * ------------------------------------------------------------------------ */
 size_t moe_experts_workspace_size(int T, int k, int E, int H, int I, int wfmt);
@@ -538,8 +541,8 @@ int moe_clock_record(unsigned long long* sums);
  *   owns, for their expert's gate/up blocks (so one decoder's steps must
  *   stay ordered on one stream).
  *   out_dtype other than MOE_DT_F32 / MOE_DT_BF16 is MOE_EINVAL.
- *   int8 experts (bf16 activations) run their two projections as two launches
- *   behind the quantisation of the step's tokens.
+ *   int8 experts (bf16 activations, 16-byte aligned) run their two projections
+ *   as two launches behind the quantisation of the step's tokens.
  *   When the cache splits misses (moe_cache_set_split), the misses assigned
  *   to the CPU run with moe_cpu_ffn from the pool on the calling thread while
  *   the GPU works on the others (bf16 activations with bf16, int4 or MXFP4

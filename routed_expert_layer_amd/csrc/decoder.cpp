@@ -276,6 +276,8 @@ static int update_slot_table(moe_decoder_t* d, int layer, int n, int nm, hipStre
 int moe_decoder_step(moe_decoder_t* d, int step, int layer, const void* x, int T, const void* Wr, const float* bias,
                      void* out, int out_dtype, void* stream, int* n_miss) {
   if (!d || !x || !Wr || !out) return dfail(MOE_EINVAL, "moe_decoder_step: null argument");
+  if (d->wfmt == MOE_W_INT8 && !moe::aligned16(x))
+    return dfail(MOE_EINVAL, "moe_decoder_step: int8 experts need 16-byte aligned activations");
   if (T < 1 || T > d->Tmax) return dfail(MOE_EINVAL, "moe_decoder_step: T=%d outside [1, %d]", T, d->Tmax);
   if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16)
     return dfail(MOE_EINVAL, "moe_decoder_step: out_dtype %d is neither MOE_DT_F32 nor MOE_DT_BF16", out_dtype);

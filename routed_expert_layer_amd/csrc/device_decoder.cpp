@@ -178,6 +178,8 @@ int moe_device_decoder_destroy(moe_device_decoder_t* d) {
 int moe_device_decoder_step(moe_device_decoder_t* d, int layer, const void* x, int T, const void* Wr,
                             const float* bias, void* out, int out_dtype, void* stream) {
   if (!d || !x || !Wr || !out) return dd_fail(MOE_EINVAL, "moe_device_decoder_step: null argument");
+  if (d->wfmt == MOE_W_INT8 && !moe::aligned16(x))
+    return dd_fail(MOE_EINVAL, "moe_device_decoder_step: int8 experts need 16-byte aligned activations");
   if (T < 1 || T > d->Tmax) return dd_fail(MOE_EINVAL, "moe_device_decoder_step: T=%d outside [1, %d]", T, d->Tmax);
   if (layer < 0 || layer >= d->L) return dd_fail(MOE_EINVAL, "moe_device_decoder_step: layer %d out of range", layer);
   if (out_dtype != MOE_DT_F32 && out_dtype != MOE_DT_BF16)

@@ -1,7 +1,6 @@
-// What the prefill GEMM kernels share: wait counts, direct-to-LDS loads and the super-tile shapes.
+// What the prefill GEMM kernels share: wait counts and direct-to-LDS loads.
 #pragma once
 #include "dev_common.hpp"
-#include "moe_kernels.hpp"
 
 namespace moe {
 namespace {
@@ -20,26 +19,6 @@ __device__ __forceinline__ void buffer_load_lds16(const void* base, uint32_t off
   const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, -1, 0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, 0, 0, 0);
 }
-
-// Per expert, a super-tile is GM token tiles x GN weight tiles (GM*GN <= 32
-// block slots): GM = the smallest power of two covering its token tiles, at
-// most 8; GN = the largest power of two dividing the weight tiles that fits
-// beside it. Super-tiles per expert: ceil(m tiles / GM) x (n tiles / GN).
-// Returns that count for a group of `rows` rows (0 for none) and sets
-// shape = GM | GN << 8. Host planner and device planner use the same rule.
-__host__ __device__ inline int supertiles_of(int rows, int N, int tile_tokens, int& shape) {
-  const int NTB = N / 256;
-  int gn_div = 1;
-  while (gn_div < 16 && NTB % (gn_div * 2) == 0) gn_div *= 2;
-  const int mtiles = (rows + tile_tokens - 1) / tile_tokens;
-  int GM = 8;
-  while (GM > 1 && GM / 2 >= mtiles) GM /= 2;
-  const int GN = (32 / GM) < gn_div ? 32 / GM : gn_div;
-  shape = GM | (GN << 8);
-  return rows > 0 ? (mtiles + GM - 1) / GM * (NTB / GN) : 0;
-}
-
-inline int supertile_blocks(int tot) { return (tot + 7) / 8 * 256; }  // 8 XCDs x 32 slots per round
 
 }  // namespace
 }  // namespace moe

@@ -501,6 +501,24 @@ __global__ __launch_bounds__(512, 1) void gemm_mxfp4(const uint16_t* __restrict_
   }
 }
 
+// Per expert, a super-tile is GM token tiles x GN weight tiles (GM*GN <= 32
+// block slots): GM = the smallest power of two covering its token tiles, at
+// most 8; GN = the largest power of two dividing the weight tiles that fits
+// beside it. Super-tiles per expert: ceil(m tiles / GM) x (n tiles / GN).
+// Returns that count for a group of `rows` rows (0 for none) and sets
+// shape = GM | GN << 8. Host planner and device planner use the same rule.
+__host__ __device__ inline int supertiles_of(int rows, int N, int tile_tokens, int& shape) {
+  const int NTB = N / 256;
+  int gn_div = 1;
+  while (gn_div < 16 && NTB % (gn_div * 2) == 0) gn_div *= 2;
+  const int mtiles = (rows + tile_tokens - 1) / tile_tokens;
+  int GM = 8;
+  while (GM > 1 && GM / 2 >= mtiles) GM /= 2;
+  const int GN = (32 / GM) < gn_div ? 32 / GM : gn_div;
+  shape = GM | (GN << 8);
+  return rows > 0 ? (mtiles + GM - 1) / GM * (NTB / GN) : 0;
+}
+
 // Fills item[i].w with GM | GN << 8 and tile_prefix; returns the total.
 int plan_supertiles(int4* item, int n, int* tile_prefix, int N, int tile_tokens) {
   int tot = 0;
@@ -513,6 +531,8 @@ int plan_supertiles(int4* item, int n, int* tile_prefix, int N, int tile_tokens)
   tile_prefix[n] = tot;
   return tot;
 }
+
+inline int supertile_blocks(int tot) { return (tot + 7) / 8 * 256; }  // 8 XCDs x 32 slots per round
 
 // Up to 64 entries of both projections' tables per upload launch: the two
 // share the items' slot and rows and differ in the super-tile shape (item.w)
@@ -656,19 +676,6 @@ __global__ __launch_bounds__(1024) void plan_tables_kernel(const int32_t* __rest
 
 bool gemm2_supported(int N, int K) { return N % 256 == 0 && K % 32 == 0; }
 
-hipError_t plan_gemm_tables(const int4* items, int n, int H, int I, int tile_tokens, GemmTable* t1, GemmTable* t2,
-                            int (&tot)[2], hipStream_t s) {
-  return plan_and_upload(items, n, H, I, tile_tokens, t1, t2, tot, s);
-}
-
-hipError_t launch_plan_tables(const int32_t* counts, const int32_t* offsets, const int32_t* slot_of, int E,
-                              int n_slots, int rows_max, int N1, int N2, int split, int tt0, int tt1, void* tables,
-                              hipStream_t s) {
-  hipLaunchKernelGGL(plan_tables_kernel, dim3(1), dim3((E + 63) / 64 * 64), 0, s, counts, offsets, slot_of, E,
-                     n_slots, rows_max, N1, N2, split, tt0, tt1, static_cast<char*>(tables));
-  return hipGetLastError();
-}
-
 void set_clock_sums(unsigned long long* sums) { g_clock_sums = sums; }
 
 // Both projections of every listed expert: groups of more than 256 rows with
@@ -759,8 +766,9 @@ hipError_t launch_ffn_grouped(int wfmt, const void* x, const int32_t* perm_src, 
   if (E < 1 || E > kTableItems || !grouped_supported(wfmt, H, I)) return hipErrorInvalidValue;
   const bool mx = wfmt == 3;
   char* tb = static_cast<char*>(tables);
-  hipError_t e = launch_plan_tables(counts, offsets, slot_of, E, n_slots, rows_max, 2 * I, H, mx ? 0 : 256,
-                                    mx ? 128 : 256, 128, tb, s);
+  hipLaunchKernelGGL(plan_tables_kernel, dim3(1), dim3((E + 63) / 64 * 64), 0, s, counts, offsets, slot_of, E,
+                     n_slots, rows_max, 2 * I, H, mx ? 0 : 256, mx ? 128 : 256, 128, tb);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const GemmTable* tab[2][2];
   for (int p = 0; p < 2; ++p)

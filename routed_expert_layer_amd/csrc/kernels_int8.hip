@@ -166,17 +166,18 @@ struct DevItems {
 //   else: prefill, an entry for each tile of tile_rows rows, and their number.
 //     Up to kSuper tiles of a group make a super-row; an entry is {slot, first
 //     row of the super-row, its rows, tiles in it | this one's index << 8}.
+// At most `cap` are written, however the counts overlap.
 constexpr int kSuper = 8;
 struct Plan {
   const int32_t *counts, *offsets, *slot_of;
-  int E, n_slots, rows_max, tile_rows;
+  int E, n_slots, rows_max, tile_rows, cap;
   int32_t* n;  // nullptr: no plan
   int4* items;
 };
 
 // Thread's group `it` of a list of 256 (`base` entries before it); returns the new number of entries. E, lds: LDS.
-__device__ __forceinline__ int plan_groups(int4 it, bool ok, int base, int tile_rows, int4* items, int (*lds)[256],
-                                           int4* group) {
+__device__ __forceinline__ int plan_groups(int4 it, bool ok, int base, int tile_rows, int cap, int4* items,
+                                           int (*lds)[256], int4* group) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int mine = !ok ? 0 : tile_rows ? (it.z + tile_rows - 1) / tile_rows : 1;
   int x = mine;
@@ -195,7 +196,7 @@ __device__ __forceinline__ int plan_groups(int4 it, bool ok, int base, int tile_
   lds[1][tid] = before + x;  // inclusive
   group[tid] = it;
   __syncthreads();
-  for (int q = tid; q < all; q += 256) {
+  for (int q = tid; q < min(all, cap - base); q += 256) {
     int lo = 0, hi = 255;  // the group of entry q: the first whose inclusive count is above q
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
@@ -211,7 +212,7 @@ __device__ __forceinline__ int plan_groups(int4 it, bool ok, int base, int tile_
     items[base + q] = e;
   }
   __syncthreads();
-  return base + all;
+  return min(base + all, cap);
 }
 
 __device__ __forceinline__ void run_plan(const Plan& p) {
@@ -228,18 +229,18 @@ __device__ __forceinline__ void run_plan(const Plan& p) {
       it.x = p.slot_of ? p.slot_of[e] : e;
       ok = it.z > 0 && it.y >= 0 && (long long)it.y + it.z <= p.rows_max && it.x >= 0 && it.x < p.n_slots;
     }
-    base = plan_groups(it, ok, base, p.tile_rows, p.items, lds, group);
+    base = plan_groups(it, ok, base, p.tile_rows, p.cap, p.items, lds, group);
   }
   if (threadIdx.x == 0) *p.n = base;
 }
 
 // Prefill entries of up to kMaxItems groups listed on the host.
-__global__ __launch_bounds__(256) void plan_list(const ArgItems wk, int tile_rows, int32_t* __restrict__ n,
+__global__ __launch_bounds__(256) void plan_list(const ArgItems wk, int tile_rows, int cap, int32_t* __restrict__ n,
                                                  int4* __restrict__ items) {
   __shared__ int lds[2][256];
   __shared__ int4 group[256];
   const bool ok = (int)threadIdx.x < wk.wa.n;
-  const int all = plan_groups(ok ? wk.wa.item[threadIdx.x] : make_int4(0, 0, 0, 0), ok, 0, tile_rows, items, lds, group);
+  const int all = plan_groups(ok ? wk.wa.item[threadIdx.x] : make_int4(0, 0, 0, 0), ok, 0, tile_rows, cap, items, lds, group);
   if (threadIdx.x == 0) *n = all;
 }
 
@@ -327,10 +328,13 @@ __global__ __launch_bounds__(256) void pack_int8_unit(const float* __restrict__ 
   if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  const float most = __uint_as_float(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]))) * (127.f * 128.f * (float)I);
+  const float most = __uint_as_float(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
   // exponents within what fp32 holds; scales of 0, or not finite, need none
   int e = 0;
-  if (most > 0.f && most < INFINITY) e = min(max(14 - ilogbf(most), -120), 120);
+  if (most > 0.f && most < INFINITY) {
+    const int m = ilogbf(most);
+    e = min(max(14 - m - ilogbf(ldexpf(most, -m) * (127.f * 128.f * (float)I)), -126), 126);
+  }
   *unit = ldexpf(1.f, e);
 }
 
@@ -445,42 +449,44 @@ __device__ __forceinline__ void put_h_codes(char* lds, int m, int col, const Row
 
 // The codes of rows [r0, r0 + n) of h (n <= 16) into LDS by a block of 256
 // threads: a row's maximum over the block, then its codes, kQuantRows rows at a
-// time in registers (rows of up to 2048; longer ones are read twice). Columns
+// time in registers (rows of up to 1024 P; longer ones are read twice). Columns
 // of rows past n are left as they are: they are other tokens' columns of the
 // products, which are not stored. mx: LDS of 16 x 4 words.
 constexpr int kQuantRows = 4;
+template <int P>
 __device__ __forceinline__ void quantise_h_rows(const float* __restrict__ h, int r0, int n, int I, char* lds,
                                                 float* scales, uint32_t (*mx)[4]) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (int m0 = 0; m0 < n; m0 += kQuantRows) {
-    f32x4_t v[kQuantRows][2];
+    f32x4_t v[kQuantRows][P];
 #pragma unroll
     for (int r = 0; r < kQuantRows; ++r) {
-      const float* row = h + (size_t)(r0 + min(m0 + r, n - 1)) * I;
+      const float* row = h + (size_t)(r0 + m0 + r) * I;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
+      for (int p = 0; p < P; ++p) {
         const int i = 4 * tid + 1024 * p;
         v[r][p] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        if (i < I) v[r][p] = *reinterpret_cast<const f32x4_t*>(row + i);
+        if (m0 + r < n && i < I) v[r][p] = *reinterpret_cast<const f32x4_t*>(row + i);
       }
     }
 #pragma unroll
     for (int r = 0; r < kQuantRows; ++r) {
+      if (m0 + r >= n) break;
       uint32_t m = 0;
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int w = 0; w < 4; ++w) m = max(m, abs_bits(v[r][p][w]));
-      if (I > 2048) {
-        const float* row = h + (size_t)(r0 + min(m0 + r, n - 1)) * I;
-        for (int i = 4 * tid + 2048; i < I; i += 1024) {
+      if (I > 1024 * P) {
+        const float* row = h + (size_t)(r0 + m0 + r) * I;
+        for (int i = 4 * tid + 1024 * P; i < I; i += 1024) {
           const f32x4_t q = *reinterpret_cast<const f32x4_t*>(row + i);
 #pragma unroll
           for (int w = 0; w < 4; ++w) m = max(m, abs_bits(q[w]));
         }
       }
       m = wave_max_u32(m);
-      if (lane == 0 && m0 + r < n) mx[m0 + r][wave] = m;
+      if (lane == 0) mx[m0 + r][wave] = m;
     }
     __syncthreads();
 #pragma unroll
@@ -488,11 +494,11 @@ __device__ __forceinline__ void quantise_h_rows(const float* __restrict__ h, int
       if (m0 + r >= n) break;
       const RowQuant rq(max(max(mx[m0 + r][0], mx[m0 + r][1]), max(mx[m0 + r][2], mx[m0 + r][3])));
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < P; ++p)
         if (4 * tid + 1024 * p < I) put_h_codes(lds, m0 + r, 4 * tid + 1024 * p, rq, v[r][p]);
-      if (I > 2048) {
+      if (I > 1024 * P) {
         const float* row = h + (size_t)(r0 + m0 + r) * I;
-        for (int i = 4 * tid + 2048; i < I; i += 1024)
+        for (int i = 4 * tid + 1024 * P; i < I; i += 1024)
           put_h_codes(lds, m0 + r, i, rq, *reinterpret_cast<const f32x4_t*>(row + i));
       }
       if (tid == 0) scales[m0 + r] = rq.scale();
@@ -523,7 +529,7 @@ __global__ __launch_bounds__(256) void int8_decode_down(const float* __restrict_
   __shared__ float sh[16];
   __shared__ uint32_t mx[16][4];
   for (int m0 = 0; m0 < it.z; m0 += 16) {
-    quantise_h_rows(h, it.y + m0, min(16, it.z - m0), I, codes, sh, mx);
+    quantise_h_rows<(NF > 4 ? 2 : 1)>(h, it.y + m0, min(16, it.z - m0), I, codes, sh, mx);
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < R; ++t)
@@ -563,6 +569,9 @@ __device__ __forceinline__ size_t h_tile_at(size_t row, int piece, int q, int I)
 // that run together on an XCD share 8 x 4 tiles' operands in its L2.
 constexpr int kGroupN = 4;
 
+// PHASE 1: gate/up from tokens' codes (rows through src) to h, tiled as above.
+// PHASE 2: the down projection from h's codes to y.
+//
 // What a prefill down projection leaves of its rows: fp32 rows of y; or, for a
 // bf16 layer output, fp16 rows (11 bits) in units of their row factor (below),
 // since a token's sum of them is rounded to 8 bits right after: their error is
@@ -999,7 +1008,7 @@ hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const in
       const int tile = tile_rows_for(rows, wa.n);
       int32_t* count = reinterpret_cast<int32_t*>(b + w.plan);
       int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
-      hipLaunchKernelGGL(plan_list, dim3(1), dim3(256), 0, s, wk, tile, count, entries);
+      hipLaunchKernelGGL(plan_list, dim3(1), dim3(256), 0, s, wk, tile, w.entries, count, entries);
       if ((e = hipGetLastError()) == hipSuccess)
         // rows_total: the pass between the products covers every row of the workspace, listed or not
         e = gemm_products(xq, sx, nullptr, rows_total, wa.n, tile, count, entries, slot_base, slot_stride, H, I, h,
@@ -1044,7 +1053,7 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   int32_t* n = reinterpret_cast<int32_t*>(b + w.plan);
   int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
   hipError_t e = launch_quantise_tokens(xb, T, H, xq, sx,
-                                        Plan{counts, offsets, slot_of, E, n_slots, rows, tile, n, entries}, s);
+                                        Plan{counts, offsets, slot_of, E, n_slots, rows, tile, w.entries, n, entries}, s);
   if (e != hipSuccess) return e;
   if (gemm)
     e = gemm_products(xq, sx, perm_src, rows, groups, tile, n, entries, slot_base, slot_stride, H, I, h,

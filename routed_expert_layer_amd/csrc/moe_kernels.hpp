@@ -270,14 +270,6 @@ hipError_t launch_ffn_grouped(int wfmt, const void* x, const int32_t* perm_src, 
                               const int32_t* offsets, const int32_t* slot_of, int E, int n_slots, int rows_max,
                               const char* slot_base, size_t slot_stride, int H, int I, void* hbuf, float* y,
                               void* tables, hipStream_t s);
-// The planners of those work lists alone: the host planner's tables of n items (gate/up N = 2I, down N = H, tiles of
-// tile_tokens rows; tot receives the super-tile counts), and the device planner's four tables (groups of more than
-// `split` rows in part 0, tiles of tt0 rows, the others in part 1, tiles of tt1; projections of N1 and N2 columns).
-hipError_t plan_gemm_tables(const int4* items, int n, int H, int I, int tile_tokens, GemmTable* t1, GemmTable* t2,
-                            int (&tot)[2], hipStream_t s);
-hipError_t launch_plan_tables(const int32_t* counts, const int32_t* offsets, const int32_t* slot_of, int E,
-                              int n_slots, int rows_max, int N1, int N2, int split, int tt0, int tt1, void* tables,
-                              hipStream_t s);
 int router_gemm2_splits(int T, int H, int E);
 hipError_t launch_router_gemm2(const void* x, const void* wrt, int T, int H, int E, float* partial, int nsplit,
                                hipStream_t s);

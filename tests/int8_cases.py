@@ -20,9 +20,9 @@ def expert(H, I, seed, device="cpu"):
 
 def reference(X, w, half=False):
     """(y, tol) of an expert on rows X in 64 bits. The kernel's h carries fp32 roundings: the integer sum and its two
-    scales 3 half steps, g's share through silu at most (1 + |g|) of that again, exp and the quotient and the product
-    6 more: below 2^-24 (16 + 2 |g|) relative, 2^-19 for |g| < 8 and 2^-18 for |g| < 24. As code units that is at most
-    127 * 2^-18; an h whose 127 h / max|h| lies nearer than that to a half may get either code, which moves y by one
+    scales 3 half steps (of 2^-24) for u and for g, g's share through silu at most (1 + |g|) times that; the exponential's
+    argument in base 2 |g| + 1.5 more, it and the reciprocal a step each, the sum and the two products 3: below
+    13 + 4.5 |g| half steps, 2^-18 relative for |g| < 11. As code units that is at most 127 * 2^-18; an h whose 127 h / max|h| lies nearer than that to a half may get either code, which moves y by one
     step of its scale times its weight. Beside that y carries 2^-18 relative of the row's scale and the final
     products' roundings, over the sum of magnitudes.
     half: the layer's prefill form keeps rows that go into a bf16 output in fp16, scaled by a power of two u with

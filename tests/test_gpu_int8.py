@@ -330,3 +330,105 @@ def test_prefill_layer_with_int8_experts(L, T, H, I, gated):
     # moe_route's weights carry fp32 exponentials: 1e-5, as the routing tests allow
     ic.check(np64(out), ref, tol + (1e-5 * cfg.k * np.abs(ref).max() if not gated else 2.0 ** -22 * np.abs(ref).max()),
              "int8 prefill layer")
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(3, 2, 2, 64, 8192), (17, 2, 1, 4160, 64), (5, 3, 2, 8256, 128), (2, 2, 1, 16384, 64),
+                                       (40, 2, 1, 16384, 128), (40, 3, 2, 256, 8192), (40, 24, 12, 256, 128)])
+@pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
+def test_experts_widest_shapes(L, T, E, k, H, I, bf16):
+    """The largest H and I, and choices of more experts than the combine has in flight."""
+    experts = [ic.expert(H, I, e + I, dev) for e in range(E)]
+    slots, stride = pack(L, H, I, experts, range(E), E)
+    x, rt = tokens(T, H, T), routing(T, E, k, H)
+    out = run(L, x, rt, slots, stride, None, E, H, I, torch.bfloat16 if bf16 else torch.float32)
+    torch.cuda.synchronize()
+    ic.check(np64(out), *expected(x, experts, rt, range(E), E, half=bf16), f"{H}x{I}", bf16)
+
+
+@pytest.mark.parametrize("T", [4, 50])
+def test_experts_same_expert_twice(L, T):
+    """A choice that names an expert twice has a row for each, weighted by its own weight."""
+    E, k, H, I = 4, 3, 256, 128
+    experts = [ic.expert(H, I, e, dev) for e in range(E)]
+    slots, stride = pack(L, H, I, experts, range(E), E)
+    x, r = tokens(T, H, 3), np.random.default_rng(T)
+    idx = r.integers(0, E, (T, k))
+    idx[0] = 2
+    w = r.random((T, k)).astype(np.float32)
+    order = np.argsort(idx.reshape(-1), kind="stable")
+    pos = np.empty(T * k, np.int64)
+    pos[order] = np.arange(T * k)
+    counts = np.bincount(idx.reshape(-1), minlength=E)
+    t = lambda a, d=torch.int32: torch.from_numpy(np.ascontiguousarray(a)).to(d).to(dev)  # noqa: E731
+    rt = dict(idx=idx, counts=counts,
+              dev=dict(topk_idx=t(idx), topk_w=t(w, torch.float32), perm_src=t(order // k), perm_pos=t(pos.reshape(T, k)),
+                       counts=t(counts), offsets=t(np.concatenate([[0], np.cumsum(counts)]))))
+    out = run(L, x, rt, slots, stride, None, E, H, I)
+    torch.cuda.synchronize()
+    ys = [ic.reference(np64(x), e) for e in experts]
+    y, tol = np.zeros((T, H)), np.zeros((T, H))
+    for j in range(k):
+        yj = np.stack([ys[idx[a, j]][0][a] for a in range(T)])
+        wj = w[:, j:j + 1].astype(np.float64)
+        y += wj * yj
+        tol += wj * np.stack([ys[idx[a, j]][1][a] for a in range(T)]) + k * 2.0 ** -23 * wj * np.abs(yj)
+    ic.check(np64(out), y, tol, "twice")
+
+
+def test_experts_two_streams_at_once(L):
+    """Decode and prefill sizes on two streams together, each with its own workspace, equal the same calls alone."""
+    E, k, H, I = 8, 2, 512, 256
+    experts = [ic.expert(H, I, e, dev) for e in range(E)]
+    slots, stride = pack(L, H, I, experts, range(E), E)
+    calls = [[(tokens(T, H, T + q), routing(T, E, k, T + q)) for T in (1, 300, 16, 40)] for q in range(2)]
+    alone = [[run(L, x, rt, slots, stride, None, E, H, I) for x, rt in q] for q in calls]
+    size = L.moe_experts_workspace_size(300, k, E, H, I, L.MOE_W_INT8)
+    ws = [torch.full((size,), 255, dtype=torch.uint8, device=dev) for _ in range(2)]
+    outs = [[torch.full_like(o, float("nan")) for o in q] for q in alone]
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for q in range(2):
+            x, rt = calls[q][i]
+            run(L, x, rt, slots, stride, None, E, H, I, ws=ws[q], out=outs[q][i], stream=ss[q])
+    torch.cuda.synchronize()
+    for q in range(2):
+        for i in range(4):
+            assert torch.equal(outs[q][i], alone[q][i]), (q, i)
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+def test_ffn_list_of_many_experts(L, mode):
+    """More items than one launch takes, some of them in slots shared, and tiles of 256 rows."""
+    H, I, E = 256, 128, 3
+    rows = [1 + (5 * i) % 9 for i in range(64)] + ([300, 520] if mode == "prefill" else [30]) + [2] * 5
+    experts = [ic.expert(H, I, e, dev) for e in range(E)]
+    slots, stride = pack(L, H, I, experts, range(E), E)
+    total, T = sum(rows), 50
+    x = tokens(T, H, 1)
+    src = np.random.default_rng(2).integers(0, T, size=total).astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(rows)])
+    work = np.array([[i % E, i % E, off[i], n] for i, n in enumerate(rows)], np.int32)
+    y = torch.full((total, H), float("nan"), device=dev)
+    ws = torch.full((L.moe_ffn_workspace_size(total, H, I, L.MOE_W_INT8),), 255, dtype=torch.uint8, device=dev)
+    L.moe_ffn(x, torch.from_numpy(src).to(dev), work, slots, stride, L.MOE_W_INT8, H, I, y, ws,
+              L.MOE_FFN_DECODE if mode == "decode" else L.MOE_FFN_PREFILL)
+    torch.cuda.synchronize()
+    yg, x64 = np64(y), np64(x)
+    for i, n in enumerate(rows):
+        ic.check(yg[off[i]:off[i] + n], *ic.reference(x64[src[off[i]:off[i] + n]], experts[i % E]), f"item {i}")
+
+
+def test_decoders_refuse_unaligned_tokens(L):
+    from routed_expert_layer_amd.runtime import DecodeLayer, DeviceDecodeLayer, ExpertStore
+    cfg = int8_config(L=1)
+    store = ExpertStore(1, cfg.E, cfg.H, cfg.I, "int8")
+    try:
+        W, b = gen.router_weight(cfg, 0, dev), torch.zeros(cfg.E, device=dev)
+        x = torch.zeros(cfg.T * cfg.H + 1, dtype=torch.bfloat16, device=dev)[1:].view(cfg.T, cfg.H)
+        with pytest.raises(L.MoEError, match="16-byte"):
+            DecodeLayer(store, cfg.S, cfg.T, cfg.k, "bf16", dev).step(0, 0, x, W, b)
+        with pytest.raises(L.MoEError, match="16-byte"):
+            DeviceDecodeLayer(store, cfg.S, cfg.T, cfg.k, "bf16", dev).step(0, x, W, b)
+    finally:
+        store.close()

@@ -277,3 +277,34 @@ def test_prefill_layer_under_a_gate(L):
     ge = ExpertCache64(cfg, 0)
     check_close(np64(out), oracle.combine(oracle.expert_outputs(np64(x), off, src, lambda e: ge(int(e))), pos, w),
                 "gated prefill layer")
+
+
+@pytest.mark.parametrize("T,E,k,G,keep", [(3, 1023, 5, 33, 7), (70, 1023, 16, 33, 7), (5000, 512, 8, 1, 1), (16384, 48, 2, 1, 1),
+                                          (16385, 96, 6, 8, 3), (16500, 512, 4, 4, 2), (16400, 1023, 3, 33, 9)])
+def test_select_long_and_wide(L, T, E, k, G, keep):
+    """Past the batches that two launches group, and the shapes with most experts a lane."""
+    g = torch.Generator(device=dev).manual_seed(T + E)
+    l = torch.randn((T, E), generator=g, device=dev) * 1.5
+    kw = dict(score="sigmoid", n_group=G, topk_group=keep, group_top=2, scale=2.0,
+              balance=0.2 * torch.randn(E, generator=g, device=dev))
+    o = select(L, l, L.Gate(**kw), k)
+    torch.cuda.synchronize()
+    check(o, l, k, f"T{T} E{E}", **kw)
+
+
+def test_select_two_streams_at_once(L):
+    """Calls of several sizes on two streams together, each with its own workspace and outputs."""
+    E, k = 256, 8
+    kw = dict(score="sigmoid", n_group=8, topk_group=4, group_top=2)
+    ls = [[torch.randn((T, E), device=dev) for T in (1, 300, 5000, 17)] for _ in range(2)]
+    ws = [torch.empty(L.moe_select_workspace_size(5000, E, k), dtype=torch.uint8, device=dev) for _ in range(2)]
+    outs = [[outputs(l.shape[0], E, k) for l in q] for q in ls]
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for q in range(2):
+            select(L, ls[q][i], L.Gate(**kw), k, outs[q][i], ws[q], ss[q])
+    torch.cuda.synchronize()
+    for q in range(2):
+        for l, o in zip(ls[q], outs[q]):
+            check(o, l, k, f"stream {q} T{l.shape[0]}", **kw)
