@@ -45,33 +45,48 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // Codes of a row.
 // ---------------------------------------------------------------------------
 // What a row's codes are formed with, from the largest magnitude (as bits, so
-// that infinities and NaN compare above every finite value).
+// that infinities and NaN compare above every finite value). A code is
+// rne(127 v / amax) exactly, without a branch (one for the values near a half
+// costs more code than the rest together: 333 rows of 1280 took 6.5 us, 4.2
+// so): the half that decides is c = floor(t) + 1/2 for t = 127 v / amax in
+// fp32, on either side of an integer, and the side of 127 v - c amax moves it
+// by a quarter before it is rounded. Both are scaled so that A = amax 2^B is in
+// [2^32, 2^33): a difference that is not 0 is above a quarter then, and c A has
+// 16 bits for bf16 v, so that its difference is rounded once; for fp32 v the
+// part of c A below 24 bits is taken off too, behind a first difference that
+// is exact wherever the sum's sign could depend on it (|t - c| < |t| / 127).
 struct RowQuant {
-  float amax, up, inv;  // up: a power of two that keeps 127 / amax finite; inv = 127 / (amax up)
-  bool finite;
+  float amax, up, inv, k127, a32;
   __device__ __forceinline__ explicit RowQuant(uint32_t amax_bits) {
-    finite = amax_bits < 0x7F800000u;
     amax = __uint_as_float(amax_bits);
-    up = amax < 0x1p-100f ? 0x1p+100f : 1.f;
-    inv = (finite && amax > 0.f) ? 127.f / (amax * up) : 0.f;
+    up = amax < 0x1p-80f ? 0x1p+100f : 1.f;  // a power of two that keeps 127 / amax and 2^B finite
+    const float a = amax * up;
+    const bool some = amax_bits - 1u < 0x7F800000u - 1u;  // else the codes are 0, or any: their scale is NaN
+    const float b = __uint_as_float((286u - (__float_as_uint(a) >> 23)) << 23);
+    inv = some ? 127.f / a : 0.f;
+    k127 = some ? 127.f * b : 0.f;
+    a32 = some ? a * b : 0.f;
   }
   // The scale: NaN for a row with an infinity or NaN (its products are then NaN), 0 for a row of zeros.
-  __device__ __forceinline__ float scale() const { return finite ? amax / 127.f : __uint_as_float(0x7FC00000u); }
-  // rne(127 v / amax). The fp32 quotient is off by less than 1e-4; where it is that near to a half, the exact side
-  // is taken from 127 v - (n + 1/2) amax, which 64 bits hold exactly (halves are common: v = amax / 2 gives 63.5).
-  __device__ __forceinline__ int code(float v) const {
-    const float t = (v * up) * inv;
-    float n = rintf(t);
-    if (__builtin_expect(fabsf(t - n) > 0.4999f, 0)) {
-      const float lo = floorf(t);
-      const double d = (double)v * 127.0 - ((double)lo + 0.5) * (double)amax;
-      n = d > 0.0 ? lo + 1.f : (d < 0.0 ? lo : 2.f * rintf(0.5f * (lo + 0.5f)));
-    }
-    return finite ? (int)n : 0;
+  __device__ __forceinline__ float scale() const {
+    return __float_as_uint(amax) < 0x7F800000u ? amax / 127.f : __uint_as_float(0x7FC00000u);
   }
+  // A word whose low byte is v's code.
+  template <bool BF16>
+  __device__ __forceinline__ uint32_t code(float v) const {
+    v *= up;
+    const float c = floorf(v * inv) + 0.5f, p = c * a32;
+    float d = fmaf(v, k127, -p);
+    if constexpr (!BF16) d -= fmaf(c, a32, -p);
+    return __float_as_uint((c + __builtin_amdgcn_fmed3f(d, -0.25f, 0.25f)) + 12582912.f);  // 1.5 2^23
+  }
+  template <bool BF16>
+  __device__ __forceinline__ uint32_t pack2(float a, float b) const {
+    return __builtin_amdgcn_perm(code<BF16>(b), code<BF16>(a), 0x0c0c0400u);
+  }
+  template <bool BF16>
   __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) const {
-    return (uint32_t)(code(a) & 0xFF) | ((uint32_t)(code(b) & 0xFF) << 8) | ((uint32_t)(code(c) & 0xFF) << 16) |
-           ((uint32_t)code(d) << 24);
+    return pack2<BF16>(a, b) | __builtin_amdgcn_perm(code<BF16>(d), code<BF16>(c), 0x04000c0cu);
   }
 };
 
@@ -128,8 +143,8 @@ __device__ __forceinline__ void quantise_row(const uint16_t* __restrict__ row, i
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const uint32_t a = raw[c][w >> 1][2 * (w & 1)], b = raw[c][w >> 1][2 * (w & 1) + 1];
-        o[w] = rq.pack4(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
-                        __uint_as_float(b & 0xFFFF0000u));
+        o[w] = rq.pack4<true>(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
+                              __uint_as_float(b & 0xFFFF0000u));
       }
       *reinterpret_cast<u32x4_t*>(codes + (size_t)p * 16) = o;
     }
@@ -443,7 +458,7 @@ __device__ __forceinline__ void put_h_codes(char* lds, int m, int col, const Row
   for (int p = 0; p < 2; ++p) {
     const int c = col + 2 * p;
     *reinterpret_cast<uint16_t*>(lds + (c >> 6) * 1024 + (((c >> 1) & 3) * 16 + m) * 16 + 2 * ((c >> 3) & 7)) =
-        (uint16_t)((rq.code(v[2 * p]) & 0xFF) | ((rq.code(v[2 * p + 1]) & 0xFF) << 8));
+        (uint16_t)rq.pack2<false>(v[2 * p], v[2 * p + 1]);
   }
 }
 
@@ -553,9 +568,9 @@ __global__ __launch_bounds__(256) void int8_decode_down(const float* __restrict_
 }
 
 // ---------------------------------------------------------------------------
-// Prefill: grouped GEMM, 256 weight rows x 128 or 256 tokens a block and 64 of
+// Prefill: grouped GEMM, 16 BN_T weight rows x 16 BM_T tokens a block and 64 of
 // K a stage, both operands straight into LDS in fragment order; eight waves of
-// 64 x 64 (128 tokens) or 128 x 64.
+// 32 x 64 (128 x 128), 64 x 64 (256 x 128) or 128 x 64 (256 x 256).
 // ---------------------------------------------------------------------------
 // h of prefill: 16-row tiles, 8 columns a piece, the two columns of a lane
 // together: the gate/up product's store of a fragment is 512 contiguous bytes
@@ -578,7 +593,7 @@ constexpr int kGroupN = 4;
 // an eighth of that rounding's, and y's traffic, read back by the combine, is
 // as long as the weights' (16384 tokens x 6 of 64 experts: 1.6 GB written and
 // read in fp32).
-template <int PHASE, int BM_T, bool HALF>
+template <int PHASE, int BM_T, bool HALF, int BN_T = 16>
 __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
                                                     const int32_t* __restrict__ src, const int32_t* __restrict__ n_entries,
                                                     const int4* __restrict__ entries,
@@ -586,9 +601,8 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
                                                     size_t mat_off, size_t scale_off, int N, int K, int H, int I,
                                                     float* __restrict__ hout, void* __restrict__ yout,
                                                     float* __restrict__ factor) {
-  constexpr int BN_T = 16;
   constexpr int NS = BM_T == 16 ? 4 : 6;
-  constexpr int WN = BM_T == 16 ? 8 : 4;
+  constexpr int WN = BN_T * BM_T / 32;
   constexpr int WM = 4;
   constexpr int WAVES_N = BN_T / WN;
   static_assert(WAVES_N * (BM_T / WM) == 8, "wave grid");
@@ -811,7 +825,7 @@ __global__ __launch_bounds__(64 * kReqWaves) void requantise_h(const float* __re
   auto store = [&](int c, const float2 (&o)[8]) {
     u32x4_t b;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) b[w] = rq.pack4(o[2 * w].x, o[2 * w].y, o[2 * w + 1].x, o[2 * w + 1].y);
+    for (int w = 0; w < 4; ++w) b[w] = rq.pack4<false>(o[2 * w].x, o[2 * w].y, o[2 * w + 1].x, o[2 * w + 1].y);
     *reinterpret_cast<u32x4_t*>(hq + (tile * pieces + c) * 1024 + lane * 16) = b;
   };
 #pragma unroll
@@ -938,23 +952,36 @@ hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src,
                          const int32_t* n, const int4* entries, const char* slot_base, size_t slot_stride, int H, int I,
                          float* h, uint8_t* hq, float* sh, void* y, float* factor, hipStream_t s) {
   const Int8Layout L = int8_layout(H, I);
-  const auto grid = [&](int N) { return dim3((unsigned)(((size_t)(rows / tile_rows + groups) * (N / 256) + 7) / 8 * 8)); };
-  const auto product = [&](auto kernel, int N, int K, const uint8_t* b, const float* bs, const int32_t* from, size_t mat,
-                           size_t scales) {
-    hipLaunchKernelGGL(kernel, grid(N), dim3(512), 0, s, b, bs, from, n, entries, slot_base, slot_stride, mat, scales, N,
+  const size_t most = rows / tile_rows + groups;  // entries
+  // Less than a block a CU: 128 weight rows a block, twice the blocks (a call of 333 tokens x 5 of 20 experts of
+  // 1280 x 640 42.1 -> 36.6 us; with blocks for 256 to 1024, 64 x 8 of 128 experts of 2048 x 768, 122 -> 129 us).
+  const auto narrow = [&](int N) { return tile_rows == 128 && most * (N / 256) < 256; };
+  const auto product = [&](auto kernel, int columns, int N, int K, const uint8_t* b, const float* bs,
+                           const int32_t* from, size_t mat, size_t scales) {
+    const dim3 grid((unsigned)((most * (N / columns) + 7) / 8 * 8));
+    hipLaunchKernelGGL(kernel, grid, dim3(512), 0, s, b, bs, from, n, entries, slot_base, slot_stride, mat, scales, N,
                        K, H, I, h, y, factor);
     return hipGetLastError();
   };
-  hipError_t e = tile_rows == 256 ? product(int8_gemm<1, 16, false>, 2 * I, H, xq, sx, src, L.p1, L.p1s)
-                                  : product(int8_gemm<1, 8, false>, 2 * I, H, xq, sx, src, L.p1, L.p1s);
+  const auto up = [&](auto kernel, int columns) {
+    return product(kernel, columns, 2 * I, H, xq, sx, src, L.p1, L.p1s);
+  };
+  const auto down = [&](auto kernel, int columns) {
+    return product(kernel, columns, H, I, hq, sh, nullptr, L.p2, L.p2s);
+  };
+  hipError_t e = tile_rows == 256 ? up(int8_gemm<1, 16, false>, 256)
+                 : narrow(2 * I)  ? up(int8_gemm<1, 8, false, 8>, 128)
+                                  : up(int8_gemm<1, 8, false>, 256);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(requantise_h, dim3((rows + 15) / 16), dim3(64 * kReqWaves), 0, s, h, I, hq, sh);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (factor != nullptr)
-    return tile_rows == 256 ? product(int8_gemm<2, 16, true>, H, I, hq, sh, nullptr, L.p2, L.p2s)
-                            : product(int8_gemm<2, 8, true>, H, I, hq, sh, nullptr, L.p2, L.p2s);
-  return tile_rows == 256 ? product(int8_gemm<2, 16, false>, H, I, hq, sh, nullptr, L.p2, L.p2s)
-                          : product(int8_gemm<2, 8, false>, H, I, hq, sh, nullptr, L.p2, L.p2s);
+    return tile_rows == 256 ? down(int8_gemm<2, 16, true>, 256)
+           : narrow(H)      ? down(int8_gemm<2, 8, true, 8>, 128)
+                            : down(int8_gemm<2, 8, true>, 256);
+  return tile_rows == 256 ? down(int8_gemm<2, 16, false>, 256)
+         : narrow(H)      ? down(int8_gemm<2, 8, false, 8>, 128)
+                          : down(int8_gemm<2, 8, false>, 256);
 }
 
 }  // namespace
