@@ -363,14 +363,15 @@ int cache_fill_async(moe_cache_t* cache, const moe_miss_t* misses, int n,
  * wfmt     MOE_W_F32 (x fp32), MOE_W_BF16, MOE_W_INT4 or MOE_W_MXFP4 (x bf16);
  *          the tiled GEMM (MOE_FFN_PREFILL) takes bf16 weights (H % 128,
  *          I % 64 == 0), MXFP4 weights (H % 256 == 0) and int8 weights
- *          (H % 256 == 0, I % 128 == 0); AUTO runs the matrix-vector kernels
+ *          (H % 128 == 0, I % 128 == 0); AUTO runs the matrix-vector kernels
  *          for the other formats. MOE_W_INT8 (x bf16, quantised here through
  *          perm_src) needs 16-byte aligned x, slots, y_perm and workspace
  * y_perm   device out fp32 [rows_total, H] (only listed rows are written)
  * workspace device scratch, >= moe_ffn_workspace_size(rows_total, H, I, wfmt)
  *          bytes, where rows_total bounds every row index used
  * mode     MOE_FFN_AUTO picks the matrix-vector kernels when every group has
- *          at most 32 rows and the tiled matrix-core GEMM otherwise.
+ *          at most 32 rows and the tiled matrix-core GEMM otherwise; for
+ *          int8 weights the GEMM from 4 rows an item on, on average.
  * Errors: MOE_EINVAL for null pointers, unsupported shapes or formats.
  * ------------------------------------------------------------------------ */
 typedef struct { int32_t expert, slot, row_begin, rows; } moe_work_t;
@@ -423,9 +424,10 @@ int moe_ffn_grouped(const void* x, int dtype, const int32_t* perm_src, const int
  *   workspace device scratch, >= moe_experts_workspace_size(...) bytes
  * x, slots, out and workspace 16-byte aligned. Limits: E <= 1024; the codes of
  * the tokens and of the T*k rows within 4 GiB each.
- * With a bf16 `out` the rows of more than 32 tokens (where the shape runs the
- * tiled GEMM) are kept in 11 bits before the sum; a column whose channel scale
- * s2 is below 2^-20 of its expert's largest keeps fewer.
+ * Calls of T*k >= 4*E rows run the tiled GEMM where the shape allows it
+ * (moe_ffn). With a bf16 `out` they keep rows in 11 bits before the sum; a
+ * column whose channel scale s2 is below 2^-20 of its expert's largest keeps
+ * fewer.
  * Errors: MOE_EINVAL (null, sizes, formats, alignment), MOE_EHIP.
  * ------------------------------------------------------------------------ */
 size_t moe_experts_workspace_size(int T, int k, int E, int H, int I, int wfmt);

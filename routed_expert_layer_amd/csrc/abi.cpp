@@ -422,12 +422,14 @@ int moe_ffn(const void* x, int dtype, const int32_t* perm_src, const moe_work_t*
   const size_t blob = moe_expert_bytes(wfmt, H, I);
   if (slot_stride < blob) return fail(MOE_EINVAL, "moe_ffn: slot_stride %zu < blob size %zu", slot_stride, blob);
   int rows_total = 0, max_rows = 0;
+  long long listed = 0;
   for (int i = 0; i < n_work; ++i) {
     const moe_work_t& w = work[i];
     if (w.rows < 0 || w.row_begin < 0 || w.slot < 0)
       return fail(MOE_EINVAL, "moe_ffn: work item %d has negative field", i);
     rows_total = std::max(rows_total, w.row_begin + w.rows);
     max_rows = std::max(max_rows, w.rows);
+    listed += w.rows;
   }
   if (ws_bytes < moe_ffn_workspace_size(rows_total, H, I, wfmt))
     return fail(MOE_EINVAL, "moe_ffn: workspace too small for %d rows", rows_total);
@@ -439,10 +441,10 @@ int moe_ffn(const void* x, int dtype, const int32_t* perm_src, const moe_work_t*
     if (!gemm_ok)
       return fail(MOE_EINVAL,
                   "moe_ffn: prefill GEMM needs bf16 weights with H %% 128 == 0 and I %% 64 == 0, MXFP4 weights "
-                  "with H %% 256 == 0, or int8 weights with H %% 256 == 0 and I %% 128 == 0");
+                  "with H %% 256 == 0, or int8 weights with H and I multiples of 128");
     prefill = true;
   } else if (mode == MOE_FFN_AUTO) {
-    prefill = max_rows > 32 && gemm_ok;
+    prefill = gemm_ok && (wfmt == MOE_W_INT8 ? moe::int8_gemm_pays(listed, n_work) : max_rows > 32);
   }
   if (wfmt == MOE_W_INT8) {
     if (!moe::int8_rows_ok(rows_total, rows_total, H, I))

@@ -944,7 +944,9 @@ hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const fl
 
 // Rows a prefill tile holds: 256 when groups have that many on average (16384 tokens over 64 experts: the 128-row tile
 // reads each weight tile twice as often from L2), else 128 (a 96-row group leaves half of a 256-row tile's waves idle).
-int tile_rows_for(int rows, int groups) { return (long long)rows >= 256ll * groups ? 256 : 128; }
+int tile_rows_for(int rows, int groups, int H) {
+  return (long long)rows >= 256ll * groups && H % 256 == 0 ? 256 : 128;
+}
 
 // The two products and the pass between them over planned entries (at most rows / tile + groups). factor: y's rows are
 // left in fp16 with one each; nullptr: fp32 rows.
@@ -953,9 +955,9 @@ hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src,
                          float* h, uint8_t* hq, float* sh, void* y, float* factor, hipStream_t s) {
   const Int8Layout L = int8_layout(H, I);
   const size_t most = rows / tile_rows + groups;  // entries
-  // Less than a block a CU: 128 weight rows a block, twice the blocks (a call of 333 tokens x 5 of 20 experts of
+  // N in 128s, or less than a block a CU: 128 weight rows a block, twice the blocks (333 tokens x 5 of 20 experts of
   // 1280 x 640 42.1 -> 36.6 us; with blocks for 256 to 1024, 64 x 8 of 128 experts of 2048 x 768, 122 -> 129 us).
-  const auto narrow = [&](int N) { return tile_rows == 128 && most * (N / 256) < 256; };
+  const auto narrow = [&](int N) { return N % 256 != 0 || (tile_rows == 128 && most * (N / 256) < 256); };
   const auto product = [&](auto kernel, int columns, int N, int K, const uint8_t* b, const float* bs,
                            const int32_t* from, size_t mat, size_t scales) {
     const dim3 grid((unsigned)((most * (N / columns) + 7) / 8 * 8));
@@ -1032,7 +1034,7 @@ hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const in
     if (!gemm) {
       e = decode_products(wk, wa.n, xq, sx, nullptr, slot_base, slot_stride, H, I, h, y, s);
     } else {
-      const int tile = tile_rows_for(rows, wa.n);
+      const int tile = tile_rows_for(rows, wa.n, H);
       int32_t* count = reinterpret_cast<int32_t*>(b + w.plan);
       int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
       hipLaunchKernelGGL(plan_list, dim3(1), dim3(256), 0, s, wk, tile, w.entries, count, entries);
@@ -1072,11 +1074,10 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   uint8_t* xq = reinterpret_cast<uint8_t*>(b + w.xq);
   float *sx = reinterpret_cast<float*>(b + w.sx), *h = reinterpret_cast<float*>(b + w.h);
   const uint16_t* xb = static_cast<const uint16_t*>(x);
-  // Few rows an expert: weights streamed once per 16 rows; else the tiled GEMM where the shape allows it.
-  const bool gemm = int8_gemm_supported(H, I) && T > 32;
+  const bool gemm = int8_gemm_supported(H, I) && int8_gemm_pays(rows, E);
   const bool half = gemm && out_bf16;
   float* factor = half ? h : nullptr;  // over h, which is codes by then
-  const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups) : 0;
+  const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups, H) : 0;
   int32_t* n = reinterpret_cast<int32_t*>(b + w.plan);
   int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
   hipError_t e = launch_quantise_tokens(xb, T, H, xq, sx,

@@ -90,9 +90,13 @@ CASES = [
     (2, 3, 3, 192, 320, 0),     # K tails of the decode kernels, every expert
     (7, 16, 4, 1088, 704, 0.5),
     (16, 4, 2, 256, 128, 1.0),
-    (17, 2, 1, 256, 128, 0),    # a group past one tile of 16 rows
+    (17, 2, 1, 256, 128, 0),    # the tiled products: from 4 rows an expert on
+    (40, 16, 1, 256, 128, 6.0),  # few rows an expert, but groups past one tile of 16 rows
+    (6, 3, 2, 384, 128, 0),     # tiles of 128 weight rows, where H is no multiple of 256
+    (700, 2, 1, 640, 384, 0),   # the same with groups of more than 256 rows
+    (90, 6, 3, 128, 256, 1.0),
     (32, 2, 2, 320, 192, 0),
-    (33, 8, 2, 256, 128, 0.5),  # the tiled products from here on
+    (33, 8, 2, 256, 128, 0.5),
     (64, 16, 6, 512, 256, 1.5),
     (40, 4, 2, 320, 192, 0.5),  # a shape that only the decode kernels take
     (130, 5, 3, 768, 384, 0.5),
