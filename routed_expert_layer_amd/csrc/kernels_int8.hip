@@ -601,7 +601,9 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
                                                     size_t mat_off, size_t scale_off, int N, int K, int H, int I,
                                                     float* __restrict__ hout, void* __restrict__ yout,
                                                     float* __restrict__ factor) {
-  constexpr int NS = BM_T == 16 ? 4 : 6;
+  // stages: 128 KiB for one block a CU, or 64 and 72 KiB for two (with 6, so one block a CU, 2048 tokens x 4 of 90
+  // experts of 1024 x 512 took 68.7 us, not 62.0, 8192 x 6 of 256 of 4096 x 2048 2104, not 1994)
+  constexpr int NS = BM_T == 16 || BN_T == 8 ? 4 : 3;
   constexpr int WN = BN_T * BM_T / 32;
   constexpr int WM = 4;
   constexpr int WAVES_N = BN_T / WN;
@@ -612,7 +614,7 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
   __shared__ __attribute__((aligned(1024))) char lds[NS][STAGE];
 
   // an eighth of the tiles for each XCD (blocks b with the same b % 8), in order
-  const int NTB = N / (16 * BN_T), total = *n_entries * NTB, share = (total + 7) / 8;
+  const int NTB = (N / 16 + BN_T - 1) / BN_T, last = N / 16 - 1, total = *n_entries * NTB, share = (total + 7) / 8;
   const int in_share = (int)(blockIdx.x >> 3), t = (int)(blockIdx.x & 7) * share + in_share;
   if (in_share >= share || t >= total) return;
   const int ent = t / NTB;
@@ -638,7 +640,7 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
   for (int q = 0; q < FPW; ++q) {
     const int f = wave + 8 * q;
     if (q < QW) {
-      off[q] = (uint32_t)((nt * BN_T + f) * KC) * 1024u + lane * 16;
+      off[q] = (uint32_t)(min(nt * BN_T + f, last) * KC) * 1024u + lane * 16;  // past N: not stored
       kstep[q] = 1024;
     } else {
       int mloc = mt * (16 * BM_T) + (f - FA) * 16 + (lane & 15);
@@ -744,7 +746,7 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
   f32x4_t sw[WN];
 #pragma unroll
   for (int i = 0; i < WN; ++i)
-    sw[i] = *reinterpret_cast<const f32x4_t*>(wscale + 16 * (nt * BN_T + wn * WN + i) + 4 * (lane >> 4));
+    sw[i] = *reinterpret_cast<const f32x4_t*>(wscale + 16 * min(nt * BN_T + wn * WN + i, last) + 4 * (lane >> 4));
   float st[WM];
 #pragma unroll
   for (int j = 0; j < WM; ++j) {
@@ -764,6 +766,7 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
 #pragma unroll
     for (int i = 0; i < WN; ++i) {
       const int ntile = nt * BN_T + wn * WN + i;
+      if (ntile > last) break;
       const i32x4_t s = acc[i][j];
       f32x4_t v;
 #pragma unroll
@@ -942,11 +945,10 @@ hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const fl
   return decode_down<W, 8, true>(wk, n_items, slot_base, slot_stride, H, I, h, y, s);
 }
 
-// Rows a prefill tile holds: 256 when groups have that many on average (16384 tokens over 64 experts: the 128-row tile
-// reads each weight tile twice as often from L2), else 128 (a 96-row group leaves half of a 256-row tile's waves idle).
-int tile_rows_for(int rows, int groups, int H) {
-  return (long long)rows >= 256ll * groups && H % 256 == 0 ? 256 : 128;
-}
+// Rows a prefill tile holds: 256 when groups have 384 on average, else 128, of which two blocks fit on a CU. Calls in us,
+// 128 / 256 rows: 16 experts of 2048 x 768 with 256 rows each 57 / 67 (most groups need a second tile then), 8 of
+// 3968 x 1920 with 256 77 / 99, with 512 138 / 123; 64 of 4096 x 2048 with 384 858 / 835, with 768 1589 / 1500.
+int tile_rows_for(int rows, int groups) { return (long long)rows >= 384ll * groups ? 256 : 128; }
 
 // The two products and the pass between them over planned entries (at most rows / tile + groups). factor: y's rows are
 // left in fp16 with one each; nullptr: fp32 rows.
@@ -955,12 +957,12 @@ hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src,
                          float* h, uint8_t* hq, float* sh, void* y, float* factor, hipStream_t s) {
   const Int8Layout L = int8_layout(H, I);
   const size_t most = rows / tile_rows + groups;  // entries
-  // N in 128s, or less than a block a CU: 128 weight rows a block, twice the blocks (333 tokens x 5 of 20 experts of
+  // Less than a block a CU: 128 weight rows a block, twice the blocks (a call of 333 tokens x 5 of 20 experts of
   // 1280 x 640 42.1 -> 36.6 us; with blocks for 256 to 1024, 64 x 8 of 128 experts of 2048 x 768, 122 -> 129 us).
-  const auto narrow = [&](int N) { return N % 256 != 0 || (tile_rows == 128 && most * (N / 256) < 256); };
+  const auto narrow = [&](int N) { return tile_rows == 128 && most * ((N + 255) / 256) < 256; };
   const auto product = [&](auto kernel, int columns, int N, int K, const uint8_t* b, const float* bs,
                            const int32_t* from, size_t mat, size_t scales) {
-    const dim3 grid((unsigned)((most * (N / columns) + 7) / 8 * 8));
+    const dim3 grid((unsigned)((most * ((N + columns - 1) / columns) + 7) / 8 * 8));
     hipLaunchKernelGGL(kernel, grid, dim3(512), 0, s, b, bs, from, n, entries, slot_base, slot_stride, mat, scales, N,
                        K, H, I, h, y, factor);
     return hipGetLastError();
@@ -1034,7 +1036,7 @@ hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const in
     if (!gemm) {
       e = decode_products(wk, wa.n, xq, sx, nullptr, slot_base, slot_stride, H, I, h, y, s);
     } else {
-      const int tile = tile_rows_for(rows, wa.n, H);
+      const int tile = tile_rows_for(rows, wa.n);
       int32_t* count = reinterpret_cast<int32_t*>(b + w.plan);
       int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
       hipLaunchKernelGGL(plan_list, dim3(1), dim3(256), 0, s, wk, tile, w.entries, count, entries);
@@ -1077,7 +1079,7 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   const bool gemm = int8_gemm_supported(H, I) && int8_gemm_pays(rows, E);
   const bool half = gemm && out_bf16;
   float* factor = half ? h : nullptr;  // over h, which is codes by then
-  const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups, H) : 0;
+  const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups) : 0;
   int32_t* n = reinterpret_cast<int32_t*>(b + w.plan);
   int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
   hipError_t e = launch_quantise_tokens(xb, T, H, xq, sx,
