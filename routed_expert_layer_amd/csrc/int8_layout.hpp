@@ -59,7 +59,7 @@ __host__ __device__ inline int int8_k2_source(int c, int q, int j) { return 64 *
 // Workspace of the products: token codes and scales, h (fp32), its codes and
 // scales, the plan (a count, then an entry for each group or 128-row tile).
 struct Int8Ws {
-  size_t xq, sx, h, hq, sh, plan, bytes;
+  size_t xq, sx, h, hq, sh, plan, done, bytes;
   int entries;  // that the plan holds behind its count
 };
 inline Int8Ws int8_ws(size_t rows, size_t tokens, int H, int I) {
@@ -72,7 +72,8 @@ inline Int8Ws int8_ws(size_t rows, size_t tokens, int H, int I) {
   w.sh = align_up(w.hq + padded * I, 256);
   w.plan = align_up(w.sh + padded * 4, 256);
   w.entries = (int)(rows / 128) + kTableItems + 1;
-  w.bytes = w.plan + 256 + align_up((size_t)w.entries * 16, 256);
+  w.done = w.plan + 256 + align_up((size_t)w.entries * 16, 256);  // counts by group of output columns
+  w.bytes = w.done + align_up((size_t)H / 8, 256);
   return w;
 }
 hipError_t launch_pack_int8(int H, int I, const void* Q1, const void* Q3, const void* Q2, const void* S1,

@@ -164,6 +164,7 @@ struct ArgItems {
 struct DevItems {
   const int32_t* n;
   const int4* items;
+  __device__ __forceinline__ int count() const { return *n; }
   __device__ __forceinline__ bool get(int i, int4& it) const {
     if (i >= *n) return false;
     const int4 v = items[i];
@@ -188,6 +189,8 @@ struct Plan {
   int E, n_slots, rows_max, tile_rows, cap;
   int32_t* n;  // nullptr: no plan
   int4* items;
+  uint32_t* zero;  // `zeros` words are cleared besides
+  int zeros;
 };
 
 // Thread's group `it` of a list of 256 (`base` entries before it); returns the new number of entries. E, lds: LDS.
@@ -231,6 +234,7 @@ __device__ __forceinline__ int plan_groups(int4 it, bool ok, int base, int tile_
 }
 
 __device__ __forceinline__ void run_plan(const Plan& p) {
+  for (int q = threadIdx.x; q < p.zeros; q += 256) p.zero[q] = 0u;
   __shared__ int lds[2][256];
   __shared__ int4 group[256];
   int base = 0;
@@ -521,17 +525,86 @@ __device__ __forceinline__ void quantise_h_rows(const float* __restrict__ h, int
   }
 }
 
+// A float of y to or from other blocks of the same launch: at device scope (sc1), whichever XCDs they are on. base:
+// wave-uniform, p within 2^32 bytes above it.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t device_rows(const float* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), (short)0, -1, 0x00020000);
+}
+__device__ __forceinline__ f32x4_t device_load4(const float* base, const float* p) {
+  return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                         device_rows(base), (uint32_t)((const char*)p - (const char*)base), 0, 16));
+}
+__device__ __forceinline__ void device_store4(float* base, float* p, const f32x4_t& v) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), device_rows(base),
+                                         (uint32_t)((char*)p - (char*)base), 0, 16);
+}
+
+// What a short step's down projection forms its output from: each block, once
+// its part of y is stored, counts itself at its columns (`done`, zeroed by the
+// launch before), and the one that comes last there adds the tokens' rows up in
+// the combine's order, so the result does not depend on which block that is;
+// no block waits for another. Saves a launch, but y goes past the L2s and the
+// last blocks work alone, so up to kSumRows rows only. Calls in us, without /
+// with: one token x 6 of 64 experts of 4096 x 2048 36.4 / 34.9, 4 x 6 85.5 /
+// 85.0, 8 x 6 117 / 118; 4 x 2 of 96 of 1024 x 512 19.0 / 16.0, 16 x 2 19.2 /
+// 20.8; 4 x 8 of 128 of 2048 x 768 31.2 / 32.9.
+constexpr int kSumRows = 24;
+struct SumArgs {
+  const int32_t *topk_idx, *perm_pos, *slot_of;
+  const float* topk_w;
+  int T, k, n_slots;
+  void* out;
+  int out_bf16;
+  uint32_t* done;  // [H / (16 R)]
+};
+
+template <int COLS>
+__device__ __forceinline__ void sum_columns(const SumArgs& f, const float* y, int H, int col0) {
+  for (int q = threadIdx.x; q < f.T * (COLS / 4); q += 256) {
+    const int t = q / (COLS / 4), col = col0 + 4 * (q - t * (COLS / 4));
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < f.k; j0 += 8) {
+      f32x4_t v[8];
+      float w[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        w[u] = 0.f;
+        v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (j0 + u >= f.k) continue;
+        const int e = f.topk_idx[t * f.k + j0 + u];
+        const int slot = f.slot_of ? f.slot_of[e] : e;
+        if (slot < 0 || slot >= f.n_slots) continue;
+        w[u] = f.topk_w[t * f.k + j0 + u];
+        v[u] = device_load4(y, y + (size_t)f.perm_pos[t * f.k + j0 + u] * H + col);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = fmaf(w[u], v[u][c], acc[c]);
+    }
+    if (f.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(f.out) + (size_t)t * H + col) =
+          make_uint2(bf16_bits(acc[0]) | bf16_bits(acc[1]) << 16, bf16_bits(acc[2]) | bf16_bits(acc[3]) << 16);
+    else
+      *reinterpret_cast<f32x4_t*>(static_cast<float*>(f.out) + (size_t)t * H + col) = acc;
+  }
+}
+
 // Down projection: a block is R 16-row tiles of P2 (16 R output columns) of an
 // item; it forms the codes of the item's rows of h itself, while its weights
 // are on their way.
-template <typename W, int NF, bool MORE, int R>
+template <typename W, int NF, bool MORE, int R, bool SUM>
 __global__ __launch_bounds__(256) void int8_decode_down(const float* __restrict__ h, const W wk,
                                                         const char* __restrict__ slot_base, size_t slot_stride,
-                                                        const Int8Layout L, int H, int I, float* __restrict__ y) {
+                                                        const Int8Layout L, int H, int I, float* y, const SumArgs f) {
   const int NB = H / (16 * R);
   const int item = blockIdx.x / NB, tile0 = (blockIdx.x - item * NB) * R;
   int4 it;
-  if (!wk.get(item, it)) return;
+  if (!wk.get(item, it)) {
+    if constexpr (SUM)
+      if (item == 0) sum_columns<16 * R>(f, y, H, 16 * tile0);  // no expert of the step has a slot: zeros
+    return;
+  }
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
   const int KC = I / 64, c0 = (KC * wave) >> 2, c1 = (KC * (wave + 1)) >> 2;
   const char* blob = slot_base + (size_t)it.x * slot_stride;
@@ -561,9 +634,23 @@ __global__ __launch_bounds__(256) void int8_decode_down(const float* __restrict_
       f32x4_t o;
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[c] = (float)s[c] * (st * sw[c]);
-      *reinterpret_cast<f32x4_t*>(y + (size_t)(it.y + m) * H + n0) = o;
+      float* row = y + (size_t)(it.y + m) * H + n0;
+      if constexpr (SUM)
+        device_store4(y, row, o);
+      else
+        *reinterpret_cast<f32x4_t*>(row) = o;
     }
     __syncthreads();
+  }
+  if constexpr (SUM) {
+    __shared__ int last;
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's stores have completed
+    __syncthreads();                // ... and every wave's
+    if (threadIdx.x == 0)
+      last = __hip_atomic_fetch_add(f.done + tile0 / R, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u ==
+             (uint32_t)wk.count();
+    __syncthreads();
+    if (last) sum_columns<16 * R>(f, y, H, 16 * tile0);
   }
 }
 
@@ -917,17 +1004,22 @@ hipError_t launch_quantise_tokens(const uint16_t* x, int T, int H, uint8_t* xq, 
 
 template <typename W, int NF, bool MORE>
 hipError_t decode_down(const W& wk, int n_items, const char* slot_base, size_t slot_stride, int H, int I,
-                       const float* h, float* y, hipStream_t s) {
+                       const float* h, float* y, const SumArgs* sum, hipStream_t s) {
   constexpr int R = 2;  // H is a multiple of 64
-  hipLaunchKernelGGL((int8_decode_down<W, NF, MORE, R>), dim3(n_items * (H / (16 * R))), dim3(256), (size_t)16 * I, s, h, wk,
-                     slot_base, slot_stride, int8_layout(H, I), H, I, y);
-  return hipGetLastError();
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(n_items * (H / (16 * R))), dim3(256), (size_t)16 * I, s, h, wk, slot_base,
+                       slot_stride, int8_layout(H, I), H, I, y, sum != nullptr ? *sum : SumArgs{});
+    return hipGetLastError();
+  };
+  if constexpr (std::is_same_v<W, DevItems>)
+    if (sum != nullptr) return run(int8_decode_down<W, NF, MORE, R, true>);
+  return run(int8_decode_down<W, NF, MORE, R, false>);
 }
 
 template <typename W>
 hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const float* sx, const int32_t* src,
                            const char* slot_base, size_t slot_stride, int H, int I, float* h, float* y,
-                           hipStream_t s) {
+                           hipStream_t s, const SumArgs* sum = nullptr) {
   const Int8Layout L = int8_layout(H, I);
   const auto up = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(n_items * (I / 8)), dim3(256), 0, s, xq, sx, src, wk, slot_base, slot_stride, L, H,
@@ -940,9 +1032,9 @@ hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const fl
   else up(int8_decode_up<W, 8, true>);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (I <= 1024) return decode_down<W, 4, false>(wk, n_items, slot_base, slot_stride, H, I, h, y, s);
-  if (I <= 2048) return decode_down<W, 8, false>(wk, n_items, slot_base, slot_stride, H, I, h, y, s);
-  return decode_down<W, 8, true>(wk, n_items, slot_base, slot_stride, H, I, h, y, s);
+  if (I <= 1024) return decode_down<W, 4, false>(wk, n_items, slot_base, slot_stride, H, I, h, y, sum, s);
+  if (I <= 2048) return decode_down<W, 8, false>(wk, n_items, slot_base, slot_stride, H, I, h, y, sum, s);
+  return decode_down<W, 8, true>(wk, n_items, slot_base, slot_stride, H, I, h, y, sum, s);
 }
 
 // Rows a prefill tile holds: 256 when groups have 384 on average, else 128, of which two blocks fit on a CU. Calls in us,
@@ -1082,9 +1174,17 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups) : 0;
   int32_t* n = reinterpret_cast<int32_t*>(b + w.plan);
   int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
+  const bool sums = !gemm && rows <= kSumRows;
+  uint32_t* done = reinterpret_cast<uint32_t*>(b + w.done);
   hipError_t e = launch_quantise_tokens(xb, T, H, xq, sx,
-                                        Plan{counts, offsets, slot_of, E, n_slots, rows, tile, w.entries, n, entries}, s);
+                                        Plan{counts, offsets, slot_of, E, n_slots, rows, tile, w.entries, n, entries, done,
+                                             sums ? H / 32 : 0},
+                                        s);
   if (e != hipSuccess) return e;
+  if (sums) {
+    const SumArgs f{topk_idx, perm_pos, slot_of, topk_w, T, k, n_slots, out, (int)out_bf16, done};
+    return decode_products(DevItems{n, entries}, groups, xq, sx, perm_src, slot_base, slot_stride, H, I, h, y, s, &f);
+  }
   if (gemm)
     e = gemm_products(xq, sx, perm_src, rows, groups, tile, n, entries, slot_base, slot_stride, H, I, h,
                       reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, factor, s);

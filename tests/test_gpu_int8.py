@@ -87,6 +87,8 @@ CASES = [
     # T, E, k, H, I, skew
     (1, 4, 1, 64, 64, 0),
     (1, 8, 6, 512, 256, 0),
+    (12, 8, 2, 256, 128, 0.5),  # the last call whose down projection forms the output
+    (13, 8, 2, 256, 128, 0.5),
     (2, 3, 3, 192, 320, 0),     # K tails of the decode kernels, every expert
     (7, 16, 4, 1088, 704, 0.5),
     (16, 4, 2, 256, 128, 1.0),
