@@ -6,7 +6,8 @@
 // an expert), then blocks of 64 tokens that add the counts up, each for
 // itself, and place their rows. Longer batches add the counts up in a launch
 // of its own (each block reading every count would be the longer way: 512
-// chunks x 256 experts are 128 KiB a block).
+// chunks x 256 experts are 128 KiB a block). Captured calls in us, one block / two launches: 32 tokens of 128 experts 10.6
+// / 12.5, 64 13.2 / 12.5, 64 of 64 experts 8.4 / 9.7; two / three: 16384 of 64 14.0 / 17.9, of 256 30.3 / 35.3.
 #include "dev_common.hpp"
 #include "dev_select.hpp"
 #include "moe_kernels.hpp"
@@ -314,7 +315,8 @@ hipError_t select_kernels(const SelectCall& a) {
   }
   const SelectWs w = select_ws(a.T, a.E);
   const bool few = a.T <= kFewTokens;
-  // 16 tokens a block while that leaves at most a block for each CU; the masks hold 64
+  // 16 tokens a block while that leaves at most a block for each CU; the masks hold 64 (512 tokens of 256 experts with
+  // 16 / 64 a block 15.2 / 18.5 us, 8192 with 32 / 16 23.6 / 24.1)
   const int chunk = a.T <= 4096 ? 16 : RVE > 0 || !few ? kMaxTokensPerBlock : 32;
   const int chunks = (a.T + chunk - 1) / chunk, threads = RVE > 0 ? chunk * 16 : 1024;
   int32_t* hist = reinterpret_cast<int32_t*>(a.ws + w.hist);
@@ -333,11 +335,19 @@ hipError_t select_kernels(const SelectCall& a) {
   return hipGetLastError();
 }
 
-// A row a token (RVE experts a lane) where the shape fits one and a wave a token would take several turns.
+// A row a token (RVE experts a lane) or a wave a token. Up to 16 tokens each wave of the block has one anyway. In a
+// block of its own a wave with 16 tokens' work to share takes four turns of a row's; from two launches on, a wave a token
+// has the shorter chain, and a row the fewer instructions once the chip is full, which is later the more experts a
+// lane of the row holds. Captured calls in us, row / wave: 64 tokens x 256 experts of 8 groups 13.7 / 26.9, 512 15.2 /
+// 13.8, 2048 20.7 / 14.0, 8192 27.0 / 23.6, 16384 30.3 / 39.8; 128 experts of 4 groups, 512 14.2 / 13.1, 2048 14.4 /
+// 13.4, 4096 15.1 / 17.5; 64 experts, 512 10.6 / 11.0. Without a balance most experts need no score: 256 experts by
+// softmax, 4096 tokens 14.6 / 13.7, 8192 16.9 / 19.6.
 template <int VE>
 hipError_t select_shapes(const SelectCall& a) {
   const SelectShape row = select_shape(a.E, a.g.n_group, 16);
-  if (a.T > 16 && a.src.nsplit == 1 && a.src.bias == nullptr && a.src.keep == nullptr && row.lanes > 0) {
+  const bool given = a.src.nsplit == 1 && a.src.bias == nullptr && a.src.keep == nullptr;
+  const bool wave = a.T <= 16 || (a.T > kOneBlock && a.T <= (row.ve > 8 ? (a.g.balance != nullptr ? 8192 : 4096) : row.ve > 4 ? 2048 : 0));
+  if (given && !wave && row.lanes > 0) {
     SelectCall b = a;
     b.row_lanes = row.lanes;
     if (row.ve <= 4) return select_kernels<VE, 4>(b);

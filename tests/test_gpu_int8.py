@@ -438,3 +438,46 @@ def test_decoders_refuse_unaligned_tokens(L):
             DeviceDecodeLayer(store, cfg.S, cfg.T, cfg.k, "bf16", dev).step(0, x, W, b)
     finally:
         store.close()
+
+
+def test_experts_graph_of_a_short_step(L):
+    """A step whose down projection forms the output, captured and replayed on changing tokens and routings, with eager
+    calls on the same workspace between the replays; an expert without a slot, and steps of which none has one."""
+    E, k, H, I, T = 16, 3, 512, 256, 2
+    experts = [ic.expert(H, I, e, dev) for e in range(E)]
+    slot_of = list(range(E))
+    slots, stride = pack(L, H, I, experts, slot_of, E)
+    s = torch.cuda.Stream()
+    x, rt = tokens(T, H, 0), routing(T, E, k, 0)
+    size = max(L.moe_experts_workspace_size(n, k, E, H, I, L.MOE_W_INT8) for n in (T, 40))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device=dev)
+    out = torch.empty((T, H), device=dev)
+    table = torch.tensor(slot_of, dtype=torch.int32, device=dev)
+    d = rt["dev"]
+
+    def step(stream):
+        L.moe_experts(x, d["topk_idx"], d["topk_w"], d["perm_src"], d["perm_pos"], d["counts"], d["offsets"], table, E,
+                      slots, stride, L.MOE_W_INT8, H, I, out, ws, stream)
+
+    torch.cuda.synchronize()
+    L.moe_graph_begin(s)
+    step(s)
+    graph = L.moe_graph_end(s)
+    for i in range(6):
+        nx, nrt = tokens(T, H, 10 + i), routing(T, E, k, 20 + i)
+        x.copy_(nx)
+        for n in d:
+            d[n].copy_(nrt["dev"][n])
+        now = [-1 if i == 5 or (i % 2 and e == nrt["idx"][0][0]) else e for e in range(E)]
+        table.copy_(torch.tensor(now, dtype=torch.int32))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        L.moe_graph_launch(graph, s)
+        torch.cuda.synchronize()
+        replay = out.clone()
+        run(L, tokens(40, H, i), routing(40, E, k, i), slots, stride, now, E, H, I, ws=ws)
+        out.fill_(float("nan"))
+        step(None)
+        torch.cuda.synchronize()
+        assert torch.equal(out, replay), f"replay {i}"
+        ic.check(np64(out), *expected(nx, experts, nrt, now, E), f"replay {i}")
