@@ -137,7 +137,8 @@ int moe_route_noalloc(const void* x, int dtype, const void* Wr, const float* bia
  * The grouping outputs are moe_route's.
  *
  * moe_select: from logits, device fp32 [T, E]. Scratch of at least
- *   moe_select_workspace_size(T, E, k) bytes, 16-byte aligned.
+ *   moe_select_workspace_size(T, E, k) bytes, 16-byte aligned; calls that may
+ *   overlap (on two streams, in two graphs) need one each.
  * moe_route_scored: from x and Wr, with moe_route's logits (bias [E] is added
  *   to the logits), arguments, scratch and limits.
  * Limits: 1 <= k <= min(E, 16), E <= 1024, n_group <= 64 dividing E,
@@ -421,7 +422,8 @@ int moe_ffn_grouped(const void* x, int dtype, const int32_t* perm_src, const int
  *   wfmt     MOE_W_INT8; other formats run moe_ffn or moe_ffn_grouped, then
  *            moe_combine
  *   out      device [T, H] of out_dtype (fp32 or bf16)
- *   workspace device scratch, >= moe_experts_workspace_size(...) bytes
+ *   workspace device scratch, >= moe_experts_workspace_size(...) bytes; calls
+ *            that may overlap (on two streams, in two graphs) need one each
  * x, slots, out and workspace 16-byte aligned. Limits: E <= 1024; the codes of
  * the tokens and of the T*k rows within 4 GiB each.
  * Calls of T*k >= 4*E rows run the tiled GEMM where the shape allows it
