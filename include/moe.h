@@ -427,9 +427,7 @@ int moe_ffn_grouped(const void* x, int dtype, const int32_t* perm_src, const int
  * x, slots, out and workspace 16-byte aligned. Limits: E <= 1024; the codes of
  * the tokens and of the T*k rows within 4 GiB each.
  * Calls of T*k >= 4*E rows run the tiled GEMM where the shape allows it
- * (moe_ffn). With a bf16 `out` they keep rows in 11 bits before the sum; a
- * column whose channel scale s2 is below 2^-20 of its expert's largest keeps
- * fewer.
+ * (moe_ffn). Rows stay in fp32 until they are added, whatever `out` is.
  * Errors: MOE_EINVAL (null, sizes, formats, alignment), MOE_EHIP.
  * ------------------------------------------------------------------------ */
 size_t moe_experts_workspace_size(int T, int k, int E, int H, int I, int wfmt);

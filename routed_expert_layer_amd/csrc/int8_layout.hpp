@@ -13,11 +13,11 @@ namespace moe {
 // the gate/up product leaves its columns in (int8_k2_source): lane group q
 // holds, of every 8 columns, the two that the accumulator lanes of group q
 // hold. fp32 scales: P1's in row order (gate and up interleaved), P2's by
-// column, then one power of two that brings every possible product of P2 into
-// fp16 (see kRowBits). Sections [P1 codes][P1 scales][P2 codes][P2 scales and
-// the power], 256-B aligned.
+// column, and a reserved word behind them, which the size of a blob counts and
+// nothing reads. Sections [P1 codes][P1 scales][P2 codes][P2 scales, word],
+// 256-B aligned.
 struct Int8Layout {
-  size_t p1, p1s, p2, p2s, unit, bytes;
+  size_t p1, p1s, p2, p2s, bytes;
 };
 inline Int8Layout int8_layout(int H, int I) {
   Int8Layout l{};
@@ -26,8 +26,7 @@ inline Int8Layout int8_layout(int H, int I) {
   l.p1s = align_up(2 * HI, 256);
   l.p2 = align_up(l.p1s + (size_t)2 * I * 4, 256);
   l.p2s = align_up(l.p2 + HI, 256);
-  l.unit = l.p2s + (size_t)H * 4;
-  l.bytes = align_up(l.unit + 4, 256);
+  l.bytes = align_up(l.p2s + (size_t)H * 4 + 4, 256);
   return l;
 }
 // H, I multiples of 64. The decode kernels hold 16 rows of I codes in LDS, and

@@ -338,26 +338,6 @@ __global__ __launch_bounds__(256) void pack_int8_kernel(const int8_t* __restrict
   if (r < (size_t)H) reinterpret_cast<float*>(blob + L.p2s)[r] = S2[r];
 }
 
-// The power of two 2^u with |sum * scale * 2^u| <= 2^15 for any codes (|sum| <= 127 * 128 I) and the expert's scales.
-__global__ __launch_bounds__(256) void pack_int8_unit(const float* __restrict__ S2, int H, int I,
-                                                      float* __restrict__ unit) {
-  __shared__ uint32_t wmax[4];
-  uint32_t m = 0;
-  for (int n = threadIdx.x; n < H; n += 256) m = max(m, abs_bits(S2[n]));
-  m = wave_max_u32(m);
-  if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  const float most = __uint_as_float(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
-  // exponents within what fp32 holds; scales of 0, or not finite, need none
-  int e = 0;
-  if (most > 0.f && most < INFINITY) {
-    const int m = ilogbf(most);
-    e = min(max(14 - m - ilogbf(ldexpf(most, -m) * (127.f * 128.f * (float)I)), -126), 126);
-  }
-  *unit = ldexpf(1.f, e);
-}
-
 // ---------------------------------------------------------------------------
 // Decode: every weight byte is read once, straight from memory into matrix
 // instructions whose other operand holds up to 16 tokens' codes. Bound by the
@@ -680,22 +660,19 @@ __device__ __forceinline__ size_t h_tile_at(size_t row, int piece, int q, int I)
 constexpr int kGroupN = 4;
 
 // PHASE 1: gate/up from tokens' codes (rows through src) to h, tiled as above.
-// PHASE 2: the down projection from h's codes to y.
-//
-// What a prefill down projection leaves of its rows: fp32 rows of y; or, for a
-// bf16 layer output, fp16 rows (11 bits) in units of their row factor (below),
-// since a token's sum of them is rounded to 8 bits right after: their error is
-// an eighth of that rounding's, and y's traffic, read back by the combine, is
-// as long as the weights' (16384 tokens x 6 of 64 experts: 1.6 GB written and
-// read in fp32).
-template <int PHASE, int BM_T, bool HALF, int BN_T = 16>
+// PHASE 2: the down projection from h's codes to fp32 rows of y, as the decode
+// kernels leave them: a token's rows may cancel, and what fewer bits take from
+// them is then no longer below the rounding of their sum. (fp16 rows with a
+// factor each, for bf16 outputs, made 16384 tokens x 6 of 64 experts of 4096 x
+// 2048 2.93 ms, not 3.15, but lost 2^-12 of the rows: 9e-4 relative on mixed
+// inputs, all of the sum where rows cancel.)
+template <int PHASE, int BM_T, int BN_T = 16>
 __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ bsrc, const float* __restrict__ bscale,
                                                     const int32_t* __restrict__ src, const int32_t* __restrict__ n_entries,
                                                     const int4* __restrict__ entries,
                                                     const char* __restrict__ slot_base, size_t slot_stride,
                                                     size_t mat_off, size_t scale_off, int N, int K, int H, int I,
-                                                    float* __restrict__ hout, void* __restrict__ yout,
-                                                    float* __restrict__ factor) {
+                                                    float* __restrict__ hout, float* __restrict__ yout) {
   // stages: 128 KiB for one block a CU, or 64 and 72 KiB for two (with 6, so one block a CU, 2048 tokens x 4 of 90
   // experts of 1024 x 512 took 68.7 us, not 62.0, 8192 x 6 of 256 of 4096 x 2048 2104, not 1994)
   constexpr int NS = BM_T == 16 || BN_T == 8 ? 4 : 3;
@@ -836,7 +813,6 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
   }
 
   const float* wscale = reinterpret_cast<const float*>(blob + scale_off);
-  const float unit = (PHASE == 2 && HALF) ? wscale[N] : 1.f;
   // every scale first, so that their loads are in flight together
   f32x4_t sw[WN];
 #pragma unroll
@@ -848,10 +824,6 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
     const int mloc = mt * (16 * BM_T) + (wm * WM + j) * 16 + (lane & 15);
     const size_t row = (size_t)(it.y + min(mloc, it.z - 1));
     st[j] = bscale[(PHASE == 1 && src) ? (size_t)src[row] : row];
-    if constexpr (PHASE == 2 && HALF) {
-      if (mloc < it.z && nt == 0 && wn == 0 && lane < 16) factor[row] = st[j] / unit;  // once a row
-      st[j] = unit;
-    }
   }
 #pragma unroll
   for (int j = 0; j < WM; ++j) {
@@ -869,12 +841,8 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
       if constexpr (PHASE == 1)
         *reinterpret_cast<float2*>(hout + h_tile_at(row, ntile, lane >> 4, I)) =
             make_float2(swiglu(v[0], v[1]), swiglu(v[2], v[3]));
-      else if constexpr (HALF)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(yout) + row * H + 16 * ntile + 4 * (lane >> 4)) =
-            make_uint2(f32_to_f16_bits(v[0]) | (uint32_t)f32_to_f16_bits(v[1]) << 16,
-                       f32_to_f16_bits(v[2]) | (uint32_t)f32_to_f16_bits(v[3]) << 16);
       else
-        *reinterpret_cast<f32x4_t*>(static_cast<float*>(yout) + row * H + 16 * ntile + 4 * (lane >> 4)) = v;
+        *reinterpret_cast<f32x4_t*>(yout + row * H + 16 * ntile + 4 * (lane >> 4)) = v;
     }
   }
 }
@@ -938,13 +906,12 @@ __global__ __launch_bounds__(64 * kReqWaves) void requantise_h(const float* __re
   if (wave == 0 && lane < 16) sh[tile * 16 + lane] = rq.scale();
 }
 
-// out[t] = sum over j of w[t, j] y[pos[t, j]], j ascending, over the experts that have a slot. HALF: fp16 rows with a
-// factor each. A thread takes 8 columns, all of a token's rows in flight together (up to kAhead of them).
-// Bound by memory: 16384 tokens x 6 rows of 4096 in fp16 189 us, 5.0 TB/s.
+// out[t] = sum over j of w[t, j] y[pos[t, j]], j ascending, over the experts that have a slot.
+// A thread takes 8 columns, all of a token's rows in flight together (up to kAhead of them).
+// Bound by memory: each row of y is read once.
 constexpr int kAhead = 8;
-template <bool OUT_BF16, bool HALF, bool UNIFORM>
-__global__ __launch_bounds__(256) void int8_combine(const void* __restrict__ y, const float* __restrict__ factor,
-                                                    const int32_t* __restrict__ perm_pos,
+template <bool OUT_BF16, bool UNIFORM>
+__global__ __launch_bounds__(256) void int8_combine(const float* __restrict__ y, const int32_t* __restrict__ perm_pos,
                                                     const int32_t* __restrict__ topk_idx,
                                                     const float* __restrict__ topk_w,
                                                     const int32_t* __restrict__ slot_of, int n_slots, int k, int H,
@@ -957,36 +924,26 @@ __global__ __launch_bounds__(256) void int8_combine(const void* __restrict__ y, 
   if (t >= (size_t)T) return;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 < k; j0 += kAhead) {
-    u32x4_t v[kAhead][HALF ? 1 : 2];
+    f32x4_t v[kAhead][2];
     float w[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       w[u] = 0.f;
-#pragma unroll
-      for (int p = 0; p < (HALF ? 1 : 2); ++p) v[u][p] = u32x4_t{0u, 0u, 0u, 0u};
+      v[u][0] = v[u][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       if (j0 + u >= k) continue;
       const int e = topk_idx[t * k + j0 + u];
       const int slot = slot_of ? slot_of[e] : e;
       if (slot < 0 || slot >= n_slots) continue;
-      const size_t row = (size_t)perm_pos[t * k + j0 + u];
+      const float* row = y + (size_t)perm_pos[t * k + j0 + u] * H + n;
       w[u] = topk_w[t * k + j0 + u];
-      if constexpr (HALF) {
-        w[u] *= factor[row];
-        v[u][0] = ld16(static_cast<const uint16_t*>(y) + row * H + n);
-      } else {
-        v[u][0] = ld16(static_cast<const float*>(y) + row * H + n);
-        v[u][1] = ld16(static_cast<const float*>(y) + row * H + n + 4);
-      }
+      v[u][0] = *reinterpret_cast<const f32x4_t*>(row);
+      v[u][1] = *reinterpret_cast<const f32x4_t*>(row + 4);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
       if (j0 + u < k) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float x = HALF ? f16_bits_to_f32(v[u][0][c >> 1] >> (16 * (c & 1)) & 0xFFFFu)
-                               : __uint_as_float(v[u][HALF ? 0 : c >> 2][c & 3]);
-          acc[c] = fmaf(w[u], x, acc[c]);
-        }
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[u], v[u][c >> 2][c & 3], acc[c]);
       }
   }
   if constexpr (OUT_BF16) {
@@ -1052,11 +1009,10 @@ hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const fl
 // 3968 x 1920 with 256 77 / 99, with 512 138 / 123; 64 of 4096 x 2048 with 384 858 / 835, with 768 1589 / 1500.
 int tile_rows_for(int rows, int groups) { return (long long)rows >= 384ll * groups ? 256 : 128; }
 
-// The two products and the pass between them over planned entries (at most rows / tile + groups). factor: y's rows are
-// left in fp16 with one each; nullptr: fp32 rows.
+// The two products and the pass between them over planned entries (at most rows / tile + groups).
 hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src, int rows, int groups, int tile_rows,
                          const int32_t* n, const int4* entries, const char* slot_base, size_t slot_stride, int H, int I,
-                         float* h, uint8_t* hq, float* sh, void* y, float* factor, hipStream_t s) {
+                         float* h, uint8_t* hq, float* sh, float* y, hipStream_t s) {
   const Int8Layout L = int8_layout(H, I);
   const size_t most = rows / tile_rows + groups;  // entries
   // Less than a block a CU: 128 weight rows a block, twice the blocks (a call of 333 tokens x 5 of 20 experts of
@@ -1066,7 +1022,7 @@ hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src,
                            const int32_t* from, size_t mat, size_t scales) {
     const dim3 grid((unsigned)((most * ((N + columns - 1) / columns) + 7) / 8 * 8));
     hipLaunchKernelGGL(kernel, grid, dim3(512), 0, s, b, bs, from, n, entries, slot_base, slot_stride, mat, scales, N,
-                       K, H, I, h, y, factor);
+                       K, H, I, h, y);
     return hipGetLastError();
   };
   const auto up = [&](auto kernel, int columns) {
@@ -1075,19 +1031,15 @@ hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src,
   const auto down = [&](auto kernel, int columns) {
     return product(kernel, columns, H, I, hq, sh, nullptr, L.p2, L.p2s);
   };
-  hipError_t e = tile_rows == 256 ? up(int8_gemm<1, 16, false>, 256)
-                 : narrow(2 * I)  ? up(int8_gemm<1, 8, false, 8>, 128)
-                                  : up(int8_gemm<1, 8, false>, 256);
+  hipError_t e = tile_rows == 256 ? up(int8_gemm<1, 16>, 256)
+                 : narrow(2 * I)  ? up(int8_gemm<1, 8, 8>, 128)
+                                  : up(int8_gemm<1, 8>, 256);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(requantise_h, dim3((rows + 15) / 16), dim3(64 * kReqWaves), 0, s, h, I, hq, sh);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (factor != nullptr)
-    return tile_rows == 256 ? down(int8_gemm<2, 16, true>, 256)
-           : narrow(H)      ? down(int8_gemm<2, 8, true, 8>, 128)
-                            : down(int8_gemm<2, 8, true>, 256);
-  return tile_rows == 256 ? down(int8_gemm<2, 16, false>, 256)
-         : narrow(H)      ? down(int8_gemm<2, 8, false, 8>, 128)
-                          : down(int8_gemm<2, 8, false>, 256);
+  return tile_rows == 256 ? down(int8_gemm<2, 16>, 256)
+         : narrow(H)      ? down(int8_gemm<2, 8, 8>, 128)
+                          : down(int8_gemm<2, 8>, 256);
 }
 
 }  // namespace
@@ -1100,10 +1052,6 @@ hipError_t launch_pack_int8(int H, int I, const void* Q1, const void* Q3, const 
                      static_cast<const int8_t*>(Q1), static_cast<const int8_t*>(Q3), static_cast<const int8_t*>(Q2),
                      static_cast<const float*>(S1), static_cast<const float*>(S3), static_cast<const float*>(S2), H, I,
                      static_cast<char*>(blob), L);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pack_int8_unit, dim3(1), dim3(256), 0, s, static_cast<const float*>(S2), H, I,
-                     reinterpret_cast<float*>(static_cast<char*>(blob) + L.unit));
   return hipGetLastError();
 }
 
@@ -1145,7 +1093,7 @@ hipError_t launch_ffn_int8_list(const void* x, const int32_t* perm_src, const in
       if ((e = hipGetLastError()) == hipSuccess)
         // rows_total: the pass between the products covers every row of the workspace, listed or not
         e = gemm_products(xq, sx, nullptr, rows_total, wa.n, tile, count, entries, slot_base, slot_stride, H, I, h,
-                          reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, nullptr, s);
+                          reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
     }
     if (e != hipSuccess) return e;
   }
@@ -1179,8 +1127,6 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   float *sx = reinterpret_cast<float*>(b + w.sx), *h = reinterpret_cast<float*>(b + w.h);
   const uint16_t* xb = static_cast<const uint16_t*>(x);
   const bool gemm = int8_gemm_supported(H, I) && int8_gemm_pays(rows, E);
-  const bool half = gemm && out_bf16;
-  float* factor = half ? h : nullptr;  // over h, which is codes by then
   const int groups = std::min(E, rows), tile = gemm ? tile_rows_for(rows, groups) : 0;
   int32_t* n = reinterpret_cast<int32_t*>(b + w.plan);
   int4* entries = reinterpret_cast<int4*>(b + w.plan + 256);
@@ -1197,18 +1143,17 @@ hipError_t launch_experts_int8(const void* x, int T, int k, int E, const int32_t
   }
   if (gemm)
     e = gemm_products(xq, sx, perm_src, rows, groups, tile, n, entries, slot_base, slot_stride, H, I, h,
-                      reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, factor, s);
+                      reinterpret_cast<uint8_t*>(b + w.hq), reinterpret_cast<float*>(b + w.sh), y, s);
   else
     e = decode_products(DevItems{n, entries}, groups, xq, sx, perm_src, slot_base, slot_stride, H, I, h, y, s);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)(((size_t)T * (H / 8) + 255) / 256));
   const auto combine = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, y, factor, perm_pos, topk_idx, topk_w, slot_of, n_slots, k, H, T,
-                       out);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, y, perm_pos, topk_idx, topk_w, slot_of, n_slots, k, H, T, out);
     return hipGetLastError();
   };
-  if (half) return H % 512 == 0 ? combine(int8_combine<true, true, true>) : combine(int8_combine<true, true, false>);
-  return out_bf16 ? combine(int8_combine<true, false, false>) : combine(int8_combine<false, false, false>);
+  if (!out_bf16) return combine(int8_combine<false, false>);
+  return gemm && H % 512 == 0 ? combine(int8_combine<true, true>) : combine(int8_combine<true, false>);
 }
 
 }  // namespace moe
