@@ -501,12 +501,11 @@ __device__ __forceinline__ bool select_row(float (&l)[VE], const float* __restri
 #pragma unroll
   for (int v = 1; v < VE; ++v) top = fmaxf(top, x[v]);
   top = kept && ok > 0 ? top : -INFINITY;
-  const auto reach = [&](float at_least) {
-    const float T = kept && ok > 0 ? at_least : INFINITY;  // an infinite value is not decided here
+  const auto reach = [&](float T) {  // counts what is picked below, no more: a dropped group's logit may be infinite
     int n = 0;
 #pragma unroll
     for (int v = 0; v < VE; ++v) n += x[v] >= T ? 1 : 0;
-    return n;
+    return kept && ok > 0 ? n : 0;
   };
   float hi = row_max(top), lo = below_all(-row_max(top > -INFINITY ? -top : -INFINITY), hi);
   const int doubts = row_sum(unsure ? 1 : 0);
