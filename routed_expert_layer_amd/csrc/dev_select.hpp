@@ -100,8 +100,12 @@ __device__ __forceinline__ float score32(float l, float m, float iz, int score) 
 }
 // Bounds between which another group's rank may come before one of `rank` or not. Logits 1e-6 apart have different
 // 64-bit scores up to 20 (a sigmoid's distance from 1) and down to -600 (of the largest, for a softmax).
+// By c, a rank r of one c or of two, a + b, of magnitudes up to M: each c is off by kErr / 2 and its rounding 2^-24 |c|,
+// their sum by 2^-24 |r|, so r by kErr + 2^-22 M at most. Where M <= 1 + 2 |r| (else rank_cancels) that is below
+// 1.5 kErr + 2^-21 |r|. Two ranks r, o then differ truly if |r - o| > 3 kErr + 2^-21 (|r| + |o|): d covers it for
+// |o| <= 2 |r|, and a larger |o| is itself twice that far from r.
 __device__ __forceinline__ void rank_bounds(float rank, bool by_c, int score, float m, float& above, float& below) {
-  const float d = by_c ? 4.f * kErr + 0x1p-21f * fabsf(rank) : 1e-6f;
+  const float d = by_c ? 8.f * kErr + 0x1p-19f * fabsf(rank) : 1e-6f;
   above = by_c ? rank + d : fmaxf(rank + d, score == 0 ? m - 600.f : -600.f);
   below = rank - d;
 }
@@ -151,9 +155,10 @@ template <int D, typename F>
 __device__ __forceinline__ void top2_step(Top2<F>& t, int lanes, bool two) {
   if (lanes > D) t.merge(across<D>(t.a), two ? across<D>(t.b) : t.b);
 }
-// A group's rank, on each of its lanes, from the lanes' values (`ok` of them first).
+// A group's rank, on each of its lanes, from the lanes' values (`ok` of them first). cancels: its two c are of opposite
+// signs (balances that pin one expert and mask another) and their sum says nothing of the error that it carries.
 template <int WIDTH, int VE, typename F>
-__device__ __forceinline__ F group_rank(const F (&c)[VE], int ok, int lanes, bool two) {
+__device__ __forceinline__ F group_rank(const F (&c)[VE], int ok, int lanes, bool two, bool& cancels) {
   Top2<F> t{-INFINITY, -INFINITY};
 #pragma unroll
   for (int v = 0; v < VE; ++v)
@@ -167,6 +172,7 @@ __device__ __forceinline__ F group_rank(const F (&c)[VE], int ok, int lanes, boo
     top2_step<32>(t, lanes, two);
   }
   const F r = two ? t.a + t.b : t.a;
+  cancels = two && fmax(fabs(t.a), fabs(t.b)) > 1 + 2 * fabs(r);
   return isnan(r) ? (F)-INFINITY : r;  // of infinite balances of either sign
 }
 // How many groups come before this lane's: larger ranks, and equal ones of lower groups.
@@ -197,7 +203,8 @@ __device__ __forceinline__ void select_exact(const float (&l)[VE], int ok, int b
   }
   bool kept = true;
   if (g.topk_group < g.n_group) {
-    const double rank = group_rank<64>(c, ok, lanes, g.group_top == 2 && per > 1);
+    bool cancels;  // not of interest in 64 bits
+    const double rank = group_rank<64>(c, ok, lanes, g.group_top == 2 && per > 1, cancels);
     kept = groups_before(rank, group, lanes, g.n_group) < g.topk_group;
   }
 #pragma unroll
@@ -272,7 +279,8 @@ __device__ __forceinline__ void select_token(const float* logits, const float* b
   bool unsure = false, kept = true;
   if (drops) {
     const bool by_c = bal != nullptr || two;
-    const float rank = by_c ? group_rank<64>(c, ok, lanes, two) : group_rank<64>(l, ok, lanes, false);
+    bool cancels;
+    const float rank = by_c ? group_rank<64>(c, ok, lanes, two, cancels) : group_rank<64>(l, ok, lanes, false, cancels);
     float above, below;  // groups surely before this one, and groups that may be
     rank_bounds(rank, by_c, g.score, m, above, below);
     int sure = 0, may = -1;  // its own rank is one of the latter
@@ -282,7 +290,7 @@ __device__ __forceinline__ void select_token(const float* logits, const float* b
       may += o >= below ? 1 : 0;
     }
     kept = may < g.topk_group;
-    unsure = !kept && sure < g.topk_group;
+    unsure = cancels || (!kept && sure < g.topk_group);
     unsure = unsure || (kept && !(by_c || g.score == 0 ? rank < INFINITY : rank < 20.f));
     unsure = unsure && group < g.n_group;
   }
@@ -454,7 +462,7 @@ __device__ __forceinline__ bool select_row(float (&l)[VE], const float* __restri
   }
   // x: the values that decide
   float x[VE];
-  bool kept = true, unsure = false;
+  bool kept = true, unsure = false, cancels = false;
   if (bal != nullptr || (two && drops)) {
     const float iz = (float)(1.0 / z);
     float c[VE];
@@ -465,12 +473,12 @@ __device__ __forceinline__ bool select_row(float (&l)[VE], const float* __restri
       if (bal != nullptr) c[v] = v < ok ? s + bal[base + v] : -INFINITY;
     }
     float rank = 0.f;
-    if (drops) rank = group_rank<16>(c, ok, lanes, two);
+    if (drops) rank = group_rank<16>(c, ok, lanes, two, cancels);
 #pragma unroll
     for (int v = 0; v < VE; ++v) x[v] = bal != nullptr ? c[v] : l[v];
     most = rank;
   } else {
-    if (drops) most = group_rank<16>(l, ok, lanes, false);
+    if (drops) most = group_rank<16>(l, ok, lanes, false, cancels);
 #pragma unroll
     for (int v = 0; v < VE; ++v) x[v] = l[v];
   }
@@ -493,7 +501,7 @@ __device__ __forceinline__ bool select_row(float (&l)[VE], const float* __restri
         }
     }
     kept = may < g.topk_group;
-    unsure = !kept && sure < g.topk_group;
+    unsure = cancels || (!kept && sure < g.topk_group);
     unsure = unsure || (kept && !(by_c || g.score == 0 ? rank < INFINITY : rank < 20.f));
     unsure = unsure && group < g.n_group;
   }

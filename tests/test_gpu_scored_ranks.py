@@ -26,6 +26,30 @@ SIZES = [10, 16, 48, 64, 300, 5000, 16400]
 
 @pytest.mark.parametrize("T", SIZES)
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_group_ranks_that_cancel(L, T, score):
+    """Balances that pin one expert of a group and mask another: the group's two largest scores are near +B and -B, and
+    their sum in 32 bits is off by up to 2^-24 B, far more than it is relative to itself."""
+    g = torch.Generator(device=dev).manual_seed(T)
+    for E, G, keep, k in ((16, 8, 4, 4), (64, 8, 3, 5), (256, 8, 4, 6)):
+        if E * T > 2000000:  # the statement in Python takes a second for 3 million scores
+            continue
+        l = torch.randn((T, E), generator=g, device=dev)
+        for B in (1e3, 1e5, 1e6):
+            b = 0.1 * torch.randn(E, generator=g, device=dev)
+            groups = b.view(G, E // G)
+            groups[:, 0] += B
+            groups[:, 1:] -= B
+            run(L, l, k, f"{score} E{E} B{B:g}", score=score, n_group=G, topk_group=keep, group_top=2, balance=b)
+        # one such group among ordinary ones, its rank near theirs
+        b = 0.1 * torch.randn(E, generator=g, device=dev)
+        groups = b.view(G, E // G)
+        groups[2, 0] += 1e6
+        groups[2, 1:] -= 1e6
+        run(L, l, k, f"{score} E{E} one group", score=score, n_group=G, topk_group=keep, group_top=2, balance=b)
+
+
+@pytest.mark.parametrize("T", SIZES)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_infinite_logits_in_groups_that_are_dropped(L, T, score):
     """With the two best ranking a group, one infinite logit (a score of 1) does not keep it: its expert is not chosen,
     and the others' choice is as without it."""
