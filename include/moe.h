@@ -144,7 +144,9 @@ int moe_route_noalloc(const void* x, int dtype, const void* Wr, const float* bia
  * Limits: 1 <= k <= min(E, 16), E <= 1024, n_group <= 64 dividing E,
  * 1 <= topk_group <= n_group, k <= topk_group * (E / n_group), group_top 1 or
  * 2, scale finite; balance device fp32 [E] or NULL. The gate is read during
- * the call; its balance array must stay until the work has run. T = 0 writes
+ * the call; its balance array must stay until the work has run (a graph's:
+ * until its last replay; a decoder's: until the steps and graphs enqueued
+ * under that gate have run, also after another gate is set). T = 0 writes
  * counts = offsets = 0. Errors: MOE_EINVAL, MOE_EHIP.
  *
  * moe_decoder_set_gate, moe_device_decoder_set_gate: the decoder's later steps

@@ -46,7 +46,9 @@ class DecoderBuffers(ctypes.Structure):
 
 class Gate(ctypes.Structure):
     """moe_gate_t: softmax or sigmoid scores, a balance bias for the choice alone (GPU fp32 tensor [E] or None, kept
-    alive here), groups of experts of which each token keeps topk_group, and the weights' renormalisation and scale."""
+    alive here until it is replaced), groups of experts of which each token keeps topk_group, and the weights'
+    renormalisation and scale. The library's calls read the balance when their work runs, and a captured one at every
+    replay: the tensor has to stay until then. Decoders and PrefillLayer keep the ones that they were given."""
     _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
                 ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("_balance", ctypes.c_void_p)]
@@ -55,9 +57,17 @@ class Gate(ctypes.Structure):
         names = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
         if isinstance(score, str) and score not in names:
             raise ValueError(f"unknown score {score!r}")
-        super().__init__(names.get(score, score), n_group, topk_group, group_top, int(bool(renorm)), scale,
-                         None if balance is None else _gpu(balance, _device(balance, "balance"), "float32", "balance"))
+        super().__init__(names.get(score, score), n_group, topk_group, group_top, int(bool(renorm)), scale)
         self.balance = balance
+
+    @property
+    def balance(self):
+        return self._tensor
+
+    @balance.setter
+    def balance(self, t):
+        self._balance = None if t is None else _gpu(t, _device(t, "balance"), "float32", "balance")
+        self._tensor = t
 
 
 class MoEError(RuntimeError):
@@ -248,6 +258,13 @@ def _gate_ref(gate, E=None, dev=None):
     if b is not None and ((E is not None and b.shape != (E,)) or (dev is not None and b.get_device() != dev)):
         raise ValueError(f"balance: {E} entries on the call's GPU are needed, not {tuple(b.shape)} on {b.device}")
     return ctypes.byref(gate)
+
+
+def keep_balance(kept, gate):
+    """Adds the balance of a gate (or None) to a dict of those that queued or captured work may read. To change values
+    often, write them into the tensor that is kept, in the order of the work that reads it."""
+    if gate is not None and gate.balance is not None:
+        kept[id(gate.balance)] = gate.balance
 
 
 def _nbytes(t):
@@ -556,6 +573,7 @@ class MoeDecoder:
         if not self.h:
             raise MoEError(st.value, _lib.moe_last_error().decode())
         self.cache = cache
+        self.balances = {}  # of every gate set so far
 
     def close(self):
         if self.h and _lib is not None:  # module globals may be gone at interpreter exit
@@ -611,14 +629,17 @@ def moe_prefill_layer_scored(x, Wr, bias, gate, k, I, wfmt, layer_base, blob_str
 
 
 def moe_decoder_set_gate(dec, gate, E=None):
-    """gate: a Gate (its balance tensor, of E entries when given, is kept alive with the decoder) or None for moe_route's
-    softmax."""
+    """gate: a Gate (copied; its balance tensor, of E entries when given, is kept alive as long as the decoder) or None
+    for moe_route's softmax."""
     _check(_lib.moe_decoder_set_gate(dec.h, _gate_ref(gate, E)), "moe_decoder_set_gate")
+    keep_balance(dec.balances, gate)
     dec.gate = gate
 
 
 def moe_device_decoder_set_gate(dec, gate, E=None):
+    """As moe_decoder_set_gate."""
     _check(_lib.moe_device_decoder_set_gate(dec.h, _gate_ref(gate, E)), "moe_device_decoder_set_gate")
+    keep_balance(dec.balances, gate)
     dec.gate = gate
 
 
@@ -671,6 +692,7 @@ class MoeDeviceDecoder:
                                                 ctypes.byref(st))
         if not self.h:
             raise MoEError(st.value, _lib.moe_last_error().decode())
+        self.balances = {}  # of every gate set so far
 
     def close(self):
         if self.h and _lib is not None:

@@ -195,7 +195,7 @@ class DecodeLayer:
         L.moe_cache_set_split(self.cache, rate_gpu, rate_cpu)
 
     def set_gate(self, gate):
-        """Later steps choose experts under this Gate (None: softmax over the chosen logits)."""
+        """Later steps choose experts under this Gate as it is now (None: softmax over the chosen logits)."""
         L.moe_decoder_set_gate(self.dec, gate, self.E)
 
     def measure_rates(self, layer=0, n=4, rows=None):
@@ -281,8 +281,8 @@ class DeviceDecodeLayer:
         return o
 
     def set_gate(self, gate):
-        """Later steps choose experts under this Gate (None: softmax over the chosen logits); a captured graph keeps
-        the gate it was captured with."""
+        """Later steps choose experts under this Gate as it is now (None: softmax over the chosen logits); a captured
+        graph keeps the gate it was captured with, and the layer its balance."""
         L.moe_device_decoder_set_gate(self.dec, gate, self.E)
 
     @staticmethod
@@ -319,7 +319,7 @@ class PrefillLayer:
     combine; nothing waits for the GPU. With `gate` (a Gate), its choice and weights; int8 experts run moe_experts."""
 
     def __init__(self, H, I, E, k, T, stride, device="cuda", keep_logits=False, wfmt=L.MOE_W_BF16, gate=None):
-        self.gate = gate
+        self.gate, self.balances = gate, {}
         self.H, self.I, self.E, self.k, self.stride, self.wfmt = H, I, E, k, stride, wfmt
         self.rb = RouteBuffers(T, H, E, k, device, keep_logits)
         rows = T * k
@@ -327,6 +327,10 @@ class PrefillLayer:
         self.ffn_ws = torch.empty(L.moe_ffn_workspace_size(rows, H, I, wfmt), dtype=torch.uint8, device=device)
         self.out = torch.empty((T, H), dtype=torch.float32, device=device)
         self.bufs = L.decoder_buffers(self.rb.buffer_dict(self.y_perm, self.ffn_ws))
+
+    def keep_balance(self):
+        """The balances of the gates of every call so far stay with the layer: queued or captured calls read them."""
+        L.keep_balance(self.balances, self.gate)
 
     def forward(self, x, Wr, bias, layer_base, stream=None, timer=None):
         """Enqueue the layer on the stream; returns the output tensor (valid once the stream reaches it).
@@ -338,6 +342,7 @@ class PrefillLayer:
         if self.gate is not None:
             if timer is not None:
                 raise ValueError("the timed form of the layer takes no gate")
+            self.keep_balance()
             L.moe_prefill_layer_scored(x, Wr, bias, self.gate, self.k, self.I, self.wfmt, layer_base, self.stride,
                                        self.bufs, self.out[:T], s)
             return self.out[:T]
