@@ -251,11 +251,12 @@ def _routing_args(dev, T, k, E, topk_idx, topk_w, counts, offsets, perm_src, per
             _gpu(perm_src, dev, "int32", "perm_src"), _gpu(perm_pos, dev, "int32", "perm_pos", tk))
 
 
-def _gate_ref(gate, E=None, dev=None):
+def _gate_ref(gate, E, dev):
+    """A gate for a call over E experts on GPU `dev`."""
     if gate is None:
         return None
     b = gate.balance
-    if b is not None and ((E is not None and b.shape != (E,)) or (dev is not None and b.get_device() != dev)):
+    if b is not None and (b.shape != (E,) or b.get_device() != dev):
         raise ValueError(f"balance: {E} entries on the call's GPU are needed, not {tuple(b.shape)} on {b.device}")
     return ctypes.byref(gate)
 
@@ -336,10 +337,10 @@ def moe_route_scored(x, Wr, bias, gate, k, topk_idx, topk_w, logits, counts, off
     """moe_route with the choice and the weights of a Gate."""
     T, H = x.shape
     E = Wr.shape[1]
-    _check(_lib.moe_route_scored(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias), _gate_ref(gate, E), T, H, E, k,
-                                 _dptr(topk_idx), _dptr(topk_w), _dptr(logits), _dptr(counts), _dptr(offsets),
-                                 _dptr(perm_src), _dptr(perm_pos), _dptr(workspace), _nbytes(workspace),
-                                 _stream(stream)), "moe_route_scored")
+    _check(_lib.moe_route_scored(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias),
+                                 _gate_ref(gate, E, x.get_device()), T, H, E, k, _dptr(topk_idx), _dptr(topk_w),
+                                 _dptr(logits), _dptr(counts), _dptr(offsets), _dptr(perm_src), _dptr(perm_pos),
+                                 _dptr(workspace), _nbytes(workspace), _stream(stream)), "moe_route_scored")
 
 
 # ---------------------------------------------------------------------------
@@ -573,6 +574,7 @@ class MoeDecoder:
         if not self.h:
             raise MoEError(st.value, _lib.moe_last_error().decode())
         self.cache = cache
+        self.E, self.gpu = E, bufs["ffn_ws"].get_device()
         self.balances = {}  # of every gate set so far
 
     def close(self):
@@ -623,22 +625,25 @@ def moe_prefill_layer_scored(x, Wr, bias, gate, k, I, wfmt, layer_base, blob_str
     """moe_prefill_layer under a Gate."""
     T, H = x.shape
     E = Wr.shape[1]
-    _check(_lib.moe_prefill_layer_scored(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias), _gate_ref(gate, E), T, H, E,
-                                         k, I, wfmt, _dptr(layer_base), blob_stride, ctypes.byref(bufs), _dptr(out),
-                                         _dtype_code(out), _stream(stream)), "moe_prefill_layer_scored")
+    _check(_lib.moe_prefill_layer_scored(_dptr(x), _dtype_code(x), _dptr(Wr), _dptr(bias),
+                                         _gate_ref(gate, E, x.get_device()), T, H, E, k, I, wfmt, _dptr(layer_base),
+                                         blob_stride, ctypes.byref(bufs), _dptr(out), _dtype_code(out),
+                                         _stream(stream)), "moe_prefill_layer_scored")
 
 
 def moe_decoder_set_gate(dec, gate, E=None):
-    """gate: a Gate (copied; its balance tensor, of E entries when given, is kept alive as long as the decoder) or None
-    for moe_route's softmax."""
-    _check(_lib.moe_decoder_set_gate(dec.h, _gate_ref(gate, E)), "moe_decoder_set_gate")
+    """gate: a Gate (copied; its balance tensor is kept alive as long as the decoder) or None for moe_route's softmax. E
+    is the decoder's own."""
+    ref = _gate_ref(gate, dec.E, dec.gpu)
+    _check(_lib.moe_decoder_set_gate(dec.h, ref), "moe_decoder_set_gate")
     keep_balance(dec.balances, gate)
     dec.gate = gate
 
 
 def moe_device_decoder_set_gate(dec, gate, E=None):
     """As moe_decoder_set_gate."""
-    _check(_lib.moe_device_decoder_set_gate(dec.h, _gate_ref(gate, E)), "moe_device_decoder_set_gate")
+    ref = _gate_ref(gate, dec.E, dec.gpu)
+    _check(_lib.moe_device_decoder_set_gate(dec.h, ref), "moe_device_decoder_set_gate")
     keep_balance(dec.balances, gate)
     dec.gate = gate
 
@@ -692,6 +697,7 @@ class MoeDeviceDecoder:
                                                 ctypes.byref(st))
         if not self.h:
             raise MoEError(st.value, _lib.moe_last_error().decode())
+        self.E, self.gpu = E, bufs["ffn_ws"].get_device()
         self.balances = {}  # of every gate set so far
 
     def close(self):

@@ -17,7 +17,7 @@ def L():
 
 class Tensor:
     """A GPU tensor's interface, as far as the binding asks for it."""
-    dtype = torch.float32
+    dtype, is_cuda = torch.float32, True
 
     def __init__(self, *shape, gpu=0, at=4096):
         self.shape, self.gpu, self.at, self.device = shape, gpu, at, f"cuda:{gpu}"
@@ -120,6 +120,36 @@ def test_prefill_layer_keeps_its_balances(L, calls):
     pl.keep_balance()
     gc.collect()
     assert ref() is not None and len(pl.balances) == 2
+
+
+@pytest.mark.parametrize("bad", [dict(shape=(7,)), dict(shape=(9,)), dict(shape=(8, 1)), dict(shape=(8,), gpu=1)],
+                         ids=lambda d: "-".join(f"{k}={v}" for k, v in d.items()))
+def test_a_balance_of_another_size_or_gpu_is_refused(L, calls, bad):
+    """By every entry point that takes a gate, before the library is called."""
+    E, T, k, H = 8, 4, 2, 64
+    g = L.Gate(balance=Tensor(*bad["shape"], gpu=bad.get("gpu", 0)))
+    good = L.Gate(balance=Tensor(E))
+    out = Tensor(1)
+    xw = [Tensor(T, H), Tensor(H, E)]
+
+    def scored(gate):
+        L.moe_route_scored(*xw, None, gate, k, out, out, None, out, out, out, out, out)
+
+    def prefill(gate):
+        L.moe_prefill_layer_scored(*xw, None, gate, k, 128, L.MOE_W_BF16, out, 4096, L.DecoderBuffers(), out)
+
+    entries = [scored, prefill]
+    for kind in ("host", "device"):
+        d, set_gate = decoder(L, kind, E)
+        entries.append(lambda gate, d=d, f=set_gate: f(d, gate))
+        entries.append(lambda gate, d=d, f=set_gate: f(d, gate, gate.balance.shape[0]))
+    for call in entries:
+        del calls[:]
+        with pytest.raises(ValueError, match="balance"):
+            call(g)
+        assert calls == []
+        call(good)
+        assert len(calls) == 1
 
 
 @pytest.mark.gpu
