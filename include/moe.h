@@ -568,7 +568,8 @@ int moe_clock_record(unsigned long long* sums);
  *   least S_new * slot_stride bytes) every kept entry into it; the decoder
  *   then uses that buffer (free the old one once the stream has passed the
  *   copies). slot_base NULL keeps the buffer, which must then hold S_new
- *   slots. Errors as moe_cache_resize, EHIP.
+ *   slots. Errors as moe_cache_resize, EHIP; EINVAL for int8 experts with a
+ *   slot_base off 16 bytes (nothing has changed then).
  * ------------------------------------------------------------------------ */
 typedef struct moe_decoder moe_decoder_t;
 typedef struct {
@@ -708,7 +709,8 @@ int moe_cpu_threads(void);
  *   safe point), plans on the host, copies the blobs as moe_decoder_resize
  *   does, rewrites the tables (reallocated when S changes), and waits again.
  *   S_new must stay >= min(E, k*T_max). Graphs captured before a resize read
- *   the old tables and buffer: capture again. Errors: ECAPACITY, EHIP, ENOMEM.
+ *   the old tables and buffer: capture again. Errors: ECAPACITY, EHIP, ENOMEM,
+ *   EINVAL as moe_decoder_resize.
  * moe_device_decoder_clear_trace, moe_device_decoder_slot_of: as for the host
  *   cache. stats, trace and slot_of read GPU memory with blocking copies: call
  *   them once the stream's steps have completed.

@@ -575,6 +575,8 @@ int moe_decoder_set_gate(moe_decoder_t* d, const moe_gate_t* gate) {
 
 int moe_decoder_resize(moe_decoder_t* d, int S_new, void* slot_base, void* stream) {
   if (!d) return dfail(MOE_EINVAL, "moe_decoder_resize: null decoder");
+  if (d->wfmt == MOE_W_INT8 && !moe::aligned16(slot_base))
+    return dfail(MOE_EINVAL, "moe_decoder_resize: int8 experts need 16-byte aligned slots");
   const int S_old = moe_cache_capacity(d->cache);
   int n_layers = 0;
   (void)moe_cache_layers(d->cache, &n_layers);

@@ -242,6 +242,8 @@ int moe_device_decoder_set_gate(moe_device_decoder_t* d, const moe_gate_t* gate)
 
 int moe_device_decoder_resize(moe_device_decoder_t* d, int S_new, void* slot_base, void* stream) {
   if (!d) return dd_fail(MOE_EINVAL, "moe_device_decoder_resize: null decoder");
+  if (d->wfmt == MOE_W_INT8 && !moe::aligned16(slot_base))
+    return dd_fail(MOE_EINVAL, "moe_device_decoder_resize: int8 experts need 16-byte aligned slots");
   if (S_new < d->max_items)
     return dd_fail(MOE_ECAPACITY, "moe_device_decoder_resize: S must stay at least min(E, k*T_max) = %d",
                    d->max_items);
