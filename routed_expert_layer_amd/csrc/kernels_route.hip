@@ -554,9 +554,8 @@ RoutePlan plan_route(int T, int H, int E, bool bf16) {
     p.partial_bytes = align_up((size_t)p.nsplit * T * E * sizeof(float), 256);
   }
   p.hist_off = p.partial_bytes;
-  const int E4 = (E + 3) / 4 * 4;  // a scored gate counts four experts to a word
-  p.bits_off = align_up(p.hist_off + (size_t)nchunks * E4 * sizeof(int32_t), 256);
-  p.wrt_off = align_up(p.bits_off + (size_t)nchunks * E4 * sizeof(uint64_t), 256);
+  p.bits_off = align_up(p.hist_off + (size_t)nchunks * E * sizeof(int32_t), 256);
+  p.wrt_off = align_up(p.bits_off + (size_t)nchunks * E * sizeof(uint64_t), 256);
   p.total = p.wrt_off + (p.mode == 1 ? align_up((size_t)H * E * 2, 256) : 0) + 256;
   return p;
 }
@@ -630,7 +629,7 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
       hipLaunchKernelGGL(router_partial_kernel<false>, grid, dim3(256), 0, s, x, Wr, T, H, E, p.hchunk, partial);
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
-  if (gate != nullptr)
+  if (gate != nullptr)  // hist_off to wrt_off + 256 hold what select_workspace_bytes asks for
     return launch_select(partial, p.nsplit, bias, logits, *gate, T, E, k, topk_idx, topk_w, counts, offsets, perm_src,
                          perm_pos, w + p.hist_off, s, counts_mirror);
   hipLaunchKernelGGL(topk_kernel, dim3((T + 3) / 4), dim3(256), 0, s, partial, p.nsplit, bias,

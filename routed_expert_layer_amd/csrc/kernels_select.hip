@@ -284,8 +284,10 @@ struct SelectWs {
   size_t hist, bits, bytes;
 };
 SelectWs select_ws(int T, int E) {
-  // of 64-token chunks; the byte counts of 16-token chunks take as much as the 32-bit ones
-  const size_t n = (size_t)((T + 63) / 64) * ((E + 3) / 4 * 4);
+  // Counts and masks of 64-token chunks, as moe_route's scratch has them. The byte counts of up to kFewTokens lie over
+  // both, four experts to a word: of n 64-token chunks' worth at most 4 n (E + 3) bytes (16-token chunks, n <= 64) or
+  // 2 n (E + 3) (32-token ones), within the 12 n E + 256 for every E >= 1.
+  const size_t n = (size_t)((T + 63) / 64) * E;
   SelectWs w{};
   w.hist = 0;
   w.bits = align_up(n * 4, 256);
