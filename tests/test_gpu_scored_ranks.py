@@ -70,3 +70,15 @@ def test_infinite_logits_in_groups_that_are_dropped(L, T, score):
             if k <= keep * per:
                 for top in (2, 1):
                     run(L, l, k, f"{score} E{E} k{k} top{top}", score=score, n_group=G, topk_group=keep, group_top=top)
+
+
+@pytest.mark.parametrize("T,E", [(64, 64), (5000, 64), (5000, 256), (16384, 64), (16400, 64), (16400, 256)])
+def test_near_ties_in_long_batches(L, T, E):
+    """Biased scores of every token within about 2^-24 of one value, so that 32 bits decide next to no token and several
+    of a wave go through 64 bits, one after another."""
+    g = torch.Generator(device=dev).manual_seed(T + E)
+    l0 = torch.randn(E, generator=g, device=dev)
+    b = (0.75 - 1.0 / (1.0 + torch.exp(-l0.double()))).float()
+    l = l0 + 1e-6 * torch.randn((T, E), generator=g, device=dev)
+    for G, keep, top in ((1, 1, 1), (8, 3, 2)) if T * E < 2000000 else ((8, 3, 2),):
+        run(L, l, 6, f"near ties g{G}", score="sigmoid", n_group=G, topk_group=keep, group_top=top, balance=b)
