@@ -617,7 +617,9 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
     }
     return hipGetLastError();
   }
-  if (p.mode == 1) {
+  if (T == 0) {
+    // no products and no choices; the grouping below writes counts and offsets of nothing
+  } else if (p.mode == 1) {
     void* wrt = w + p.wrt_off;
     if ((err = launch_pack_fragments(Wr, H, E, wrt, s)) != hipSuccess) return err;
     if ((err = launch_router_gemm(x, wrt, T, H, E, partial, p.nsplit, s)) != hipSuccess) return err;
@@ -632,11 +634,11 @@ hipError_t launch_route(const void* x, bool bf16, const void* Wr, const float* b
   if (gate != nullptr)  // hist_off to wrt_off + 256 hold what select_workspace_bytes asks for
     return launch_select(partial, p.nsplit, bias, logits, *gate, T, E, k, topk_idx, topk_w, counts, offsets, perm_src,
                          perm_pos, w + p.hist_off, s, counts_mirror);
-  hipLaunchKernelGGL(topk_kernel, dim3((T + 3) / 4), dim3(256), 0, s, partial, p.nsplit, bias,
-                     T, E, k, topk_idx, topk_w, logits);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
   const int nchunks = (T + 63) / 64;
   if (nchunks > 0) {
+    hipLaunchKernelGGL(topk_kernel, dim3((T + 3) / 4), dim3(256), 0, s, partial, p.nsplit, bias,
+                       T, E, k, topk_idx, topk_w, logits);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
     hipLaunchKernelGGL(chunk_masks_kernel, dim3(nchunks), dim3(256), (size_t)E * 8, s, topk_idx, T, E, k, nchunks, bits,
                        hist);
     if ((err = hipGetLastError()) != hipSuccess) return err;
