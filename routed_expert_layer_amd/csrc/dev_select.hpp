@@ -12,13 +12,15 @@
 // their logits, which are in the same order, where there is no balance), forms
 // the 64-bit scores of those alone, one a lane, orders them, and keeps the
 // choice if all are above the threshold by more than the 32-bit scores' error.
-// Otherwise (about one token in a thousand) it chooses again from 64-bit
-// scores of every expert.
-// Bound by instruction issue in long batches (16384 tokens of 256 experts in 8
-// groups: 25 us, 0.7 TB/s of logits, 61% of the VALU's issue slots; choosing
-// from 64-bit scores of every expert took 86 us a call): more than half of a
-// token's instructions do not depend on how many experts a lane holds, so a
-// token has a row of 16 lanes there (select_row), four tokens to a wave. In
+// Otherwise it chooses again from 64-bit scores of every expert (one token in
+// 1600 of 256 experts with a balance, in 3600 with groups too, of which the row
+// form below hands on one in 1400; none of 82000 without a balance).
+// Long batches are instructions and the latency of their steps, not bytes
+// (16384 tokens of 256 experts in 8 groups: 25 us, 0.7 TB/s of logits, 61% of
+// the VALU's issue slots at four waves a SIMD; a first kernel that formed 64-bit
+// scores of every expert took 86 us a call): more than half of a token's
+// instructions do not depend on how many experts a lane holds, so a token has
+// a row of 16 lanes there (select_row), four tokens to a wave. In
 // short ones latency counts and a token has a wave (select_token; 6.8 us in the
 // kernel for one token of 256).
 #pragma once

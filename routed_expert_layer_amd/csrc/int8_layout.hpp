@@ -37,9 +37,9 @@ inline bool int8_shape_ok(int H, int I) {
 }
 // Whether `rows` rows over `groups` experts run the tiled GEMM: from 4 rows an expert on. The decode kernels read a
 // weight once for every 16 rows of its expert too, but with fewer rows in flight and each block forming h's codes for
-// itself. Measured, decode against GEMM, us: 64 experts of 4096 x 2048, 2.3 rows each 222 / 253, 6 rows 285 / 265; 16 of
-// 2048 x 768, 4 rows 30.1 / 29.9, 16 rows 49 / 31; 8 of 3968 x 1920, 4 rows 47.0 / 47.8, 32 rows 123 / 50; 96 of
-// 1024 x 512, 2 rows 39.4 / 41.6, 3.3 rows 50.8 / 41.7; 48 of 2048 x 1024, 2 rows 51 / 63, 3.3 rows 63 / 65.
+// itself. Measured, decode against GEMM, us: 64 experts of 4096 x 2048, 2.3 rows each 222 / 252, 6 rows 285 / 267; 16 of
+// 2048 x 768, 4 rows 30.2 / 28.8, 16 rows 49 / 30; 8 of 3968 x 1920, 4 rows 46.7 / 47.3, 32 rows 123 / 50; 96 of
+// 1024 x 512, 2 rows 39.5 / 36.2, 3.3 rows 51 / 37.7; 48 of 2048 x 1024, 2 rows 51 / 59, 3.3 rows 63 / 61.
 inline bool int8_gemm_pays(long long rows, long long groups) { return rows >= 4 * groups; }
 inline bool int8_gemm_supported(int H, int I) { return int8_shape_ok(H, I) && H % 128 == 0 && I % 128 == 0; }
 

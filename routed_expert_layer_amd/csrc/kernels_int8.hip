@@ -34,9 +34,12 @@ __device__ __forceinline__ i32x4_t mfma_i8(u32x4_t a, u32x4_t b, i32x4_t c) {
                                                0);
 }
 
-// silu(g) u for g, u a few roundings off already: the hardware's exponential and
-// reciprocal (a step each) add 1.5 |g| + 5 half steps (the exponent's argument
-// carries |g| of them), which is below what g's own error does to it.
+// silu(g) u for g, u three roundings off already, which move it by 3 (1 + |g|) + 3
+// half steps of 2^-24 at most: the hardware's exponential and reciprocal (a step
+// each; the exponent's argument carries |g| half steps) add 1.5 |g| + 5. The
+// tests count both where a code is near a half. (expf and a division moved as many
+// codes and cost 1 to 3%: 4096 tokens x 6 of 256 experts of 4096 x 2048 1467 us
+// a call, not 1453, 16384 x 6 of 64 3250, not 3155.)
 __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
@@ -265,7 +268,7 @@ __global__ __launch_bounds__(256) void plan_list(const ArgItems wk, int tile_row
 
 // T token rows to codes, four rows a block (one a wave); with a plan, block 0
 // plans the layer's work items instead. Bound by memory: 2 bytes in, 1 out
-// (16384 rows of 4096 35 us, 5.8 TB/s).
+// (16384 rows of 4096 33.5 us, 6.0 TB/s).
 template <int NC>
 __global__ __launch_bounds__(256) void quantise_tokens(const uint16_t* __restrict__ x, int T, int H,
                                                        uint8_t* __restrict__ xq, float* __restrict__ sx,
@@ -642,9 +645,9 @@ __global__ __launch_bounds__(256) void int8_decode_down(const float* __restrict_
 // K a stage, both operands straight into LDS in fragment order; eight waves of
 // 32 x 64 (128 x 128), 64 x 64 (256 x 128) or 128 x 64 (256 x 256).
 // Short groups are bound by the weights' bytes (4096 tokens x 6 of 256 experts
-// of 4096 x 2048: 871 + 445 us, 5.0 TB/s), long ones by the operands' way
-// through L2 and the matrix cores together (16384 x 6 of 64: 1585 + 919 us,
-// 1976 TOPS, the cores busy for 54 and 46% of the cycles; the products without
+// of 4096 x 2048: 862 + 462 us, 5.0 TB/s), long ones by the operands' way
+// through L2 and the matrix cores together (16384 x 6 of 64: 1577 + 1017 us,
+// 1908 TOPS, the cores busy for 53 and 41% of the cycles; the products without
 // their loads 1.7 ms, the loads without the products 2.2).
 // ---------------------------------------------------------------------------
 // h of prefill: 16-row tiles, 8 columns a piece, the two columns of a lane
@@ -674,7 +677,7 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
                                                     size_t mat_off, size_t scale_off, int N, int K, int H, int I,
                                                     float* __restrict__ hout, float* __restrict__ yout) {
   // stages: 128 KiB for one block a CU, or 64 and 72 KiB for two (with 6, so one block a CU, 2048 tokens x 4 of 90
-  // experts of 1024 x 512 took 68.7 us, not 62.0, 8192 x 6 of 256 of 4096 x 2048 2104, not 1994)
+  // experts of 1024 x 512 took 69.7 us, not 63.4, 8192 x 6 of 256 of 4096 x 2048 2212, not 2101)
   constexpr int NS = BM_T == 16 || BN_T == 8 ? 4 : 3;
   constexpr int WN = BN_T * BM_T / 32;
   constexpr int WM = 4;
@@ -852,7 +855,7 @@ __global__ __launch_bounds__(512, 1) void int8_gemm(const uint8_t* __restrict__ 
 // parts and has the 16 code bytes of its place in the token fragment (the
 // order P2 is packed in, int8_k2_source). Up to kHeld pieces a wave stay in
 // registers between the row maximum and the codes; wider rows are read again.
-// Bound by memory: 98304 rows of 2048 184 us, 5.5 TB/s.
+// Bound by memory: 98304 rows of 2048 183 us, 5.5 TB/s.
 constexpr int kHeld = 4, kReqWaves = 8;
 __global__ __launch_bounds__(64 * kReqWaves) void requantise_h(const float* __restrict__ h, int I,
                                                                uint8_t* __restrict__ hq, float* __restrict__ sh) {
@@ -908,7 +911,7 @@ __global__ __launch_bounds__(64 * kReqWaves) void requantise_h(const float* __re
 
 // out[t] = sum over j of w[t, j] y[pos[t, j]], j ascending, over the experts that have a slot.
 // A thread takes 8 columns, all of a token's rows in flight together (up to kAhead of them).
-// Bound by memory: each row of y is read once.
+// Bound by memory: 16384 tokens x 6 rows of 4096 371 us, 4.7 TB/s.
 constexpr int kAhead = 8;
 template <bool OUT_BF16, bool UNIFORM>
 __global__ __launch_bounds__(256) void int8_combine(const float* __restrict__ y, const int32_t* __restrict__ perm_pos,
@@ -1005,8 +1008,8 @@ hipError_t decode_products(const W& wk, int n_items, const uint8_t* xq, const fl
 }
 
 // Rows a prefill tile holds: 256 when groups have 384 on average, else 128, of which two blocks fit on a CU. Calls in us,
-// 128 / 256 rows: 16 experts of 2048 x 768 with 256 rows each 57 / 67 (most groups need a second tile then), 8 of
-// 3968 x 1920 with 256 77 / 99, with 512 138 / 123; 64 of 4096 x 2048 with 384 858 / 835, with 768 1589 / 1500.
+// 128 / 256 rows: 16 experts of 2048 x 768 with 256 rows each 59 / 68 (most groups need a second tile then), 8 of
+// 3968 x 1920 with 256 78 / 100, with 512 150 / 128; 64 of 4096 x 2048 with 384 922 / 895, with 768 1745 / 1640.
 int tile_rows_for(int rows, int groups) { return (long long)rows >= 384ll * groups ? 256 : 128; }
 
 // The two products and the pass between them over planned entries (at most rows / tile + groups).
@@ -1016,7 +1019,7 @@ hipError_t gemm_products(const uint8_t* xq, const float* sx, const int32_t* src,
   const Int8Layout L = int8_layout(H, I);
   const size_t most = rows / tile_rows + groups;  // entries
   // Less than a block a CU: 128 weight rows a block, twice the blocks (a call of 333 tokens x 5 of 20 experts of
-  // 1280 x 640 42.1 -> 36.6 us; with blocks for 256 to 1024, 64 x 8 of 128 experts of 2048 x 768, 122 -> 129 us).
+  // 1280 x 640 39.5 -> 34.4 us; with blocks for 256 to 1024, 64 x 8 of 128 experts of 2048 x 768, 113 -> 115 us).
   const auto narrow = [&](int N) { return tile_rows == 128 && most * ((N + 255) / 256) < 256; };
   const auto product = [&](auto kernel, int columns, int N, int K, const uint8_t* b, const float* bs,
                            const int32_t* from, size_t mat, size_t scales) {
