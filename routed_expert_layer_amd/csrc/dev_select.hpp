@@ -351,7 +351,7 @@ __device__ __forceinline__ void select_token(const float* logits, const float* b
   double s = 0.0, cs = 0.0;
   bool wrong = false;
   if (found && lane < k) {
-    const float le = logits[my_e];  // not a NaN: it reached T
+    const float le = fmaxf(logits[my_e], -INFINITY);  // a NaN is -inf: with a balance it can be chosen
     s = g.score == 0 ? share64(le, m) / z : sigmoid64(le);
     cs = s;
     double most;
@@ -571,7 +571,7 @@ __device__ __forceinline__ bool select_row(float (&l)[VE], const float* __restri
   my_e = 0;
   if (found && r < k) {
     my_e = pick[lane];
-    const float le = logits[my_e];
+    const float le = fmaxf(logits[my_e], -INFINITY);  // a NaN is -inf
     s = g.score == 0 ? share64(le, m) / z : sigmoid64(le);
     cs = s;
     double bound;

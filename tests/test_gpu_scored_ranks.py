@@ -82,3 +82,43 @@ def test_near_ties_in_long_batches(L, T, E):
     l = l0 + 1e-6 * torch.randn((T, E), generator=g, device=dev)
     for G, keep, top in ((1, 1, 1), (8, 3, 2)) if T * E < 2000000 else ((8, 3, 2),):
         run(L, l, 6, f"near ties g{G}", score="sigmoid", n_group=G, topk_group=keep, group_top=top, balance=b)
+
+
+@pytest.mark.parametrize("T", SIZES)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_nan_logits_that_are_chosen(L, T, score):
+    """A NaN logit counts as -inf: with a finite balance its expert has a finite biased score and can be chosen, always
+    where every expert of the kept groups is."""
+    g = torch.Generator().manual_seed(T + 2)
+    for E, G, keep, k in ((1, 1, 1, 1), (2, 1, 1, 2), (16, 1, 1, 16), (16, 4, 2, 8), (12, 4, 3, 4), (64, 8, 2, 16)):
+        l = torch.randn((T, E), generator=g)
+        l[torch.rand((T, E), generator=g) < 0.3] = float("nan")
+        l[0] = float("nan")
+        b = torch.randn(E, generator=g)
+        b[0] += 1.0
+        for top in (1, 2):
+            run(L, l.to(dev), k, f"{score} E{E} k{k} top{top}", score=score, n_group=G, topk_group=keep, group_top=top,
+                balance=b.to(dev))
+
+
+@pytest.mark.parametrize("T,E", [(1, 8), (9, 8), (16, 64), (40, 8), (100, 64)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_scored_with_nan_logits(L, T, E, score):
+    """The same from x and Wr: experts whose bias is a NaN have NaN logits, and a balance that chooses them."""
+    from routed_expert_layer_amd.runtime import RouteBuffers
+    H, k = 256, 8
+    g = torch.Generator().manual_seed(E)
+    x, W = torch.randn((T, H), generator=g).to(dev), torch.randn((H, E), generator=g).to(dev)
+    bias, b = torch.zeros(E), 0.1 * torch.randn(E, generator=g)
+    bias[1::3] = float("nan")
+    b[1::3] += 3.0
+    kw = dict(score=score, balance=b.to(dev), scale=2.0)
+    rb = RouteBuffers(T, H, E, k, dev, keep_logits=True)
+    rb.topk_idx.zero_()
+    rb.perm_src.fill_(-7)
+    rb.route(x, W, bias.to(dev), gate=L.Gate(**kw))
+    torch.cuda.synchronize()
+    assert torch.isnan(rb.logits[:, 1::3]).all()
+    o = dict(topk_idx=rb.topk_idx, topk_w=rb.topk_w, counts=rb.counts, offsets=rb.offsets, perm_src=rb.perm_src,
+             perm_pos=rb.perm_pos)
+    check(o, rb.logits, k, f"route T={T} E={E} {score}", **kw)
