@@ -103,7 +103,7 @@ __device__ __forceinline__ float score32(float l, float m, float iz, int score) 
 // Bounds between which another group's rank may come before one of `rank` or not. Logits 1e-6 apart have different
 // 64-bit scores up to 20 (a sigmoid's distance from 1) and down to -600 (of the largest, for a softmax).
 // By c, a rank r of one c or of two, a + b, of magnitudes up to M: each c is off by kErr / 2 and its rounding 2^-24 |c|,
-// their sum by 2^-24 |r|, so r by kErr + 2^-22 M at most. Where M <= 1 + 2 |r| (else rank_cancels) that is below
+// their sum by 2^-24 |r|, so r by kErr + 2^-22 M at most. Where M <= 1 + 2 |r| (else it cancels, and its token is undecided) that is below
 // 1.5 kErr + 2^-21 |r|. Two ranks r, o then differ truly if |r - o| > 3 kErr + 2^-21 (|r| + |o|): d covers it for
 // |o| <= 2 |r|, and a larger |o| is itself twice that far from r.
 __device__ __forceinline__ void rank_bounds(float rank, bool by_c, int score, float m, float& above, float& below) {
