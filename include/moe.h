@@ -453,6 +453,112 @@ int moe_combine(const float* y_perm, const int32_t* perm_pos, const float* topk_
                 int T, int k, int H, void* out, int out_dtype, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * Training through the layer: tokens to rows sorted by expert and back, with
+ * the gradients. moe_combine is the serving form (fp32 rows, every choice
+ * held); these take rows in either type, choices that are not held here, and
+ * give the backward pass.
+ *
+ * moe_group: the grouping of given choices (of another gate, a replayed
+ *   routing, or a part of one). An entry topk_idx[t,j] outside [0, E) is
+ *   dropped. The kept ones are ordered by (expert, t, j):
+ *     counts[e] = kept entries of e, offsets[e] = sum of the counts below e,
+ *     offsets[E] = all kept entries, perm_pos[t,j] = the entry's rank or -1,
+ *     perm_src[perm_pos[t,j]] = t; perm_src behind offsets[E] is left as it was.
+ *   A token may name an expert more than once. For a routing of moe_route
+ *   this is its own grouping. Scratch: moe_group_workspace_size bytes (may be
+ *   0), 4-byte aligned; calls that may overlap need one each.
+ *   topk_idx device int32 [T, k]; counts [E], offsets [E+1], perm_src [T*k],
+ *   perm_pos [T, k] device out int32.
+ * moe_dispatch: x_perm[perm_pos[t,j], :] = x[t, :]. x [T, H] and x_perm
+ *   [rows_max, H] of dtype. Rows that no entry names are left as they were.
+ * moe_collect: out[t, :] = sum_j topk_w[t,j] * rows[perm_pos[t,j], :], j
+ *   ascending, fp32 sums, rounded once; topk_w NULL: weights of 1, which is
+ *   the gradient of moe_dispatch. rows [rows_max, H] of dtype, out [T, H] of
+ *   out_dtype. A token without an entry gets zeros.
+ * moe_collect_backward: the gradient of moe_collect for dout [T, H] of
+ *   out_dtype:
+ *     drows[perm_pos[t,j], :] = topk_w[t,j] * dout[t, :]   (rounded once)
+ *     dw[t,j] = sum_h dout[t,h] * rows[perm_pos[t,j], h]   (fp32 sums)
+ *   drows [rows_max, H] of dtype, dw fp32 [T, k]; either may be NULL (rows is
+ *   read for dw alone). dw of an entry without a row is 0; rows of drows that
+ *   no entry names are left as they were.
+ * In all of them an entry of perm_pos outside [0, rows_max) has no row: its
+ * weight is not read into a sum and nothing is written for it. Entries must
+ * name different rows where rows are written.
+ * Limits: 1 <= k <= 16, 1 <= E <= 1024, T*k <= 2^30, 1 <= H <= 2^20; buffers
+ * aligned to their elements (rows go in 16-byte pieces where H and the
+ * addresses allow it) and not overlapping.
+ * Errors: MOE_EINVAL, MOE_EHIP.
+ * ------------------------------------------------------------------------ */
+size_t moe_group_workspace_size(int T, int k, int E);
+int moe_group(const int32_t* topk_idx, int T, int k, int E, int32_t* counts, int32_t* offsets, int32_t* perm_src,
+              int32_t* perm_pos, void* workspace, size_t ws_bytes, void* stream);
+int moe_dispatch(const void* x, int dtype, const int32_t* perm_pos, int T, int k, int H, int rows_max, void* x_perm,
+                 void* stream);
+int moe_collect(const void* rows, int dtype, const int32_t* perm_pos, const float* topk_w, int T, int k, int H,
+                int rows_max, void* out, int out_dtype, void* stream);
+int moe_collect_backward(const void* dout, int out_dtype, const void* rows, int dtype, const int32_t* perm_pos,
+                         const float* topk_w, int T, int k, int H, int rows_max, void* drows, float* dw, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * SwiGLU whose inputs are kept in 8 bits for the backward pass.
+ *
+ * moe_swiglu_save: gu [rows, 2I] of dtype holds the gate's columns, then the
+ *   up projection's:
+ *     h[r,i] = silu(gu[r,i]) * gu[r,I+i]      (from gu as given, rounded once)
+ *   and g = gu[:, :I] and u = gu[:, I:] are kept, 128 columns of either at a
+ *   time (the last ones of each may be fewer): scale = largest magnitude / 127
+ *   in fp32, code = 127 v / (largest magnitude) rounded to nearest even, the
+ *   rule of MOE_W_INT8's rows. 128 columns of zeros have scale 0; with an
+ *   infinity or NaN among them their scale is NaN.
+ *   h [rows, I] of dtype, codes int8 [rows, 2I], scales fp32
+ *   [rows, 2 * ceil(I/128)] (the gate's, then the up projection's).
+ * moe_swiglu_backward: with g^ and u^ = code * scale, s = 1 / (1 + exp(-g^)):
+ *     dgu[r,i] = dh[r,i] * u^ * s * (1 + g^ * (1 - s)),  dgu[r,I+i] = dh[r,i] * g^ * s
+ *     h[r,i]   = g^ * s * u^       (NULL: not wanted; the down projection's
+ *                                   weight gradient needs it)
+ *   dh [rows, I], dgu [rows, 2I] and h of dtype.
+ * n_rows: device int32, or NULL. With it only the first min(rows, *n_rows)
+ * rows are worked on (offsets + E of a grouping that dropped entries); those
+ * behind them are neither read nor written.
+ * Limits: rows <= 2^30, 1 <= I <= 2^20, rows * ceil(I/128) <= 2^34; buffers
+ * aligned to their elements and not overlapping.
+ * Errors: MOE_EINVAL, MOE_EHIP.
+ * ------------------------------------------------------------------------ */
+int moe_swiglu_save(const void* gu, int dtype, int rows, const int32_t* n_rows, int I, void* h, int8_t* codes,
+                    float* scales, void* stream);
+int moe_swiglu_backward(const int8_t* codes, const float* scales, const void* dh, int dtype, int rows,
+                        const int32_t* n_rows, int I, void* dgu, void* h, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * The experts' products over their groups of rows on row-major bf16 weights,
+ * and their gradients (moe_ffn_grouped is the serving form, on packed blobs).
+ * Expert e's rows are offsets[e] .. offsets[e]+counts[e]-1 (device int32 [E]
+ * and [E+1], as moe_route and moe_group write them; offsets[E] is not read).
+ *
+ * moe_matmul_grouped: w [E, K, N]. transposed 0: c[r, :] = a[r, :] W_e, a
+ *   [rows_max, K], c [rows_max, N]. transposed 1: c[r, :] = a[r, :] W_e^T, a
+ *   [rows_max, N], c [rows_max, K] (the gradient of the rows). Rows of no group
+ *   are left as they were.
+ * moe_matmul_grouped_dw: dw[e] = sum over e's rows of a[r, :]^T dc[r, :], a
+ *   [rows_max, K], dc [rows_max, N], dw [E, K, N]. An expert without rows gets
+ *   zeros.
+ * a, w and dc bf16, c and dw of out_dtype; fp32 sums, rounded once. Groups must
+ * not share rows. A group that reaches past rows_max is not computed (its rows
+ * of c are left as they were; its dw is zeros).
+ * The work is found on the GPU from counts and offsets: the calls neither wait
+ * nor allocate, launch shapes depend on rows_max and the sizes only, and they
+ * can be captured.
+ * Limits: E <= 1024, K and N multiples of 8 up to 65536, K*N <= 2^30,
+ * rows_max <= 2^30; buffers 16-byte aligned and not overlapping.
+ * Errors: MOE_EINVAL, MOE_EHIP.
+ * ------------------------------------------------------------------------ */
+int moe_matmul_grouped(const void* a, const void* w, const int32_t* counts, const int32_t* offsets, int E,
+                       int rows_max, int K, int N, int transposed, void* c, int out_dtype, void* stream);
+int moe_matmul_grouped_dw(const void* a, const void* dc, const int32_t* counts, const int32_t* offsets, int E,
+                          int rows_max, int K, int N, void* dw, int out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * Prefill double buffering.
  *
  * Page "FreeToken-rtx-4090", phase table row "Prefill" and the paragraph after

@@ -13,3 +13,4 @@ from .moe import (  # noqa: F401
 )
 from .lru import SharedLRU, TraceRec  # noqa: F401
 from .scored import gate_scores, gate_select, quantise_rows, int8_expert  # noqa: F401
+from . import train  # noqa: F401

@@ -34,6 +34,8 @@ SYMBOLS = [
     "moe_ffn_grouped", "moe_prefill_layer", "moe_route_noalloc",
     "moe_select_workspace_size", "moe_select", "moe_route_scored", "moe_experts_workspace_size", "moe_experts",
     "moe_prefill_layer_scored", "moe_decoder_set_gate", "moe_device_decoder_set_gate",
+    "moe_group_workspace_size", "moe_group", "moe_dispatch", "moe_collect", "moe_collect_backward",
+    "moe_swiglu_save", "moe_swiglu_backward", "moe_matmul_grouped", "moe_matmul_grouped_dw",
 ]
 
 
@@ -125,6 +127,15 @@ _sig("moe_ffn_workspace_size", SZ, I32, I32, I32, I32)
 _sig("moe_ffn", I32, P, I32, P, P, I32, P, SZ, I32, I32, I32, P, P, SZ, I32, P)
 _sig("moe_ffn_grouped", I32, P, I32, P, P, P, P, I32, I32, I32, P, SZ, I32, I32, I32, P, P, SZ, P)
 _sig("moe_combine", I32, P, P, P, I32, I32, I32, P, I32, P)
+_sig("moe_group_workspace_size", SZ, I32, I32, I32)
+_sig("moe_group", I32, P, I32, I32, I32, P, P, P, P, P, SZ, P)
+_sig("moe_dispatch", I32, P, I32, P, I32, I32, I32, I32, P, P)
+_sig("moe_collect", I32, P, I32, P, P, I32, I32, I32, I32, P, I32, P)
+_sig("moe_collect_backward", I32, P, I32, P, I32, P, P, I32, I32, I32, I32, P, P, P)
+_sig("moe_swiglu_save", I32, P, I32, I32, P, I32, P, P, P, P)
+_sig("moe_swiglu_backward", I32, P, P, P, I32, I32, P, I32, P, P, P)
+_sig("moe_matmul_grouped", I32, P, P, P, P, I32, I32, I32, I32, I32, P, I32, P)
+_sig("moe_matmul_grouped_dw", I32, P, P, P, P, I32, I32, I32, I32, P, I32, P)
 _sig("moe_pipe_create", P, P, SZ, I32, PI)
 _sig("moe_pipe_destroy", I32, P)
 _sig("moe_pipe_begin_layer", I32, P, I32, P, ctypes.POINTER(ctypes.c_void_p))
@@ -502,6 +513,160 @@ def moe_combine(y_perm, perm_pos, topk_w, out, stream=None):
     H = y_perm.shape[1]
     _check(_lib.moe_combine(_dptr(y_perm), _dptr(perm_pos), _dptr(topk_w), T, k, H, _dptr(out), _dtype_code(out),
                             _stream(stream)), "moe_combine")
+
+
+# ---------------------------------------------------------------------------
+def moe_group_workspace_size(T, k, E):
+    return _lib.moe_group_workspace_size(T, k, E)
+
+
+def _act(t, name):
+    """MOE_DT code of a tensor of rows."""
+    if t.dtype is _torch_dtype("bfloat16"):
+        return MOE_DT_BF16
+    if t.dtype is _torch_dtype("float32"):
+        return MOE_DT_F32
+    raise ValueError(f"{name}: a float32 or bfloat16 tensor is needed, not {t.dtype}")
+
+
+def _rows_of(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: two dimensions are needed, not shape {tuple(t.shape)}")
+    return t.shape
+
+
+def moe_group(topk_idx, E, counts, offsets, perm_src, perm_pos, workspace=None, stream=None):
+    """The grouping of given choices topk_idx (GPU int32 [T, k]; entries outside [0, E) are dropped): counts [E],
+    offsets [E+1], perm_src [T*k] and perm_pos [T, k] (GPU int32) are written. workspace: GPU bytes, or None where
+    moe_group_workspace_size(T, k, E) is 0."""
+    T, k = _rows_of(topk_idx, "topk_idx")
+    dev = _device(topk_idx, "topk_idx")
+    if perm_src.numel() < T * k:
+        raise ValueError(f"perm_src: at least {T * k} entries are needed")
+    ws, n = (None, 0) if workspace is None else (_gpu(workspace, dev, None, "workspace"), _nbytes(workspace))
+    _check(_lib.moe_group(_gpu(topk_idx, dev, "int32", "topk_idx"), T, k, E,
+                          _gpu(counts, dev, "int32", "counts", (E,)), _gpu(offsets, dev, "int32", "offsets", (E + 1,)),
+                          _gpu(perm_src, dev, "int32", "perm_src"),
+                          _gpu(perm_pos, dev, "int32", "perm_pos", (T, k)), ws, n, _stream(stream)), "moe_group")
+
+
+def moe_dispatch(x, perm_pos, x_perm, stream=None):
+    """x_perm[perm_pos[t, j]] = x[t]: x [T, H] and x_perm [rows_max, H] of one type (float32 or bfloat16)."""
+    T, H = _rows_of(x, "x")
+    rows, k = _rows_of(x_perm, "x_perm")[0], _rows_of(perm_pos, "perm_pos")[1]
+    dev = _device(x, "x")
+    dt = _act(x, "x")
+    _check(_lib.moe_dispatch(_gpu(x, dev, None, "x"), dt, _gpu(perm_pos, dev, "int32", "perm_pos", (T, k)), T, k, H,
+                             rows, _gpu(x_perm, dev, _DT_NAMES[dt], "x_perm", (rows, H)), _stream(stream)),
+           "moe_dispatch")
+
+
+def moe_collect(rows, perm_pos, topk_w, out, stream=None):
+    """out[t] = sum_j topk_w[t, j] rows[perm_pos[t, j]] (topk_w None: weights of 1); rows [rows_max, H] and out [T, H]
+    float32 or bfloat16, each."""
+    n, H = _rows_of(rows, "rows")
+    T, k = _rows_of(perm_pos, "perm_pos")
+    dev = _device(rows, "rows")
+    w = None if topk_w is None else _gpu(topk_w, dev, "float32", "topk_w", (T, k))
+    _check(_lib.moe_collect(_gpu(rows, dev, None, "rows"), _act(rows, "rows"),
+                            _gpu(perm_pos, dev, "int32", "perm_pos"), w, T, k, H, n,
+                            _gpu(out, dev, None, "out", (T, H)), _act(out, "out"), _stream(stream)), "moe_collect")
+
+
+def moe_collect_backward(dout, rows, perm_pos, topk_w, drows, dw, stream=None):
+    """The gradient of moe_collect: drows[perm_pos[t, j]] = topk_w[t, j] dout[t] (drows None: not wanted) and
+    dw[t, j] = <dout[t], rows[perm_pos[t, j]]> (dw None: not wanted, rows may then be None)."""
+    T, H = _rows_of(dout, "dout")
+    k = _rows_of(perm_pos, "perm_pos")[1]
+    dev = _device(dout, "dout")
+    like = rows if rows is not None else drows
+    if like is None or (dw is not None and rows is None):
+        raise ValueError("moe_collect_backward: dw needs rows, and drows or dw is needed")
+    n = _rows_of(like, "rows")[0]
+    dt = _act(like, "rows")
+    w = None if topk_w is None else _gpu(topk_w, dev, "float32", "topk_w", (T, k))
+    r = None if rows is None else _gpu(rows, dev, None, "rows", (n, H))
+    dr = None if drows is None else _gpu(drows, dev, _DT_NAMES[dt], "drows", (n, H))
+    d = None if dw is None else _gpu(dw, dev, "float32", "dw", (T, k))
+    _check(_lib.moe_collect_backward(_gpu(dout, dev, None, "dout"), _act(dout, "dout"), r, dt,
+                                     _gpu(perm_pos, dev, "int32", "perm_pos", (T, k)), w, T, k, H, n, dr, d,
+                                     _stream(stream)), "moe_collect_backward")
+
+
+_DT_NAMES = {MOE_DT_F32: "float32", MOE_DT_BF16: "bfloat16"}
+
+
+def _n_rows(n_rows, dev):
+    if n_rows is None:
+        return None
+    if n_rows.numel() != 1:
+        raise ValueError(f"n_rows: one entry is needed, not shape {tuple(n_rows.shape)}")
+    return _gpu(n_rows, dev, "int32", "n_rows")
+
+
+def moe_swiglu_save(gu, h, codes, scales, n_rows=None, stream=None):
+    """h = silu(gu[:, :I]) gu[:, I:], and gu kept in 8 bits: codes int8 [rows, 2I], scales float32
+    [rows, 2 ceil(I / 128)]. gu [rows, 2I] and h [rows, I] of one type. n_rows: GPU int32 of one entry (offsets[E:]),
+    the rows to work on."""
+    rows, two_i = _rows_of(gu, "gu")
+    if two_i % 2:
+        raise ValueError(f"gu: gate and up columns are needed, not {two_i}")
+    I = two_i // 2
+    dev = _device(gu, "gu")
+    dt = _act(gu, "gu")
+    _check(_lib.moe_swiglu_save(_gpu(gu, dev, None, "gu"), dt, rows, _n_rows(n_rows, dev), I,
+                                _gpu(h, dev, _DT_NAMES[dt], "h", (rows, I)),
+                                _gpu(codes, dev, "int8", "codes", (rows, two_i)),
+                                _gpu(scales, dev, "float32", "scales", (rows, 2 * ((I + 127) // 128))),
+                                _stream(stream)), "moe_swiglu_save")
+
+
+def moe_swiglu_backward(codes, scales, dh, dgu, h=None, n_rows=None, stream=None):
+    """The gradient of moe_swiglu_save's h to gu from what was kept, dgu [rows, 2I] for dh [rows, I], and h [rows, I]
+    again from it (None: not wanted); dh, dgu and h of one type."""
+    rows, I = _rows_of(dh, "dh")
+    dev = _device(dh, "dh")
+    dt = _act(dh, "dh")
+    again = None if h is None else _gpu(h, dev, _DT_NAMES[dt], "h", (rows, I))
+    _check(_lib.moe_swiglu_backward(_gpu(codes, dev, "int8", "codes", (rows, 2 * I)),
+                                    _gpu(scales, dev, "float32", "scales", (rows, 2 * ((I + 127) // 128))),
+                                    _gpu(dh, dev, None, "dh"), dt, rows, _n_rows(n_rows, dev), I,
+                                    _gpu(dgu, dev, _DT_NAMES[dt], "dgu", (rows, 2 * I)), again, _stream(stream)),
+           "moe_swiglu_backward")
+
+
+def _grouped_args(dev, counts, offsets, E):
+    return _gpu(counts, dev, "int32", "counts", (E,)), _gpu(offsets, dev, "int32", "offsets", (E + 1,))
+
+
+def moe_matmul_grouped(a, w, counts, offsets, c, transposed=False, stream=None):
+    """c[r] = a[r] w[e] for the rows r of expert e, or a[r] w[e]^T: a bfloat16 [rows_max, K] (transposed: N), w bfloat16
+    [E, K, N], c float32 or bfloat16 [rows_max, N] (transposed: K)."""
+    if w.dim() != 3:
+        raise ValueError(f"w: three dimensions are needed, not shape {tuple(w.shape)}")
+    E, K, N = w.shape
+    rows = _rows_of(a, "a")[0]
+    dev = _device(w, "w")
+    cn, of = _grouped_args(dev, counts, offsets, E)
+    _check(_lib.moe_matmul_grouped(_gpu(a, dev, "bfloat16", "a", (rows, N if transposed else K)),
+                                   _gpu(w, dev, "bfloat16", "w"), cn, of, E, rows, K, N, int(bool(transposed)),
+                                   _gpu(c, dev, None, "c", (rows, K if transposed else N)), _act(c, "c"),
+                                   _stream(stream)), "moe_matmul_grouped")
+
+
+def moe_matmul_grouped_dw(a, dc, counts, offsets, dw, stream=None):
+    """dw[e] = sum over expert e's rows of a[r]^T dc[r]: a [rows_max, K] and dc [rows_max, N] bfloat16, dw [E, K, N]
+    float32 or bfloat16."""
+    if dw.dim() != 3:
+        raise ValueError(f"dw: three dimensions are needed, not shape {tuple(dw.shape)}")
+    E, K, N = dw.shape
+    rows = _rows_of(a, "a")[0]
+    dev = _device(dw, "dw")
+    cn, of = _grouped_args(dev, counts, offsets, E)
+    _check(_lib.moe_matmul_grouped_dw(_gpu(a, dev, "bfloat16", "a", (rows, K)),
+                                      _gpu(dc, dev, "bfloat16", "dc", (rows, N)), cn, of, E, rows, K, N,
+                                      _gpu(dw, dev, None, "dw"), _act(dw, "dw"), _stream(stream)),
+           "moe_matmul_grouped_dw")
 
 
 # ---------------------------------------------------------------------------

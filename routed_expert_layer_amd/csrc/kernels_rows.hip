@@ -1,0 +1,392 @@
+// Tokens sorted by expert and back: the grouping of given choices, the copies
+// of the token rows, the weighted sum of a token's rows and its gradient.
+//
+//   order of the rows: (expert, token, j);  pos[t, j] = rank, -1 if dropped
+//   dispatch:  rows[pos[t, j]] = x[t]
+//   collect:   out[t] = sum_j w[t, j] rows[pos[t, j]]          (j ascending, fp32)
+//   backward:  drows[pos[t, j]] = w[t, j] dout[t],  dw[t, j] = <dout[t], rows[pos[t, j]]>
+//
+// All of them move bytes: a row is read once, in 16-byte loads, and written
+// once; the sums stay in registers.
+#include <algorithm>
+
+#include "dev_common.hpp"
+#include "moe_kernels.hpp"
+#include "row_vec.hpp"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Grouping.
+// ---------------------------------------------------------------------------
+constexpr int kGroupThreads = 1024;
+constexpr int kGroupWaves = kGroupThreads / 64;
+constexpr int kGroupSub = 4;                                  // 64-entry chunks a wave takes per round
+constexpr int kGroupRound = kGroupWaves * kGroupSub * 64;     // entries a block places per round: 4096
+constexpr int kGroupBlocks = 64;                              // most blocks of the two-launch form
+constexpr int kGroupExperts = 1024;
+
+// Exclusive prefix sum of v over the block's threads (1024) and its total.
+__device__ __forceinline__ int block_prefix(int v, int* sums, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s, d, 64);
+    if (lane >= d) s += o;
+  }
+  if (lane == 63) sums[wave] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < kGroupWaves; ++w) {
+    before += w < wave ? sums[w] : 0;
+    all += sums[w];
+  }
+  __syncthreads();
+  total = all;
+  return before + s - v;
+}
+
+// Choices per expert of each block's segment of the entries, hist[block][E].
+__global__ __launch_bounds__(kGroupThreads) void group_count(const int32_t* __restrict__ idx, int64_t n, int64_t seg,
+                                                             int E, int32_t* __restrict__ hist) {
+  __shared__ int h[kGroupExperts];
+  for (int e = threadIdx.x; e < E; e += kGroupThreads) h[e] = 0;
+  __syncthreads();
+  const int64_t end = min(n, (int64_t)(blockIdx.x + 1) * seg);
+  for (int64_t i = (int64_t)blockIdx.x * seg + threadIdx.x; i < end; i += kGroupThreads) {
+    const int e = idx[i];
+    if ((unsigned)e < (unsigned)E) atomicAdd(&h[e], 1);  // integers: the order does not matter
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kGroupThreads) hist[(size_t)blockIdx.x * E + e] = h[e];
+}
+
+// Places of a segment's entries. The rank of an entry among its expert's is
+// the number in earlier blocks (hist), earlier rounds (base), earlier waves and
+// chunks of the round (cnt) and lower lanes of its chunk: the lanes with the
+// same expert are found by one ballot per bit of the expert's number. With ONE
+// the only block counts for itself (n <= kGroupRound).
+template <bool ONE>
+__global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __restrict__ idx, int64_t n, int64_t seg,
+                                                             int k, int E, int bits, const int32_t* __restrict__ hist,
+                                                             int32_t* __restrict__ counts,
+                                                             int32_t* __restrict__ offsets,
+                                                             int32_t* __restrict__ perm_src,
+                                                             int32_t* __restrict__ perm_pos) {
+  __shared__ int cnt[kGroupWaves][kGroupExperts];
+  __shared__ int sums[kGroupWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint64_t below = (1ull << lane) - 1ull;
+  const int64_t first = ONE ? 0 : (int64_t)blockIdx.x * seg, end = ONE ? n : min(n, first + seg);
+  int base = 0;  // thread e: the place of the next entry of expert e
+  auto publish = [&](int count) {
+    int total;
+    const int at = block_prefix(count, sums, total);
+    if (blockIdx.x == 0) {
+      if (tid < E) {
+        counts[tid] = count;
+        offsets[tid] = at;
+      }
+      if (tid == 0) offsets[E] = total;
+    }
+    return at;
+  };
+  if constexpr (!ONE) {
+    int before = 0, all = 0;
+    if (tid < E)
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int c = hist[(size_t)b * E + tid];
+        before += b < (int)blockIdx.x ? c : 0;
+        all += c;
+      }
+    base = publish(all) + before;
+  }
+  for (int64_t r = first; ONE || r < end; r += kGroupRound) {
+    const int here = (int)min((int64_t)kGroupRound, end - r);
+    const int waves = (here + 64 * kGroupSub - 1) / (64 * kGroupSub);
+    for (int w = 0; w < waves; ++w)
+      if (tid < E) cnt[w][tid] = 0;
+    __syncthreads();
+    int e[kGroupSub], rank[kGroupSub];
+#pragma unroll
+    for (int c = 0; c < kGroupSub; ++c) {
+      const int i = (wave * kGroupSub + c) * 64 + lane;
+      const int v = i < here ? idx[r + i] : E;
+      e[c] = (unsigned)v < (unsigned)E ? v : E;
+    }
+    if (wave < waves)
+#pragma unroll
+      for (int c = 0; c < kGroupSub; ++c) {
+        uint64_t same = ~0ull;
+        for (int b = 0; b < bits; ++b) {
+          const bool on = (e[c] >> b) & 1;
+          const uint64_t m = __ballot(on);
+          same &= on ? m : ~m;
+        }
+        if (e[c] < E) {
+          const int before = cnt[wave][e[c]];
+          rank[c] = before + __popcll(same & below);
+          if ((same & below) == 0) cnt[wave][e[c]] = before + __popcll(same);
+        }
+        __builtin_amdgcn_wave_barrier();  // the next chunk's reads follow this one's writes
+      }
+    __syncthreads();
+    int run = base, count = 0;
+    if constexpr (ONE) {
+      if (tid < E)
+        for (int w = 0; w < waves; ++w) count += cnt[w][tid];
+      run = publish(count);
+    }
+    if (tid < E)
+      for (int w = 0; w < waves; ++w) {
+        const int c = cnt[w][tid];
+        cnt[w][tid] = run;
+        run += c;
+      }
+    base = run;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kGroupSub; ++c) {
+      const int i = (wave * kGroupSub + c) * 64 + lane;
+      if (i >= here) continue;
+      const bool kept = e[c] < E;
+      const int p = kept ? cnt[wave][e[c]] + rank[c] : -1;
+      perm_pos[r + i] = p;
+      if (kept) perm_src[p] = (int)((r + i) / k);
+    }
+    if constexpr (ONE) break;
+    __syncthreads();
+  }
+}
+
+int group_blocks(int64_t n) { return (int)std::min<int64_t>(kGroupBlocks, (n + kGroupRound - 1) / kGroupRound); }
+
+// ---------------------------------------------------------------------------
+// Rows. A block takes 256 >> ls tokens, 1 << ls threads each; a thread takes N
+// elements of its token's row.
+// ---------------------------------------------------------------------------
+struct RowShape {
+  int T, k, H, rows, ls;
+};
+
+template <bool BF16, int N>
+__global__ __launch_bounds__(256) void dispatch_kernel(const void* __restrict__ x, const int32_t* __restrict__ pos,
+                                                       const RowShape s, void* __restrict__ out) {
+  const int t = blockIdx.x * (256 >> s.ls) + ((int)threadIdx.x >> s.ls);
+  const int c = (blockIdx.y * (1 << s.ls) + ((int)threadIdx.x & ((1 << s.ls) - 1))) * N;
+  if (t >= s.T || c >= s.H) return;
+  RowVec<BF16, N> v;
+  v.load(x, (size_t)t * s.H + c);
+  for (int j = 0; j < s.k; ++j) {
+    const int p = pos[(size_t)t * s.k + j];
+    if ((unsigned)p < (unsigned)s.rows) v.store(out, (size_t)p * s.H + c);
+  }
+}
+
+constexpr int kRowsAtOnce = 8;  // rows of a token whose loads are in flight together
+
+template <bool BF16, bool OUT_BF16, int N>
+__global__ __launch_bounds__(256) void collect_kernel(const void* __restrict__ rows, const int32_t* __restrict__ pos,
+                                                      const float* __restrict__ w, const RowShape s,
+                                                      void* __restrict__ out) {
+  const int t = blockIdx.x * (256 >> s.ls) + ((int)threadIdx.x >> s.ls);
+  const int c = (blockIdx.y * (1 << s.ls) + ((int)threadIdx.x & ((1 << s.ls) - 1))) * N;
+  if (t >= s.T || c >= s.H) return;
+  float acc[N] = {};
+  for (int j0 = 0; j0 < s.k; j0 += kRowsAtOnce) {
+    int p[kRowsAtOnce];
+    float wj[kRowsAtOnce];
+    RowVec<BF16, N> v[kRowsAtOnce];
+#pragma unroll
+    for (int j = 0; j < kRowsAtOnce; ++j) {
+      p[j] = j0 + j < s.k ? pos[(size_t)t * s.k + j0 + j] : -1;
+      wj[j] = w && j0 + j < s.k ? w[(size_t)t * s.k + j0 + j] : 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsAtOnce; ++j)
+      if ((unsigned)p[j] < (unsigned)s.rows) v[j].load(rows, (size_t)p[j] * s.H + c);
+#pragma unroll
+    for (int j = 0; j < kRowsAtOnce; ++j)
+      if ((unsigned)p[j] < (unsigned)s.rows) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(wj[j], v[j].get(i), acc[i]);
+      }
+  }
+  RowVec<OUT_BF16, N> o;
+  o.set(acc);
+  o.store(out, (size_t)t * s.H + c);
+}
+
+// One block per token: dout's row is read once, each of the token's rows once.
+template <bool BF16, bool OUT_BF16, int N, bool DROWS, bool DW>
+__global__ __launch_bounds__(256) void collect_backward_kernel(const void* __restrict__ dout,
+                                                               const void* __restrict__ rows,
+                                                               const int32_t* __restrict__ pos,
+                                                               const float* __restrict__ w, const RowShape s,
+                                                               void* __restrict__ drows, float* __restrict__ dw) {
+  __shared__ float part[4][kRowsAtOnce];
+  const int t = blockIdx.x;
+  for (int j0 = 0; j0 < s.k; j0 += kRowsAtOnce) {
+    int p[kRowsAtOnce];
+    float wj[kRowsAtOnce], dot[kRowsAtOnce] = {};
+#pragma unroll
+    for (int j = 0; j < kRowsAtOnce; ++j) {
+      p[j] = j0 + j < s.k ? pos[(size_t)t * s.k + j0 + j] : -1;
+      wj[j] = w && j0 + j < s.k ? w[(size_t)t * s.k + j0 + j] : 1.f;
+    }
+    for (int c = (int)threadIdx.x * N; c < s.H; c += 256 * N) {
+      RowVec<OUT_BF16, N> d;
+      d.load(dout, (size_t)t * s.H + c);
+      RowVec<BF16, N> v[kRowsAtOnce];
+      if constexpr (DW) {
+#pragma unroll
+        for (int j = 0; j < kRowsAtOnce; ++j)
+          if ((unsigned)p[j] < (unsigned)s.rows) v[j].load(rows, (size_t)p[j] * s.H + c);
+      }
+#pragma unroll
+      for (int j = 0; j < kRowsAtOnce; ++j)
+        if ((unsigned)p[j] < (unsigned)s.rows) {
+          if constexpr (DW) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) dot[j] = fmaf(d.get(i), v[j].get(i), dot[j]);
+          }
+          if constexpr (DROWS) {
+            float g[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = wj[j] * d.get(i);
+            RowVec<BF16, N> o;
+            o.set(g);
+            o.store(drows, (size_t)p[j] * s.H + c);
+          }
+        }
+    }
+    if constexpr (DW) {
+#pragma unroll
+      for (int j = 0; j < kRowsAtOnce; ++j) {
+#pragma unroll
+        for (int m = 32; m > 0; m >>= 1) dot[j] += __shfl_xor(dot[j], m, 64);
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][j] = dot[j];
+      }
+      __syncthreads();
+      const int j = threadIdx.x;
+      if (j < kRowsAtOnce && j0 + j < s.k)
+        dw[(size_t)t * s.k + j0 + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
+      __syncthreads();
+    }
+  }
+}
+
+// Threads a token's row of n vectors gets, as a power of two of at most 256.
+int lane_bits(int n) {
+  int ls = 0;
+  while (ls < 8 && (1 << ls) < n) ++ls;
+  return ls;
+}
+
+// f(N as a constant) for n of 1, 2, 4, 8 (8 only with bf16 rows).
+template <bool EIGHT, typename F>
+void with_elems(int n, const F& f) {
+  if constexpr (EIGHT)
+    if (n == 8) return f(std::integral_constant<int, 8>{});
+  if (n == 4) return f(std::integral_constant<int, 4>{});
+  if (n == 2) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1>{});
+}
+
+template <typename F>
+void with_flag(bool b, const F& f) {
+  if (b) f(std::true_type{});
+  else f(std::false_type{});
+}
+
+}  // namespace
+
+size_t group_workspace_bytes(int T, int k, int E) {
+  const int64_t n = (int64_t)T * k;
+  return n <= kGroupRound ? 0 : (size_t)group_blocks(n) * E * sizeof(int32_t);
+}
+
+hipError_t launch_group(const int32_t* idx, int T, int k, int E, int32_t* counts, int32_t* offsets, int32_t* perm_src,
+                        int32_t* perm_pos, void* ws, hipStream_t s) {
+  const int64_t n = (int64_t)T * k;
+  int bits = 0;
+  while ((1 << bits) < E + 1) ++bits;
+  if (n <= kGroupRound) {
+    hipLaunchKernelGGL(group_place<true>, dim3(1), dim3(kGroupThreads), 0, s, idx, n, (int64_t)kGroupRound, k, E, bits,
+                       nullptr, counts, offsets, perm_src, perm_pos);
+    return hipGetLastError();
+  }
+  const int blocks = group_blocks(n);
+  const int64_t seg = ((n + blocks - 1) / blocks + kGroupRound - 1) / kGroupRound * kGroupRound;
+  int32_t* hist = static_cast<int32_t*>(ws);
+  hipLaunchKernelGGL(group_count, dim3(blocks), dim3(kGroupThreads), 0, s, idx, n, seg, E, hist);
+  hipLaunchKernelGGL(group_place<false>, dim3(blocks), dim3(kGroupThreads), 0, s, idx, n, seg, k, E, bits, hist, counts,
+                     offsets, perm_src, perm_pos);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const void* x, bool bf16, const int32_t* pos, int T, int k, int H, int rows, void* out,
+                           hipStream_t s) {
+  const int es = bf16 ? 2 : 4;
+  const int n = row_vec_elems(H, bf16 ? 8 : 4, {{x, es}, {out, es}});
+  const int nv = (H + n - 1) / n, ls = lane_bits(nv);
+  const RowShape sh{T, k, H, rows, ls};
+  const dim3 grid((T + (256 >> ls) - 1) / (256 >> ls), (nv + (1 << ls) - 1) >> ls);
+  with_flag(bf16, [&](auto b) {
+    constexpr bool B = decltype(b)::value;
+    with_elems<B>(n, [&](auto m) {
+      constexpr int N = decltype(m)::value;
+      hipLaunchKernelGGL((dispatch_kernel<B, N>), grid, dim3(256), 0, s, x, pos, sh, out);
+    });
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_collect(const void* rows, bool bf16, const int32_t* pos, const float* w, int T, int k, int H,
+                          int n_rows, void* out, bool out_bf16, hipStream_t s) {
+  const int n = row_vec_elems(H, bf16 ? 8 : 4, {{rows, bf16 ? 2 : 4}, {out, out_bf16 ? 2 : 4}});
+  const int nv = (H + n - 1) / n, ls = lane_bits(nv);
+  const RowShape sh{T, k, H, n_rows, ls};
+  const dim3 grid((T + (256 >> ls) - 1) / (256 >> ls), (nv + (1 << ls) - 1) >> ls);
+  with_flag(bf16, [&](auto b) {
+    constexpr bool B = decltype(b)::value;
+    with_flag(out_bf16, [&](auto ob) {
+      constexpr bool OB = decltype(ob)::value;
+      with_elems<B>(n, [&](auto m) {
+        constexpr int N = decltype(m)::value;
+        hipLaunchKernelGGL((collect_kernel<B, OB, N>), grid, dim3(256), 0, s, rows, pos, w, sh, out);
+      });
+    });
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_collect_backward(const void* dout, bool out_bf16, const void* rows, bool bf16, const int32_t* pos,
+                                   const float* w, int T, int k, int H, int n_rows, void* drows, float* dw,
+                                   hipStream_t s) {
+  const int es = bf16 ? 2 : 4;
+  const int n = row_vec_elems(H, bf16 ? 8 : 4, {{dout, out_bf16 ? 2 : 4}, {rows, es}, {drows, es}});
+  const RowShape sh{T, k, H, n_rows, 8};
+  with_flag(bf16, [&](auto b) {
+    constexpr bool B = decltype(b)::value;
+    with_flag(out_bf16, [&](auto ob) {
+      constexpr bool OB = decltype(ob)::value;
+      with_elems<B>(n, [&](auto m) {
+        constexpr int N = decltype(m)::value;
+        with_flag(drows != nullptr, [&](auto dr) {
+          with_flag(dw != nullptr, [&](auto dd) {
+            constexpr bool DR = decltype(dr)::value, DD = decltype(dd)::value;
+            if constexpr (DR || DD)
+              hipLaunchKernelGGL((collect_backward_kernel<B, OB, N, DR, DD>), dim3(T), dim3(256), 0, s, dout, rows, pos,
+                                 w, sh, drows, dw);
+          });
+        });
+      });
+    });
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

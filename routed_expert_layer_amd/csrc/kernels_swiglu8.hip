@@ -1,0 +1,214 @@
+// SwiGLU whose inputs are kept in 8 bits, and its backward pass from them.
+//
+//   g = gu[r, :I], u = gu[r, I:],  s(g) = 1 / (1 + e^-g),  h = g s(g) u
+//   kept, for 128 columns of g or u at a time:  scale = max|v| / 127,  code = rne(127 v / max|v|)
+//   backward, from g^, u^ = code * scale:
+//     dg = dh u^ s (1 + g^ (1 - s)),  du = dh g^ s,  h^ = g^ s u^
+//
+// Sixteen lanes take 128 columns of g and the same of u, eight of each a lane,
+// so a scale is one reduction over 16 lanes and every byte is moved once.
+#include "dev_common.hpp"
+#include "moe_kernels.hpp"
+#include "row_quant.hpp"
+#include "row_vec.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kKeptGroup = 128;  // columns that share a scale
+constexpr int kKeptLanes = 16, kKeptCols = 8;
+
+// 1 / (1 + e^-g) and 1 - it, neither by a difference: both keep their last bits.
+struct Sigmoid {
+  float s, t;
+  __device__ __forceinline__ explicit Sigmoid(float g) {
+    const float e = expf(-fabsf(g)), r = 1.f / (1.f + e);
+    s = g >= 0.f ? r : e * r;
+    t = g >= 0.f ? e * r : r;
+    if (isnan(g)) s = t = g;
+  }
+};
+
+// Where a thread works: a row and eight columns, c0 + i * step (i < n), of a group of 128.
+struct KeptAt {
+  int64_t row;
+  int group, c0, n, step;
+  bool on;
+};
+
+template <bool VEC>
+__device__ __forceinline__ KeptAt kept_at(int64_t rows, int I, int groups) {
+  const int64_t q = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kKeptLanes;
+  const int l = threadIdx.x & (kKeptLanes - 1);
+  KeptAt a;
+  a.row = q / groups;
+  a.group = (int)(q % groups);
+  a.step = VEC ? 1 : kKeptLanes;
+  a.c0 = a.group * kKeptGroup + (VEC ? l * kKeptCols : l);
+  const int left = min(I, (a.group + 1) * kKeptGroup) - a.c0;
+  a.n = left <= 0 ? 0 : min(kKeptCols, (left + a.step - 1) / a.step);
+  a.on = a.row < rows;
+  return a;
+}
+
+// Eight columns of a row from `base` on (VEC: one load, 16-byte aligned).
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const void* p, size_t base, const KeptAt& a, float (&f)[kKeptCols]) {
+  if constexpr (VEC) {
+    RowVec<BF16, kKeptCols> v;
+    if (a.n > 0) v.load(p, base + a.c0);
+#pragma unroll
+    for (int i = 0; i < kKeptCols; ++i) f[i] = a.n > 0 ? v.get(i) : 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kKeptCols; ++i) {
+      RowVec<BF16, 1> v;
+      v.w[0] = 0;
+      if (i < a.n) v.load(p, base + a.c0 + i * kKeptLanes);
+      f[i] = v.get(0);
+    }
+  }
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store8(void* p, size_t base, const KeptAt& a, const float (&f)[kKeptCols]) {
+  if constexpr (VEC) {
+    RowVec<BF16, kKeptCols> v;
+    v.set(f);
+    if (a.n > 0) v.store(p, base + a.c0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kKeptCols; ++i) {
+      RowVec<BF16, 1> v;
+      const float one[1] = {f[i]};
+      v.set(one);
+      if (i < a.n) v.store(p, base + a.c0 + i * kKeptLanes);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+  for (int d = kKeptLanes / 2; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d, kKeptLanes));
+  return v;
+}
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void keep8(const float (&f)[kKeptCols], const KeptAt& a, int8_t* codes, size_t base,
+                                      float* scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kKeptCols; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  const RowQuant q(max16(m));
+  if (!a.on) return;
+  if ((threadIdx.x & (kKeptLanes - 1)) == 0) *scale = q.scale();
+  if constexpr (VEC) {
+    if (a.n > 0)
+      *reinterpret_cast<u32x2_t*>(codes + base + a.c0) =
+          u32x2_t{q.pack4<BF16>(f[0], f[1], f[2], f[3]), q.pack4<BF16>(f[4], f[5], f[6], f[7])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < kKeptCols; ++i)
+      if (i < a.n) codes[base + a.c0 + i * kKeptLanes] = (int8_t)(q.code<BF16>(f[i]) & 0xFFu);
+  }
+}
+
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void swiglu_save_kernel(const void* __restrict__ gu, int64_t rows,
+                                                          const int32_t* __restrict__ n_rows, int I, int groups,
+                                                          void* __restrict__ h, int8_t* __restrict__ codes,
+                                                          float* __restrict__ scales) {
+  if (n_rows) rows = min(rows, (int64_t)*n_rows);
+  KeptAt a = kept_at<VEC>(rows, I, groups);
+  if (!a.on) a.n = 0;  // the 16 lanes of a group agree, but the wave stays whole for the reductions
+  const size_t r = (size_t)a.row * 2 * I;
+  float g[kKeptCols], u[kKeptCols], f[kKeptCols];
+  load8<BF16, VEC>(gu, r, a, g);
+  load8<BF16, VEC>(gu, r + I, a, u);
+#pragma unroll
+  for (int i = 0; i < kKeptCols; ++i) f[i] = g[i] * Sigmoid(g[i]).s * u[i];
+  store8<BF16, VEC>(h, (size_t)a.row * I, a, f);
+  float* sc = scales + (size_t)a.row * 2 * groups + a.group;
+  keep8<BF16, VEC>(g, a, codes, r, sc);
+  keep8<BF16, VEC>(u, a, codes, r + I, sc + groups);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void kept8(const int8_t* codes, size_t base, const KeptAt& a, float scale,
+                                      float (&f)[kKeptCols]) {
+  if constexpr (VEC) {
+    u32x2_t v{0, 0};
+    if (a.n > 0) v = *reinterpret_cast<const u32x2_t*>(codes + base + a.c0);
+#pragma unroll
+    for (int i = 0; i < kKeptCols; ++i) f[i] = (float)(int8_t)(v[i >> 2] >> (8 * (i & 3))) * scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kKeptCols; ++i) f[i] = i < a.n ? (float)codes[base + a.c0 + i * kKeptLanes] * scale : 0.f;
+  }
+}
+
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __restrict__ codes,
+                                                              const float* __restrict__ scales,
+                                                              const void* __restrict__ dh, int64_t rows,
+                                                              const int32_t* __restrict__ n_rows, int I, int groups,
+                                                              void* __restrict__ dgu, void* __restrict__ h) {
+  if (n_rows) rows = min(rows, (int64_t)*n_rows);
+  const KeptAt a = kept_at<VEC>(rows, I, groups);
+  if (!a.on) return;
+  const size_t r = (size_t)a.row * 2 * I;
+  const float* sc = scales + (size_t)a.row * 2 * groups + a.group;
+  float g[kKeptCols], u[kKeptCols], d[kKeptCols], dg[kKeptCols], du[kKeptCols], f[kKeptCols];
+  kept8<VEC>(codes, r, a, sc[0], g);
+  kept8<VEC>(codes, r + I, a, sc[groups], u);
+  load8<BF16, VEC>(dh, (size_t)a.row * I, a, d);
+#pragma unroll
+  for (int i = 0; i < kKeptCols; ++i) {
+    const Sigmoid s(g[i]);
+    const float gs = g[i] * s.s;
+    dg[i] = d[i] * u[i] * fmaf(gs, s.t, s.s);
+    du[i] = d[i] * gs;
+    f[i] = gs * u[i];
+  }
+  store8<BF16, VEC>(dgu, r, a, dg);
+  store8<BF16, VEC>(dgu, r + I, a, du);
+  if (h) store8<BF16, VEC>(h, (size_t)a.row * I, a, f);
+}
+
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+template <typename F>
+void with_kinds(bool bf16, bool vec, const F& f) {
+  if (bf16 && vec) f(std::true_type{}, std::true_type{});
+  else if (bf16) f(std::true_type{}, std::false_type{});
+  else if (vec) f(std::false_type{}, std::true_type{});
+  else f(std::false_type{}, std::false_type{});
+}
+
+}  // namespace
+
+hipError_t launch_swiglu_save(const void* gu, bool bf16, int rows, const int32_t* n_rows, int I, void* h,
+                              int8_t* codes, float* scales, hipStream_t s) {
+  const int groups = (I + kKeptGroup - 1) / kKeptGroup;
+  const unsigned grid = (unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256);
+  const bool vec = I % 8 == 0 && aligned_to(gu, 16) && aligned_to(h, 16) && aligned_to(codes, 8);
+  with_kinds(bf16, vec, [&](auto b, auto v) {
+    hipLaunchKernelGGL((swiglu_save_kernel<decltype(b)::value, decltype(v)::value>), dim3(grid), dim3(256), 0, s, gu,
+                       (int64_t)rows, n_rows, I, groups, h, codes, scales);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_backward(const int8_t* codes, const float* scales, const void* dh, bool bf16, int rows,
+                                  const int32_t* n_rows, int I, void* dgu, void* h, hipStream_t s) {
+  const int groups = (I + kKeptGroup - 1) / kKeptGroup;
+  const unsigned grid = (unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256);
+  const bool vec = I % 8 == 0 && aligned_to(dh, 16) && aligned_to(dgu, 16) && aligned_to(h, 16) && aligned_to(codes, 8);
+  with_kinds(bf16, vec, [&](auto b, auto v) {
+    hipLaunchKernelGGL((swiglu_backward_kernel<decltype(b)::value, decltype(v)::value>), dim3(grid), dim3(256), 0, s,
+                       codes, scales, dh, (int64_t)rows, n_rows, I, groups, dgu, h);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

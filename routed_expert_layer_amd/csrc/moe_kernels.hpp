@@ -287,6 +287,29 @@ hipError_t launch_dev_fill(const DevCache& c, const void* pool, size_t blob_stri
 // Host: reads one byte per page of a pool region on the CPU thread pool.
 void cpu_touch_pages(const void* p, size_t bytes);
 
+// ---------------------------------------------------------------------------
+// Training through the layer (kernels_rows, kernels_swiglu8, kernels_matmul):
+// arguments as the moe_* calls of include/moe.h, checked there.
+// ---------------------------------------------------------------------------
+size_t group_workspace_bytes(int T, int k, int E);
+hipError_t launch_group(const int32_t* idx, int T, int k, int E, int32_t* counts, int32_t* offsets, int32_t* perm_src,
+                        int32_t* perm_pos, void* ws, hipStream_t s);
+hipError_t launch_dispatch(const void* x, bool bf16, const int32_t* pos, int T, int k, int H, int rows, void* out,
+                           hipStream_t s);
+hipError_t launch_collect(const void* rows, bool bf16, const int32_t* pos, const float* w, int T, int k, int H,
+                          int n_rows, void* out, bool out_bf16, hipStream_t s);
+hipError_t launch_collect_backward(const void* dout, bool out_bf16, const void* rows, bool bf16, const int32_t* pos,
+                                   const float* w, int T, int k, int H, int n_rows, void* drows, float* dw,
+                                   hipStream_t s);
+hipError_t launch_swiglu_save(const void* gu, bool bf16, int rows, const int32_t* n_rows, int I, void* h,
+                              int8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_swiglu_backward(const int8_t* codes, const float* scales, const void* dh, bool bf16, int rows,
+                                  const int32_t* n_rows, int I, void* dgu, void* h, hipStream_t s);
+hipError_t launch_matmul_grouped(const void* a, const void* w, const int32_t* counts, const int32_t* offsets, int E,
+                                 int rows_max, int K, int N, bool transposed, void* c, bool out_bf16, hipStream_t s);
+hipError_t launch_matmul_grouped_dw(const void* a, const void* dc, const int32_t* counts, const int32_t* offsets, int E,
+                                    int rows_max, int K, int N, void* dw, bool out_bf16, hipStream_t s);
+
 // Sets the calling thread's moe_last_error() message; returns `code`.
 int set_error(int code, const char* fmt, ...);
 
