@@ -362,3 +362,66 @@ class PrefillLayer:
         T = x.shape[0] if T is None else T
         L.moe_ffn_grouped(x, self.rb.perm_src, self.rb.counts, self.rb.offsets, None, self.E, T * self.k,
                           layer_base, self.stride, self.wfmt, self.H, self.I, self.y_perm, self.ffn_ws, stream)
+
+
+class TrainExperts:
+    """The expert half of a layer with its backward pass, on row-major bf16 weights W13 [E, H, 2I] (gate columns, then
+    up) and W2 [E, I, H], for the choices of any gate (entries outside [0, E) are experts of another GPU: dropped).
+
+    Between forward and backward a layer keeps, for each chosen row, the token (bf16), the expert's output (bf16) and the
+    SwiGLU inputs in 8 bits with a scale for 128 columns: 4H + 2I (1 + 4/128) bytes. The rest is scratch, which layers
+    of one size that run one after another on one stream may share (`scratch` of another TrainExperts). Every call
+    only enqueues work on the stream, so both passes can be captured; the gate's own gradient starts at the returned
+    gradient of topk_w."""
+
+    def __init__(self, H, I, E, k, T, device="cuda", scratch=None):
+        self.H, self.I, self.E, self.k, self.T = H, I, E, k, T
+        rows = max(T * k, 1)
+        i32 = dict(dtype=torch.int32, device=device)
+        bf = dict(dtype=torch.bfloat16, device=device)
+        self.counts, self.offsets = torch.zeros(E, **i32), torch.zeros(E + 1, **i32)
+        self.perm_src, self.perm_pos = torch.zeros(rows, **i32), torch.zeros((T, k), **i32)
+        self.group_ws = torch.empty(max(L.moe_group_workspace_size(T, k, E), 4), dtype=torch.uint8, device=device)
+        self.x_perm, self.y_perm = torch.empty((rows, H), **bf), torch.empty((rows, H), **bf)
+        self.codes = torch.empty((rows, 2 * I), dtype=torch.int8, device=device)
+        self.scales = torch.empty((rows, 2 * ((I + 127) // 128)), device=device)
+        if scratch is None:
+            scratch = dict(gu=torch.empty((rows, 2 * I), **bf), h=torch.empty((rows, I), **bf),
+                           dh=torch.empty((rows, I), **bf), dy=torch.empty((rows, H), **bf))
+        if scratch["gu"].shape != (rows, 2 * I) or scratch["dy"].shape != (rows, H):
+            raise ValueError("scratch of a layer of another size")
+        self.scratch = scratch
+        self.topk_w = None
+
+    def forward(self, x, topk_idx, topk_w, W13, W2, out, stream=None):
+        """out [T, H] (float32 or bfloat16) = sum_j topk_w[t, j] expert(topk_idx[t, j])(x[t]); x bf16 [T, H]. topk_w is
+        read again by backward."""
+        T = x.shape[0]
+        if T > self.T:
+            raise ValueError(f"{T} tokens, and buffers for {self.T}")
+        n, sc, pos = T * self.k, self.scratch, self.perm_pos[:T]
+        L.moe_group(topk_idx, self.E, self.counts, self.offsets, self.perm_src, pos, self.group_ws, stream)
+        L.moe_dispatch(x, pos, self.x_perm[:n], stream)
+        L.moe_matmul_grouped(self.x_perm[:n], W13, self.counts, self.offsets, sc["gu"][:n], stream=stream)
+        L.moe_swiglu_save(sc["gu"][:n], sc["h"][:n], self.codes[:n], self.scales[:n], self.offsets[self.E:], stream)
+        L.moe_matmul_grouped(sc["h"][:n], W2, self.counts, self.offsets, self.y_perm[:n], stream=stream)
+        L.moe_collect(self.y_perm[:n], pos, topk_w, out, stream)
+        self.topk_w = topk_w
+        return out
+
+    def backward(self, dout, W13, W2, dx, dtopk_w, dW13, dW2, stream=None):
+        """The gradients of the last forward for dout [T, H] (float32 or bfloat16): dx [T, H], dtopk_w fp32 [T, k],
+        dW13 and dW2 (float32 or bfloat16). What forward kept is used up."""
+        if self.topk_w is None:
+            raise RuntimeError("backward without a forward before it")
+        T = dout.shape[0]
+        n, sc, pos, w = T * self.k, self.scratch, self.perm_pos[:T], self.topk_w
+        dy, dh, h, dgu, dx_perm = sc["dy"][:n], sc["dh"][:n], sc["h"][:n], sc["gu"][:n], self.y_perm[:n]
+        L.moe_collect_backward(dout, self.y_perm[:n], pos, w, dy, dtopk_w, stream)
+        L.moe_matmul_grouped(dy, W2, self.counts, self.offsets, dh, transposed=True, stream=stream)
+        L.moe_swiglu_backward(self.codes[:n], self.scales[:n], dh, dgu, h, self.offsets[self.E:], stream)
+        L.moe_matmul_grouped_dw(h, dy, self.counts, self.offsets, dW2, stream)
+        L.moe_matmul_grouped_dw(self.x_perm[:n], dgu, self.counts, self.offsets, dW13, stream)
+        L.moe_matmul_grouped(dgu, W13, self.counts, self.offsets, dx_perm, transposed=True, stream=stream)
+        L.moe_collect(dx_perm, pos, None, dx, stream)
+        self.topk_w = None
