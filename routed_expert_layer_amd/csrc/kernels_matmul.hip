@@ -4,16 +4,18 @@
 //   rows:    c[r, :] = a[r, :] W_e          (or W_e^T: the gradient of the rows)
 //   weights: dW_e = sum over the rows r of e of a[r, :]^T dc[r, :]   (0 for an expert without rows)
 //
-// One tile kernel: BM x 256 results, 32 steps of the sum per stage, operands
-// straight from global memory into LDS (16 bytes a lane, no registers), NS
-// stages in flight, one barrier per stage; a wave reads the next stage's
-// fragments into a second register set while its matrix-core instructions use
-// the current one. Operands stay as they lie in memory: one whose sum index is
-// the fast one (rows of a, W^T) is read as 16-byte pieces of its rows, one
-// whose sum index is the slow one (W, and both sides of the weight gradient)
-// through the transposing LDS read (four 16-bit values down a column for each
-// of 16 lanes). Both are stored with their pieces exchanged by an XOR of the
-// row, so that the reads of a wave fall on all banks.
+// One tile kernel: BM x 256 results, the sum in parts of 32 steps, operands
+// straight from global memory into LDS (16 bytes a lane, no registers), one
+// barrier per part; a wave reads the fragments of the next part into a second
+// register set while its matrix-core instructions use the current one.
+// Operands stay as they lie in memory: one whose sum index is the fast one
+// (rows of a, W^T) is read as 16-byte pieces of its rows, one whose sum index
+// is the slow one (W, and both sides of the weight gradient) through the
+// transposing LDS read (four 16-bit values down a column for each of 16
+// lanes). Both are stored with their pieces exchanged by an XOR of the row, so
+// that the reads of a wave fall on all banks. Each operand has a ring of its
+// own in LDS: of parts for a slow one, of pairs of parts for a fast one, whose
+// rows then come in whole cache lines.
 #include <algorithm>
 #include <type_traits>
 
@@ -27,82 +29,117 @@ namespace {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kBN = 256;     // columns of a tile
-constexpr int kStep = 32;    // sum steps of a stage
+constexpr int kPart = 32;    // sum steps of a part
 constexpr uint32_t kNone = 0x80000000u;  // a lane offset past every buffer: the load returns zeros
 
-// One operand of a tile: SIZE rows or columns of results, kStep of the sum per
-// stage. SLOW: the sum index is the slow one in memory.
+// One operand of a tile: SIZE rows or columns of results. SLOW: the sum index
+// is the slow one in memory. A slot of its ring holds kStep of the sum.
+template <typename T>
+struct type_of {
+  using type = T;
+};
+
 template <bool SLOW, int SIZE>
 struct Side {
-  static constexpr int kLoads = SIZE / 16;           // 1 KiB loads per stage
-  static constexpr int kBytes = SIZE * kStep * 2;    // LDS bytes per stage
-  // Fast: LDS holds SIZE rows of four 16-byte pieces, piece c of row r in slot c ^ (r / 2 % 4): eight rows' pieces of
+  static constexpr int kParts = SLOW ? 1 : 2, kStep = kPart * kParts;
+  static constexpr int kBytes = SIZE * kStep * 2;    // of a slot
+  static constexpr int kLoads = kBytes / 1024;       // 1 KiB loads per slot
+  // Fast: a slot holds SIZE rows of eight 16-byte pieces, piece c of row r in place c ^ turn(r): eight rows' pieces of
   // one c, which a wave reads together, lie in 128 different bytes of the banks.
-  // Slow: LDS holds kStep rows of SIZE columns; the 32-byte pair of pieces p of row k in place p ^ turn(k).
-  static __device__ __forceinline__ int turn(int k) {
-    return SIZE >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+  // Slow: a slot holds 32 rows of SIZE columns; the 32-byte pair of pieces p of row k in place p ^ turn(k).
+  static __device__ __forceinline__ int turn(int r) {
+    if constexpr (!SLOW) return r & 7;
+    return SIZE >= 128 ? (r & 3) | ((r >> 3) & 1) << 2 : ((r >> 1) & 1) | ((r >> 3) & 1) << 1;
   }
-  // Byte offset of what this lane fetches with load f of a stage, from the tile's first element; `lim` results are in
-  // the operand from there on (past them the last ones are fetched, for results that are not stored). ld in elements.
+  // Byte offset of what this lane fetches with load f of a slot, from the tile's first element; `lim` results are in
+  // the operand from there on (nothing is fetched for those past them). ld in elements.
   static __device__ __forceinline__ uint32_t fetch(int f, int lane, int ld, int lim) {
     if constexpr (SLOW) {
       constexpr int kLanes = SIZE / 8;  // lanes per row
       const int k = f * (64 / kLanes) + lane / kLanes, slot = lane % kLanes;
       const int col = ((((slot >> 1) ^ turn(k)) << 1) | (slot & 1)) * 8;
-      return (uint32_t)(k * ld + min(col, lim - 8)) * 2u;
+      return col < lim ? (uint32_t)(k * ld + col) * 2u : kNone;
     } else {
-      const int r = f * 16 + lane / 4;
-      return (uint32_t)min(r, lim - 1) * (uint32_t)ld * 2u + (uint32_t)((lane & 3) ^ ((r >> 1) & 3)) * 16u;
+      const int r = f * 8 + lane / 8;
+      return r < lim ? (uint32_t)r * (uint32_t)ld * 2u + (uint32_t)((lane & 7) ^ turn(r)) * 16u : kNone;
     }
   }
-  // The first of the eight sum steps (of a stage's 32) that this lane fetches; fast operands only.
-  static __device__ __forceinline__ int step_of(int lane) { return ((lane & 3) ^ ((lane >> 3) & 3)) * 8; }
+  // The first of the eight sum steps (of a slot's) that this lane fetches; fast operands only.
+  static __device__ __forceinline__ int step_of(int lane) { return ((lane & 7) ^ turn(lane / 8)) * 8; }
 };
 
-// Fragments of 16 results x 32 steps: lane l holds result l % 16, steps 8 (l / 16) .. + 7.
+// Fragments of 16 results x 32 steps, part h of a slot: lane l holds result l % 16, steps 8 (l / 16) .. + 7.
 template <bool SLOW, int SIZE, int N>
 struct Reader {
-  uint32_t at[SLOW ? N : 1];
+  using S = Side<SLOW, SIZE>;
+  uint32_t at[SLOW ? N : 2];
   __device__ __forceinline__ Reader(int first, int lane) {
     if constexpr (SLOW) {
       const int k = 8 * (lane >> 4) + ((lane & 15) >> 2), q = lane & 3;
 #pragma unroll
-      for (int i = 0; i < N; ++i) at[i] = k * SIZE * 2 + (((first + i) ^ Side<SLOW, SIZE>::turn(k)) << 5) + q * 8;
+      for (int i = 0; i < N; ++i) at[i] = k * SIZE * 2 + (((first + i) ^ S::turn(k)) << 5) + q * 8;
     } else {
       const int r = lane & 15;
-      at[0] = (first * 16 + r) * 64 + (((lane >> 4) ^ ((r >> 1) & 3)) << 4);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) at[h] = (first * 16 + r) * (S::kStep * 2) + (((4 * h + (lane >> 4)) ^ S::turn(r)) << 4);
     }
   }
-  __device__ __forceinline__ u32x4_t read(const char* stage, int i) const {
+  __device__ __forceinline__ u32x4_t read(const char* slot, int h, int i) const {
     if constexpr (SLOW) {
       using P = __attribute__((address_space(3))) s16x4_t*;
-      const char* p = stage + at[i];
+      const char* p = slot + at[i];
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
       const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(p + 4 * SIZE * 2));
       const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
       return u32x4_t{a[0], a[1], b[0], b[1]};
     } else {
-      return *reinterpret_cast<const u32x4_t*>(stage + at[0] + i * 1024);
+      return *reinterpret_cast<const u32x4_t*>(slot + at[h] + i * (16 * S::kStep * 2));
     }
   }
 };
 
-// One 16-byte piece per lane from base + off straight into the wave's 1 KiB at LDS byte `lds`; a lane offset of `bytes` or
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
+// N times 1 KiB, 16 bytes a lane, from base + off[i] straight into LDS at byte lds + i * APART; a lane offset of `bytes` or
 // more fetches zeros. In assembly, because the compiler waits for every load to LDS it knows of before a transposing read
-// (s_waitcnt vmcnt(0) in each stage); nothing is returned in registers, and the waits for the data are the explicit ones
+// (s_waitcnt vmcnt(0) in each part); nothing is returned in registers, and the waits for the data are the explicit ones
 // of the loop below. Five wait states stand between a vector instruction that may have written a scalar operand and the
-// load, one between the write of m0 (which nothing else in these kernels uses) and the load.
-__device__ __forceinline__ void load_lds16(const void* base, uint32_t bytes, uint32_t off, uint32_t lds) {
+// first load, one between a write of m0 (which nothing else in these kernels uses) and the load.
+template <int N, int APART>
+__device__ __forceinline__ void load_lds(const void* base, uint32_t bytes, const uint32_t (&off)[N], uint32_t lds) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
-  const u32x4_t r{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, bytes, 0x00020000u};
-  asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :
-               : "v"(off), "s"(r), "s"(lds)
-               : "memory");
+  const u32x4_t r{uniform((uint32_t)p), uniform((uint32_t)(p >> 32) & 0xFFFFu), uniform(bytes), 0x00020000u};
+  lds = uniform(lds);
+  static_assert(N == 1 || N == 2 || N == 4 || N == 8, "loads of an operand per wave");
+  if constexpr (N == 8) {
+    const uint32_t lo[4] = {off[0], off[1], off[2], off[3]}, hi[4] = {off[4], off[5], off[6], off[7]};
+    load_lds<4, APART>(base, bytes, lo, lds);
+    load_lds<4, APART>(base, bytes, hi, lds + 4 * APART);
+    return;
+  }
+  if constexpr (N == 1)
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :
+                 : "v"(off[0]), "s"(r), "s"(lds)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %2, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "v"(off[0]), "v"(off[1]), "s"(r), "s"(lds), "i"(APART)
+                 : "memory", "scc");
+  else if constexpr (N == 4)
+    asm volatile("s_nop 4\n\ts_mov_b32 m0, %5\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %4, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %4, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %4, 0 offen lds\n\t"
+                 "s_add_u32 m0, m0, %6\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %4, 0 offen lds"
+                 :
+                 : "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(r), "s"(lds), "i"(APART)
+                 : "memory", "scc");
 }
 
-// What one tile works on. a and b point at the tile's first element; lda and ldb are elements per row of memory; m and n
-// results are left from the tile's first on, `depth` sum steps.
+// What one tile works on. a and b point at the tile's first element, lda, ldb and ldc are elements per row of memory; m
+// and n results are left from the tile's first on, `depth` sum steps.
 struct Tile {
   const uint16_t* a;
   const uint16_t* b;
@@ -110,43 +147,75 @@ struct Tile {
   int lda, ldb, ldc, m, n, depth;
 };
 
-template <int BM, int WAVES_M, int WAVES_N, int NS, bool SLOW_A, bool SLOW_B, bool OUT_BF16>
+// Turn p of the loop below waits for what part p + 1 needs, and sends for what goes into the slots that part p used for
+// the last time: part p + ring of a slow operand, the pair p / 2 + ring of a fast one behind an odd part. LA, LB loads
+// each. What may still be under way behind turn p's wait: the loads sent after the last one that part p + 1 needs.
+constexpr int loads_ahead(bool slow_a, int ring_a, int la, bool slow_b, int ring_b, int lb, int parity) {
+  const int p = 64 + parity;
+  int after = 0;
+  for (int q = 0; q < p; ++q) {
+    if (slow_a || q % 2 == 1) {
+      after += la;
+      if (slow_a ? q + ring_a == p + 1 : (q - 1) / 2 + ring_a == (p + 1) / 2) after = 0;
+    }
+    if (slow_b || q % 2 == 1) {
+      after += lb;
+      if (slow_b ? q + ring_b == p + 1 : (q - 1) / 2 + ring_b == (p + 1) / 2) after = 0;
+    }
+  }
+  return after;
+}
+
+template <int BM, int RA, int RB, bool SLOW_A, bool SLOW_B>
+constexpr int kLdsBytes = RA * Side<SLOW_A, BM>::kBytes + RB * Side<SLOW_B, kBN>::kBytes;
+
+template <int BM, int WAVES_M, int WAVES_N, int RA, int RB, bool SLOW_A, bool SLOW_B, bool OUT_BF16>
 __device__ __forceinline__ void tile_product(const Tile& t, char* lds) {
   constexpr int kWaves = WAVES_M * WAVES_N;
   using A = Side<SLOW_A, BM>;
   using B = Side<SLOW_B, kBN>;
-  constexpr int kStage = A::kBytes + B::kBytes;
   constexpr int MF = BM / WAVES_M / 16, NF = kBN / WAVES_N / 16;  // fragments per wave
-  constexpr int LA = A::kLoads / kWaves, LB = B::kLoads / kWaves, L = LA + LB;
+  constexpr int LA = A::kLoads / kWaves, LB = B::kLoads / kWaves;
   static_assert(A::kLoads % kWaves == 0 && B::kLoads % kWaves == 0, "loads split over the waves");
-  const int tid = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  constexpr int kAhead[2] = {loads_ahead(SLOW_A, RA, LA, SLOW_B, RB, LB, 0),
+                             loads_ahead(SLOW_A, RA, LA, SLOW_B, RB, LB, 1)};
+  static_assert(kAhead[0] < 64 && kAhead[1] < 64, "vmcnt counts to 63");
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int wm = wave % WAVES_M, wn = wave / WAVES_M;
-  const int stages = (t.depth + kStep - 1) / kStep, tail = t.depth % kStep;
+  const int parts = (t.depth + kPart - 1) / kPart;
 
-  uint32_t off[L];
+  uint32_t off_a[LA], off_b[LB];  // lane offsets of a slot's loads
 #pragma unroll
-  for (int q = 0; q < LA; ++q) off[q] = A::fetch(wave + kWaves * q, lane, t.lda, t.m);
+  for (int q = 0; q < LA; ++q) off_a[q] = A::fetch(wave + kWaves * q, lane, t.lda, t.m);
 #pragma unroll
-  for (int q = 0; q < LB; ++q) off[LA + q] = B::fetch(wave + kWaves * q, lane, t.ldb, t.n);
-  const bool none = tail != 0 && A::step_of(lane) >= tail;  // past the sum's end in the last stage
-
-  // Stage s -> LDS buffer `buf`. Steps past the sum's end are zeros on both sides: of a slow operand by the buffer's
-  // size, of a fast one by the lane offset.
-  auto issue = [&](int s, int buf) {
-    const uint32_t base = lds0 + buf * kStage;
-    const bool last = s == stages - 1;
-    const uint32_t left = (uint32_t)min(kStep, t.depth - s * kStep);
-    const uint16_t* pa = t.a + (SLOW_A ? (size_t)s * kStep * t.lda : (size_t)s * kStep);
-    const uint16_t* pb = t.b + (SLOW_B ? (size_t)s * kStep * t.ldb : (size_t)s * kStep);
-    const uint32_t na = SLOW_A ? left * (uint32_t)t.lda * 2u : kNone;
-    const uint32_t nb = SLOW_B ? left * (uint32_t)t.ldb * 2u : kNone;
+  for (int q = 0; q < LB; ++q) off_b[q] = B::fetch(wave + kWaves * q, lane, t.ldb, t.n);
+  // Slot number s of an operand (s kStep of the sum before it) -> LDS byte `to`. Steps past the sum's end are zeros on
+  // both sides, without a fetch: of a slow operand by the buffer's size, of a fast one by the lane offset.
+  auto send = [&](auto side, auto& off, const uint16_t* p, int ld, int s, uint32_t to) {
+    using S = typename decltype(side)::type;
+    constexpr int n = sizeof(off) / sizeof(off[0]);
+    const int left = t.depth - s * S::kStep;
+    if constexpr (S::kParts == 1) {
+      load_lds<n, kWaves * 1024>(p + (int64_t)s * S::kStep * ld, (uint32_t)max(0, min(S::kStep, left)) * (uint32_t)ld * 2u,
+                                 off, to + wave * 1024);
+    } else if (left >= S::kStep) {
+      load_lds<n, kWaves * 1024>(p + (int64_t)s * S::kStep, kNone, off, to + wave * 1024);
+    } else {
+      uint32_t part[n];
 #pragma unroll
-    for (int q = 0; q < LA; ++q)
-      load_lds16(pa, na, !SLOW_A && last && none ? kNone : off[q], base + (wave + kWaves * q) * 1024);
-#pragma unroll
-    for (int q = 0; q < LB; ++q)
-      load_lds16(pb, nb, !SLOW_B && last && none ? kNone : off[LA + q], base + A::kBytes + (wave + kWaves * q) * 1024);
+      for (int q = 0; q < n; ++q) part[q] = S::step_of(lane) < left ? off[q] : kNone;
+      load_lds<n, kWaves * 1024>(p + (int64_t)s * S::kStep, kNone, part, to + wave * 1024);
+    }
+  };
+  constexpr type_of<A> side_a{};
+  constexpr type_of<B> side_b{};
+  // Turn p: the slots (by number modulo the ring) that part p leaves, filled again.
+  auto refill = [&](int p, int parity, int slot_a, int slot_b) {
+    if (SLOW_A || parity == 1)
+      send(side_a, off_a, t.a, t.lda, (SLOW_A ? p : (p - 1) / 2) + RA, lds0 + slot_a * A::kBytes);
+    if (SLOW_B || parity == 1)
+      send(side_b, off_b, t.b, t.ldb, (SLOW_B ? p : (p - 1) / 2) + RB, lds0 + RA * A::kBytes + slot_b * B::kBytes);
   };
 
   const Reader<SLOW_A, BM, MF> ra(wm * MF, lane);
@@ -163,13 +232,14 @@ __device__ __forceinline__ void tile_product(const Tile& t, char* lds) {
   // JM: this wave's fragments of rows that hold any result (uniform per wave).
   auto sum = [&](auto jm_const) {
     constexpr int JM = decltype(jm_const)::value;
-    auto read = [&](int s, Frags& f) {
-      const char* base = lds + (s % NS) * kStage;
+    auto read = [&](int slot_a, int slot_b, int parity, Frags& f) {
+      const char* pa = lds + slot_a * A::kBytes;
+      const char* pb = lds + RA * A::kBytes + slot_b * B::kBytes;
       if constexpr (JM > 0) {
 #pragma unroll
-        for (int j = 0; j < JM; ++j) f.a[j] = ra.read(base, j);
+        for (int j = 0; j < JM; ++j) f.a[j] = ra.read(pa, parity, j);
 #pragma unroll
-        for (int i = 0; i < NF; ++i) f.b[i] = rb.read(base + A::kBytes, i);
+        for (int i = 0; i < NF; ++i) f.b[i] = rb.read(pb, parity, i);
       }
     };
     auto compute = [&](const Frags& f) {
@@ -177,51 +247,67 @@ __device__ __forceinline__ void tile_product(const Tile& t, char* lds) {
       for (int i = 0; i < NF; ++i)
 #pragma unroll
         for (int j = 0; j < JM; ++j) acc[i][j] = mfma_bf16(f.b[i], f.a[j], acc[i][j]);
-    };
-    auto step = [&](int s, Frags& cur, Frags& nxt) {
-      // this wave's loads of stage s + 1 have landed, and its reads of stage s
-      if (s + NS - 1 < stages) {
-        __builtin_amdgcn_s_waitcnt(vmcnt_only(L * (NS - 2)));
-      } else {
-        __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
-      }
-      __builtin_amdgcn_s_waitcnt(lgkmcnt_only(0));
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      if (s + NS < stages) issue(s + NS, s % NS);
-      read(min(s + 1, stages - 1), nxt);
-      compute(cur);
+      // one LDS read, then a share of the matrix-core instructions, in turn
       if constexpr (JM > 0) {
         constexpr int kReads = JM * (SLOW_A ? 2 : 1) + NF * (SLOW_B ? 2 : 1);
-        constexpr int kPer = (NF * JM) / kReads > 0 ? (NF * JM) / kReads : 1;
+        constexpr int kEach = (NF * JM) / kReads > 0 ? (NF * JM) / kReads : 1;
 #pragma unroll
         for (int q = 0; q < kReads; ++q) {
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
         }
       }
     };
-    for (int s = 0; s < NS && s < stages; ++s) issue(s, s);
-    if (stages >= NS) {
-      __builtin_amdgcn_s_waitcnt(vmcnt_only(L * (NS - 1)));
-    } else {
-      __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    int slot_a = 0, slot_b = 0;  // of the part that is read next
+    auto advance = [&](int parity) {
+      if (SLOW_A || parity == 1) slot_a = slot_a + 1 == RA ? 0 : slot_a + 1;
+      if (SLOW_B || parity == 1) slot_b = slot_b + 1 == RB ? 0 : slot_b + 1;
+    };
+    // This wave's loads for part p + 1 have landed and its reads of part p are done; behind the barrier every wave's.
+    auto meet = [&](auto parity) {
+      __builtin_amdgcn_s_waitcnt(vmcnt_only(kAhead[decltype(parity)::value]));
+      __builtin_amdgcn_s_waitcnt(lgkmcnt_only(0));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    // the first parts, in the order of the turns that would have sent for them
+    constexpr int kFirst = (SLOW_A ? RA : 2 * RA) > (SLOW_B ? RB : 2 * RB) ? (SLOW_A ? RA : 2 * RA) : (SLOW_B ? RB : 2 * RB);
+#pragma unroll
+    for (int q = -kFirst; q < 0; ++q) {
+      if (q == -1) meet(odd);
+      if ((SLOW_A || (q & 1)) && (SLOW_A ? q : (q - 1) / 2) + RA >= 0) {
+        const int n = (SLOW_A ? q : (q - 1) / 2) + RA;
+        send(side_a, off_a, t.a, t.lda, n, lds0 + n * A::kBytes);
+      }
+      if ((SLOW_B || (q & 1)) && (SLOW_B ? q : (q - 1) / 2) + RB >= 0) {
+        const int n = (SLOW_B ? q : (q - 1) / 2) + RB;
+        send(side_b, off_b, t.b, t.ldb, n, lds0 + RA * A::kBytes + n * B::kBytes);
+      }
     }
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
     Frags f0, f1;
-    read(0, f0);
-    int s = 0;
-    for (; s + 1 < stages; s += 2) {
-      step(s, f0, f1);
-      step(s + 1, f1, f0);
+    read(0, 0, 0, f0);
+    int p = 0;
+    for (; p + 1 < parts; p += 2) {
+      meet(even);
+      refill(p, 0, slot_a, slot_b);
+      advance(0);
+      read(slot_a, slot_b, 1, f1);
+      compute(f0);
+      meet(odd);
+      refill(p + 1, 1, slot_a, slot_b);
+      advance(1);
+      read(slot_a, slot_b, 0, f0);
+      compute(f1);
     }
-    if (s < stages) step(s, f0, f1);
+    if (p < parts) compute(f0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_only(0));  // no load to LDS outlives the tile
   };
   static_assert(MF % 4 == 0, "the dispatch below takes quarters");
   const int rows_here = t.m - wm * MF * 16;
   const int quarter = rows_here <= 0 ? 0 : min(4, (rows_here + MF * 4 - 1) / (MF * 4));
-  if (stages > 0) switch (quarter) {
+  if (parts > 0) switch (quarter) {
     case 0: sum(std::integral_constant<int, 0>{}); break;
     case 1: sum(std::integral_constant<int, MF / 4>{}); break;
     case 2: sum(std::integral_constant<int, MF / 2>{}); break;
@@ -229,22 +315,29 @@ __device__ __forceinline__ void tile_product(const Tile& t, char* lds) {
     default: sum(std::integral_constant<int, MF>{}); break;
   }
 
-  // Lane l holds row l % 16 of a fragment and its columns 4 (l / 16) .. + 3.
+  // Lane l holds row l % 16 of a fragment and its columns 4 (l / 16) .. + 3. Of bf16 results two fragments exchange
+  // halves between neighbouring rows of 16 lanes, so that a lane has eight columns and four lanes 32.
   const int g = lane >> 4;
 #pragma unroll
   for (int j = 0; j < MF; ++j) {
     const int m = (wm * MF + j) * 16 + (lane & 15);
+    if constexpr (OUT_BF16) {
+      typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+      auto pack = [](float x, float y) { return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)x, (__bf16)y}); };
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      const int n = (wn * NF + i) * 16 + 4 * g;
-      if (m >= t.m || n >= t.n) continue;
-      const f32x4_t v = acc[i][j];
-      if constexpr (OUT_BF16) {
-        typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<u32x2_t*>(t.c + ((size_t)m * t.ldc + n) * 2) =
-            __builtin_bit_cast(u32x2_t, bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]});
-      } else {
-        *reinterpret_cast<f32x4_t*>(t.c + ((size_t)m * t.ldc + n) * 4) = v;
+      for (int i = 0; i < NF; i += 2) {
+        const f32x4_t v = acc[i][j], w = acc[i + 1][j];
+        const auto lo = __builtin_amdgcn_permlane16_swap(pack(v[0], v[1]), pack(w[0], w[1]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(pack(v[2], v[3]), pack(w[2], w[3]), false, false);
+        const int n = (wn * NF + i + (g & 1)) * 16 + 8 * (g >> 1);
+        if (m < t.m && n < t.n)
+          *reinterpret_cast<u32x4_t*>(t.c + ((size_t)m * t.ldc + n) * 2) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        const int n = (wn * NF + i) * 16 + 4 * g;
+        if (m < t.m && n < t.n) *reinterpret_cast<f32x4_t*>(t.c + ((size_t)m * t.ldc + n) * 4) = acc[i][j];
       }
     }
   }
@@ -257,18 +350,41 @@ __device__ __forceinline__ int group_of(const int32_t* counts, const int32_t* of
   return n > 0 && first >= 0 && n <= rows_max && first <= rows_max - n ? n : 0;
 }
 
-struct RowTile {
-  int e, first, rows, m, n;  // expert, its first row and rows, tile indexes; e < 0: none
-};
+// The tile of this block among `total`, or -1. The blocks of one XCD (equal block index modulo 8) run 32 at a time, on 32
+// consecutive tiles, which share operands in its L2; the next 32 go to the next XCD, so that an expert with many tiles is
+// spread over all of them. Fewer than 256 tiles are spread evenly.
+constexpr int kRun = 32;
+__device__ __forceinline__ int64_t tile_index(int64_t total) {
+  const int x = (int)(blockIdx.x & 7), q = (int)(blockIdx.x >> 3);
+  const int run = (int)min((int64_t)kRun, (total + 7) / 8), slot = q % kRun;
+  const int64_t at = ((int64_t)(q / kRun) * 8 + x) * run + slot;
+  return slot < run && at < total ? at : -1;
+}
+unsigned tile_blocks(int64_t tiles) { return (unsigned)((tiles + 8 * kRun - 1) / (8 * kRun) * 8 * kRun); }
 
-// Tile number `index` of all experts' tiles (expert, then column tile, then row tile), BM rows and kBN columns each; the
-// blocks of one XCD (equal index modulo 8) take consecutive ones, so that the blocks that run together on it share an
-// expert's rows and columns in its L2.
-template <int BM, int THREADS>
-__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ counts, const int32_t* __restrict__ offsets,
-                                             int E, int rows_max, int col_tiles, int* sums, RowTile* found) {
+// Place of tile number `left` of `rows` x `cols`: bands of eight rows, in them column by column.
+__device__ __forceinline__ void tile_place(int left, int rows, int cols, int& m, int& n) {
+  const int band = left / (8 * cols), in = left - band * 8 * cols, high = min(8, rows - band * 8);
+  m = band * 8 + in % high;
+  n = in / high;
+}
+
+template <int BM, int WAVES_M, int WAVES_N, int RA, int RB, int OCC, bool TRANSPOSED, bool OUT_BF16>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void matmul_rows_kernel(
+    const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, const int32_t* __restrict__ counts,
+    const int32_t* __restrict__ offsets, int E, int rows_max, int K, int N, char* __restrict__ c) {
+  constexpr int kThreads = 64 * WAVES_M * WAVES_N;
+  __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes<BM, RA, RB, false, !TRANSPOSED>];
+  const int depth = TRANSPOSED ? N : K, width = TRANSPOSED ? K : N;
+  const int cols = (width + kBN - 1) / kBN;
+  // Which expert's tile this is: every thread counts the tiles of a few experts, and one of them finds it among its own.
+  struct Found {
+    int e, first, rows, m, n;
+  };
+  int* sums = reinterpret_cast<int*>(lds);
+  Found* found = reinterpret_cast<Found*>(lds + 64 * sizeof(int));
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (E + THREADS - 1) / THREADS, e0 = tid * per, e1 = min(E, e0 + per);
+  const int each = (E + kThreads - 1) / kThreads, e0 = tid * each, e1 = min(E, e0 + each);
   int mine = 0, first;
   for (int e = e0; e < e1; ++e) mine += (group_of(counts, offsets, e, rows_max, first) + BM - 1) / BM;
   int s = mine;
@@ -280,41 +396,28 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ counts,
   if (lane == 63) sums[wave] = s;
   if (tid == 0) found->e = -1;
   __syncthreads();
-  int before = s - mine, total = 0;
+  int before = s - mine, all = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) {
-    before += w < wave ? sums[w] : 0;
-    total += sums[w];
+  for (int v = 0; v < kThreads / 64; ++v) {
+    before += v < wave ? sums[v] : 0;
+    all += sums[v];
   }
-  const int64_t all = (int64_t)total * col_tiles, share = (all + 7) / 8;
-  const int64_t at = (int64_t)(blockIdx.x >> 3), index = (blockIdx.x & 7) * share + at;
-  if (at < share && index < all) {
-    int64_t left = index - (int64_t)before * col_tiles;
-    if (left >= 0 && left < (int64_t)mine * col_tiles)
-      for (int e = e0; e < e1; ++e) {
-        const int n = group_of(counts, offsets, e, rows_max, first), tiles = (n + BM - 1) / BM;
-        if (left < (int64_t)tiles * col_tiles) {
-          *found = RowTile{e, first, n, (int)(left % tiles), (int)(left / tiles)};
-          break;
-        }
-        left -= (int64_t)tiles * col_tiles;
+  const int64_t index = tile_index((int64_t)all * cols);
+  int64_t left = index - (int64_t)before * cols;
+  if (index >= 0 && left >= 0 && left < (int64_t)mine * cols)
+    for (int e = e0; e < e1; ++e) {
+      const int n = group_of(counts, offsets, e, rows_max, first), tiles = (n + BM - 1) / BM;
+      if (left < (int64_t)tiles * cols) {
+        Found f{e, first, n, 0, 0};
+        tile_place((int)left, tiles, cols, f.m, f.n);
+        *found = f;
+        break;
       }
-  }
+      left -= (int64_t)tiles * cols;
+    }
   __syncthreads();
-  return *found;
-}
-
-template <int BM, int WAVES_M, int WAVES_N, int NS, bool TRANSPOSED, bool OUT_BF16>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, BM == 64 ? 2 : 1) void matmul_rows_kernel(
-    const uint16_t* __restrict__ a, const uint16_t* __restrict__ w, const int32_t* __restrict__ counts,
-    const int32_t* __restrict__ offsets, int E, int rows_max, int K, int N, char* __restrict__ c) {
-  __shared__ __attribute__((aligned(1024))) char lds[NS * (BM + kBN) * kStep * 2];
-  const int depth = TRANSPOSED ? N : K, width = TRANSPOSED ? K : N;
-  const int col_tiles = (width + kBN - 1) / kBN;
-  const RowTile f = find_tile<BM, 64 * WAVES_M * WAVES_N>(counts, offsets, E, rows_max, col_tiles,
-                                                          reinterpret_cast<int*>(lds),
-                                                          reinterpret_cast<RowTile*>(lds + 256));
-  __syncthreads();  // the stages overwrite what was found
+  const Found f = *found;
+  __syncthreads();  // the operands overwrite it
   const int e = __builtin_amdgcn_readfirstlane(f.e);
   if (e < 0) return;
   const int m0 = __builtin_amdgcn_readfirstlane(f.m) * BM, n0 = __builtin_amdgcn_readfirstlane(f.n) * kBN;
@@ -329,34 +432,32 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, BM == 64 ? 2 : 1) void matm
   t.m = __builtin_amdgcn_readfirstlane(f.rows) - m0;
   t.n = width - n0;
   t.depth = depth;
-  tile_product<BM, WAVES_M, WAVES_N, NS, false, !TRANSPOSED, OUT_BF16>(t, lds);
+  tile_product<BM, WAVES_M, WAVES_N, RA, RB, false, !TRANSPOSED, OUT_BF16>(t, lds);
 }
 
-template <int BM, int WAVES_M, int WAVES_N, int NS, bool OUT_BF16>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, BM == 64 ? 2 : 1) void matmul_dw_kernel(
+template <int BM, int WAVES_M, int WAVES_N, int RA, int RB, int OCC, bool OUT_BF16>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void matmul_dw_kernel(
     const uint16_t* __restrict__ a, const uint16_t* __restrict__ dc, const int32_t* __restrict__ counts,
-    const int32_t* __restrict__ offsets, int rows_max, int K, int N, char* __restrict__ dw) {
-  __shared__ __attribute__((aligned(1024))) char lds[NS * (BM + kBN) * kStep * 2];
-  const int row_tiles = (K + BM - 1) / BM, col_tiles = (N + kBN - 1) / kBN, tiles = row_tiles * col_tiles;
-  // as in find_tile: consecutive tiles to the blocks of one XCD
-  const unsigned share = gridDim.x / 8, extra = gridDim.x % 8, x = blockIdx.x & 7;
-  const unsigned index = x * share + min(x, extra) + (blockIdx.x >> 3);
-  const int e = (int)(index / tiles), left = (int)(index % tiles);
-  const int k0 = (left % row_tiles) * BM, n0 = (left / row_tiles) * kBN;
-  int first;
-  const int n = group_of(counts, offsets, e, rows_max, first);
-  if (n == 0) first = 0;
+    const int32_t* __restrict__ offsets, int E, int rows_max, int K, int N, char* __restrict__ dw) {
+  __shared__ __attribute__((aligned(1024))) char lds[kLdsBytes<BM, RA, RB, true, true>];
+  const int rows = (K + BM - 1) / BM, cols = (N + kBN - 1) / kBN;
+  const int64_t index = tile_index((int64_t)E * rows * cols);
+  if (index < 0) return;
+  const int e = (int)(index / (rows * cols));
+  int m, n, first;
+  tile_place((int)(index - (int64_t)e * (rows * cols)), rows, cols, m, n);
   Tile t;
-  t.a = a + (size_t)first * K + k0;
-  t.b = dc + (size_t)first * N + n0;
-  t.c = dw + ((size_t)e * K * N + (size_t)k0 * N + n0) * (OUT_BF16 ? 2 : 4);
+  t.depth = group_of(counts, offsets, e, rows_max, first);
+  if (t.depth == 0) first = 0;
+  t.a = a + (size_t)first * K + m * BM;
+  t.b = dc + (size_t)first * N + n * kBN;
+  t.c = dw + ((size_t)e * K * N + (size_t)m * BM * N + n * kBN) * (OUT_BF16 ? 2 : 4);
   t.lda = K;
   t.ldb = N;
   t.ldc = N;
-  t.m = K - k0;
-  t.n = N - n0;
-  t.depth = n;
-  tile_product<BM, WAVES_M, WAVES_N, NS, true, true, OUT_BF16>(t, lds);
+  t.m = K - m * BM;
+  t.n = N - n * kBN;
+  tile_product<BM, WAVES_M, WAVES_N, RA, RB, true, true, OUT_BF16>(t, lds);
 }
 
 }  // namespace
@@ -365,18 +466,16 @@ hipError_t launch_matmul_grouped(const void* a, const void* w, const int32_t* co
                                  int rows_max, int K, int N, bool transposed, void* c, bool out_bf16, hipStream_t s) {
   const auto* pa = static_cast<const uint16_t*>(a);
   const auto* pw = static_cast<const uint16_t*>(w);
-  const int64_t col_tiles = ((transposed ? K : N) + kBN - 1) / kBN;
+  const int64_t cols = ((transposed ? K : N) + kBN - 1) / kBN;
   const auto run = [&](auto kernel, int bm, int threads) {
-    const int64_t blocks = ((rows_max / bm + std::min(E, rows_max)) * col_tiles + 7) / 8 * 8;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, s, pa, pw, counts, offsets, E, rows_max, K, N,
+    const int64_t tiles = (rows_max / bm + std::min(E, rows_max)) * cols;
+    hipLaunchKernelGGL(kernel, dim3(tile_blocks(tiles)), dim3(threads), 0, s, pa, pw, counts, offsets, E, rows_max, K, N,
                        static_cast<char*>(c));
   };
   const auto sized = [&](auto t, auto o) {
     constexpr bool T = decltype(t)::value, O = decltype(o)::value;
-    const int64_t mean = rows_max / E;
-    if (mean <= 64) run(matmul_rows_kernel<64, 1, 4, 4, T, O>, 64, 256);
-    else if (mean <= 512) run(matmul_rows_kernel<128, 2, 4, 6, T, O>, 128, 512);
-    else run(matmul_rows_kernel<256, 2, 4, 4, T, O>, 256, 512);
+    if (rows_max / E <= 8) run(matmul_rows_kernel<64, 1, 4, 2, T ? 2 : 4, 2, T, O>, 64, 256);
+    else run(matmul_rows_kernel<256, 2, 4, 2, T ? 2 : 4, 1, T, O>, 256, 512);
   };
   if (transposed) out_bf16 ? sized(std::true_type{}, std::true_type{}) : sized(std::true_type{}, std::false_type{});
   else out_bf16 ? sized(std::false_type{}, std::true_type{}) : sized(std::false_type{}, std::false_type{});
@@ -388,12 +487,12 @@ hipError_t launch_matmul_grouped_dw(const void* a, const void* dc, const int32_t
   const auto* pa = static_cast<const uint16_t*>(a);
   const auto* pd = static_cast<const uint16_t*>(dc);
   const auto run = [&](auto kernel, int bm, int threads) {
-    const int64_t blocks = (int64_t)((N + kBN - 1) / kBN) * ((K + bm - 1) / bm) * E;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, s, pa, pd, counts, offsets, rows_max, K, N,
+    const int64_t tiles = (int64_t)((N + kBN - 1) / kBN) * ((K + bm - 1) / bm) * E;
+    hipLaunchKernelGGL(kernel, dim3(tile_blocks(tiles)), dim3(threads), 0, s, pa, pd, counts, offsets, E, rows_max, K, N,
                        static_cast<char*>(dw));
   };
-  if (rows_max / E <= 64) out_bf16 ? run(matmul_dw_kernel<64, 1, 4, 4, true>, 64, 256) : run(matmul_dw_kernel<64, 1, 4, 4, false>, 64, 256);
-  else out_bf16 ? run(matmul_dw_kernel<256, 2, 4, 4, true>, 256, 512) : run(matmul_dw_kernel<256, 2, 4, 4, false>, 256, 512);
+  out_bf16 ? run(matmul_dw_kernel<256, 2, 4, 4, 4, 1, true>, 256, 512)
+           : run(matmul_dw_kernel<256, 2, 4, 4, 4, 1, false>, 256, 512);
   return hipGetLastError();
 }
 
