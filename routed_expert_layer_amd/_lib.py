@@ -207,12 +207,19 @@ def _dptr(t):
 _raw_stream = None
 
 
-def _current_stream():
+def _bind_raw_stream():
+    """Sets _raw_stream, the query for a device's current stream."""
     global _raw_stream
     import torch
     if _raw_stream is None:
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _current_stream():
+    import torch
+    if _raw_stream is None:
+        _bind_raw_stream()
     return _raw_stream(torch.cuda.current_device())
 
 
@@ -516,84 +523,128 @@ def moe_combine(y_perm, perm_pos, topk_w, out, stream=None):
 
 
 # ---------------------------------------------------------------------------
+# The checks of the calls below: an attribute of a tensor takes 0.05 us and a Python call 0.1, so that a launch of 3 us
+# would wait for checks written with a call for each (6.2 us a moe_collect call so, 4.6 with these).
+_torch = _bf16 = _f32 = _i32 = _i8 = _raw_device = None
+
+
+def _bind_torch():
+    global _torch, _bf16, _f32, _i32, _i8, _raw_device
+    import torch
+    _bf16, _f32, _i32, _i8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
+    _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _bind_raw_stream()
+    _torch = torch
+
+
+def _here(t, name):
+    """The index of the GPU that tensor t is on; refused unless it is the current one."""
+    if _torch is None:
+        _bind_torch()
+    dev = t.get_device()
+    if dev < 0 or dev != _raw_device():
+        return _device(t, name)  # says what is wrong
+    return dev
+
+
+def _at(t, dev, dtype, shape, name):
+    """Address of a contiguous tensor of that torch dtype and shape on GPU `dev`."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: a {str(dtype)[6:]} tensor is needed, not {t.dtype}")
+    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        return _gpu(t, dev, None, name, shape)
+    return t.data_ptr()
+
+
+def _rows_dtype(t, name):
+    """(torch dtype, MOE_DT code) of a tensor of rows."""
+    d = t.dtype
+    if d is _bf16:
+        return d, MOE_DT_BF16
+    if d is _f32:
+        return d, MOE_DT_F32
+    raise ValueError(f"{name}: a float32 or bfloat16 tensor is needed, not {d}")
+
+
+def _two(t, name):
+    s = t.shape
+    if len(s) != 2:
+        raise ValueError(f"{name}: two dimensions are needed, not shape {tuple(s)}")
+    return s
+
+
+def _on_stream(s, dev):
+    return _raw_stream(dev) if s is None else s if isinstance(s, int) else s.cuda_stream
+
+
 def moe_group_workspace_size(T, k, E):
     return _lib.moe_group_workspace_size(T, k, E)
-
-
-def _act(t, name):
-    """MOE_DT code of a tensor of rows."""
-    if t.dtype is _torch_dtype("bfloat16"):
-        return MOE_DT_BF16
-    if t.dtype is _torch_dtype("float32"):
-        return MOE_DT_F32
-    raise ValueError(f"{name}: a float32 or bfloat16 tensor is needed, not {t.dtype}")
-
-
-def _rows_of(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: two dimensions are needed, not shape {tuple(t.shape)}")
-    return t.shape
 
 
 def moe_group(topk_idx, E, counts, offsets, perm_src, perm_pos, workspace=None, stream=None):
     """The grouping of given choices topk_idx (GPU int32 [T, k]; entries outside [0, E) are dropped): counts [E],
     offsets [E+1], perm_src [T*k] and perm_pos [T, k] (GPU int32) are written. workspace: GPU bytes, or None where
     moe_group_workspace_size(T, k, E) is 0."""
-    T, k = _rows_of(topk_idx, "topk_idx")
-    dev = _device(topk_idx, "topk_idx")
+    tk = T, k = _two(topk_idx, "topk_idx")
+    dev = _here(topk_idx, "topk_idx")
     if perm_src.numel() < T * k:
         raise ValueError(f"perm_src: at least {T * k} entries are needed")
     ws, n = (None, 0) if workspace is None else (_gpu(workspace, dev, None, "workspace"), _nbytes(workspace))
-    _check(_lib.moe_group(_gpu(topk_idx, dev, "int32", "topk_idx"), T, k, E,
-                          _gpu(counts, dev, "int32", "counts", (E,)), _gpu(offsets, dev, "int32", "offsets", (E + 1,)),
-                          _gpu(perm_src, dev, "int32", "perm_src"),
-                          _gpu(perm_pos, dev, "int32", "perm_pos", (T, k)), ws, n, _stream(stream)), "moe_group")
+    rc = _lib.moe_group(_at(topk_idx, dev, _i32, tk, "topk_idx"), T, k, E, _at(counts, dev, _i32, (E,), "counts"),
+                        _at(offsets, dev, _i32, (E + 1,), "offsets"),
+                        _at(perm_src, dev, _i32, perm_src.shape, "perm_src"), _at(perm_pos, dev, _i32, tk, "perm_pos"),
+                        ws, n, _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_group")
 
 
 def moe_dispatch(x, perm_pos, x_perm, stream=None):
     """x_perm[perm_pos[t, j]] = x[t]: x [T, H] and x_perm [rows_max, H] of one type (float32 or bfloat16)."""
-    T, H = _rows_of(x, "x")
-    rows, k = _rows_of(x_perm, "x_perm")[0], _rows_of(perm_pos, "perm_pos")[1]
-    dev = _device(x, "x")
-    dt = _act(x, "x")
-    _check(_lib.moe_dispatch(_gpu(x, dev, None, "x"), dt, _gpu(perm_pos, dev, "int32", "perm_pos", (T, k)), T, k, H,
-                             rows, _gpu(x_perm, dev, _DT_NAMES[dt], "x_perm", (rows, H)), _stream(stream)),
-           "moe_dispatch")
+    T, H = sx = _two(x, "x")
+    rows, k = _two(x_perm, "x_perm")[0], _two(perm_pos, "perm_pos")[1]
+    dev = _here(x, "x")
+    d, code = _rows_dtype(x, "x")
+    rc = _lib.moe_dispatch(_at(x, dev, d, sx, "x"), code, _at(perm_pos, dev, _i32, (T, k), "perm_pos"), T, k, H, rows,
+                           _at(x_perm, dev, d, (rows, H), "x_perm"), _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_dispatch")
 
 
 def moe_collect(rows, perm_pos, topk_w, out, stream=None):
     """out[t] = sum_j topk_w[t, j] rows[perm_pos[t, j]] (topk_w None: weights of 1); rows [rows_max, H] and out [T, H]
     float32 or bfloat16, each."""
-    n, H = _rows_of(rows, "rows")
-    T, k = _rows_of(perm_pos, "perm_pos")
-    dev = _device(rows, "rows")
-    w = None if topk_w is None else _gpu(topk_w, dev, "float32", "topk_w", (T, k))
-    _check(_lib.moe_collect(_gpu(rows, dev, None, "rows"), _act(rows, "rows"),
-                            _gpu(perm_pos, dev, "int32", "perm_pos"), w, T, k, H, n,
-                            _gpu(out, dev, None, "out", (T, H)), _act(out, "out"), _stream(stream)), "moe_collect")
+    n, H = sr = _two(rows, "rows")
+    T, k = tk = _two(perm_pos, "perm_pos")
+    dev = _here(rows, "rows")
+    d, code = _rows_dtype(rows, "rows")
+    od, ocode = _rows_dtype(out, "out")
+    rc = _lib.moe_collect(_at(rows, dev, d, sr, "rows"), code, _at(perm_pos, dev, _i32, tk, "perm_pos"),
+                          None if topk_w is None else _at(topk_w, dev, _f32, tk, "topk_w"), T, k, H, n,
+                          _at(out, dev, od, (T, H), "out"), ocode, _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_collect")
 
 
 def moe_collect_backward(dout, rows, perm_pos, topk_w, drows, dw, stream=None):
     """The gradient of moe_collect: drows[perm_pos[t, j]] = topk_w[t, j] dout[t] (drows None: not wanted) and
     dw[t, j] = <dout[t], rows[perm_pos[t, j]]> (dw None: not wanted, rows may then be None)."""
-    T, H = _rows_of(dout, "dout")
-    k = _rows_of(perm_pos, "perm_pos")[1]
-    dev = _device(dout, "dout")
+    T, H = so = _two(dout, "dout")
+    tk = (T, _two(perm_pos, "perm_pos")[1])
+    dev = _here(dout, "dout")
     like = rows if rows is not None else drows
     if like is None or (dw is not None and rows is None):
         raise ValueError("moe_collect_backward: dw needs rows, and drows or dw is needed")
-    n = _rows_of(like, "rows")[0]
-    dt = _act(like, "rows")
-    w = None if topk_w is None else _gpu(topk_w, dev, "float32", "topk_w", (T, k))
-    r = None if rows is None else _gpu(rows, dev, None, "rows", (n, H))
-    dr = None if drows is None else _gpu(drows, dev, _DT_NAMES[dt], "drows", (n, H))
-    d = None if dw is None else _gpu(dw, dev, "float32", "dw", (T, k))
-    _check(_lib.moe_collect_backward(_gpu(dout, dev, None, "dout"), _act(dout, "dout"), r, dt,
-                                     _gpu(perm_pos, dev, "int32", "perm_pos", (T, k)), w, T, k, H, n, dr, d,
-                                     _stream(stream)), "moe_collect_backward")
-
-
-_DT_NAMES = {MOE_DT_F32: "float32", MOE_DT_BF16: "bfloat16"}
+    sr = (_two(like, "rows")[0], H)
+    d, code = _rows_dtype(like, "rows")
+    od, ocode = _rows_dtype(dout, "dout")
+    rc = _lib.moe_collect_backward(_at(dout, dev, od, so, "dout"), ocode,
+                                   None if rows is None else _at(rows, dev, d, sr, "rows"), code,
+                                   _at(perm_pos, dev, _i32, tk, "perm_pos"),
+                                   None if topk_w is None else _at(topk_w, dev, _f32, tk, "topk_w"), T, tk[1], H, sr[0],
+                                   None if drows is None else _at(drows, dev, d, sr, "drows"),
+                                   None if dw is None else _at(dw, dev, _f32, tk, "dw"), _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_collect_backward")
 
 
 def _n_rows(n_rows, dev):
@@ -608,35 +659,33 @@ def moe_swiglu_save(gu, h, codes, scales, n_rows=None, stream=None):
     """h = silu(gu[:, :I]) gu[:, I:], and gu kept in 8 bits: codes int8 [rows, 2I], scales float32
     [rows, 2 ceil(I / 128)]. gu [rows, 2I] and h [rows, I] of one type. n_rows: GPU int32 of one entry (offsets[E:]),
     the rows to work on."""
-    rows, two_i = _rows_of(gu, "gu")
+    rows, two_i = sg = _two(gu, "gu")
     if two_i % 2:
         raise ValueError(f"gu: gate and up columns are needed, not {two_i}")
     I = two_i // 2
-    dev = _device(gu, "gu")
-    dt = _act(gu, "gu")
-    _check(_lib.moe_swiglu_save(_gpu(gu, dev, None, "gu"), dt, rows, _n_rows(n_rows, dev), I,
-                                _gpu(h, dev, _DT_NAMES[dt], "h", (rows, I)),
-                                _gpu(codes, dev, "int8", "codes", (rows, two_i)),
-                                _gpu(scales, dev, "float32", "scales", (rows, 2 * ((I + 127) // 128))),
-                                _stream(stream)), "moe_swiglu_save")
+    dev = _here(gu, "gu")
+    d, code = _rows_dtype(gu, "gu")
+    rc = _lib.moe_swiglu_save(_at(gu, dev, d, sg, "gu"), code, rows, _n_rows(n_rows, dev), I,
+                              _at(h, dev, d, (rows, I), "h"), _at(codes, dev, _i8, sg, "codes"),
+                              _at(scales, dev, _f32, (rows, 2 * ((I + 127) // 128)), "scales"), _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_swiglu_save")
 
 
 def moe_swiglu_backward(codes, scales, dh, dgu, h=None, n_rows=None, stream=None):
     """The gradient of moe_swiglu_save's h to gu from what was kept, dgu [rows, 2I] for dh [rows, I], and h [rows, I]
     again from it (None: not wanted); dh, dgu and h of one type."""
-    rows, I = _rows_of(dh, "dh")
-    dev = _device(dh, "dh")
-    dt = _act(dh, "dh")
-    again = None if h is None else _gpu(h, dev, _DT_NAMES[dt], "h", (rows, I))
-    _check(_lib.moe_swiglu_backward(_gpu(codes, dev, "int8", "codes", (rows, 2 * I)),
-                                    _gpu(scales, dev, "float32", "scales", (rows, 2 * ((I + 127) // 128))),
-                                    _gpu(dh, dev, None, "dh"), dt, rows, _n_rows(n_rows, dev), I,
-                                    _gpu(dgu, dev, _DT_NAMES[dt], "dgu", (rows, 2 * I)), again, _stream(stream)),
-           "moe_swiglu_backward")
-
-
-def _grouped_args(dev, counts, offsets, E):
-    return _gpu(counts, dev, "int32", "counts", (E,)), _gpu(offsets, dev, "int32", "offsets", (E + 1,))
+    rows, I = sh = _two(dh, "dh")
+    dev = _here(dh, "dh")
+    d, code = _rows_dtype(dh, "dh")
+    sg = (rows, 2 * I)
+    rc = _lib.moe_swiglu_backward(_at(codes, dev, _i8, sg, "codes"),
+                                  _at(scales, dev, _f32, (rows, 2 * ((I + 127) // 128)), "scales"),
+                                  _at(dh, dev, d, sh, "dh"), code, rows, _n_rows(n_rows, dev), I,
+                                  _at(dgu, dev, d, sg, "dgu"), None if h is None else _at(h, dev, d, sh, "h"),
+                                  _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_swiglu_backward")
 
 
 def moe_matmul_grouped(a, w, counts, offsets, c, transposed=False, stream=None):
@@ -644,14 +693,16 @@ def moe_matmul_grouped(a, w, counts, offsets, c, transposed=False, stream=None):
     [E, K, N], c float32 or bfloat16 [rows_max, N] (transposed: K)."""
     if w.dim() != 3:
         raise ValueError(f"w: three dimensions are needed, not shape {tuple(w.shape)}")
-    E, K, N = w.shape
-    rows = _rows_of(a, "a")[0]
-    dev = _device(w, "w")
-    cn, of = _grouped_args(dev, counts, offsets, E)
-    _check(_lib.moe_matmul_grouped(_gpu(a, dev, "bfloat16", "a", (rows, N if transposed else K)),
-                                   _gpu(w, dev, "bfloat16", "w"), cn, of, E, rows, K, N, int(bool(transposed)),
-                                   _gpu(c, dev, None, "c", (rows, K if transposed else N)), _act(c, "c"),
-                                   _stream(stream)), "moe_matmul_grouped")
+    E, K, N = sw = w.shape
+    rows = _two(a, "a")[0]
+    dev = _here(w, "w")
+    cd, code = _rows_dtype(c, "c")
+    rc = _lib.moe_matmul_grouped(_at(a, dev, _bf16, (rows, N if transposed else K), "a"), _at(w, dev, _bf16, sw, "w"),
+                                 _at(counts, dev, _i32, (E,), "counts"), _at(offsets, dev, _i32, (E + 1,), "offsets"), E,
+                                 rows, K, N, 1 if transposed else 0,
+                                 _at(c, dev, cd, (rows, K if transposed else N), "c"), code, _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_matmul_grouped")
 
 
 def moe_matmul_grouped_dw(a, dc, counts, offsets, dw, stream=None):
@@ -659,14 +710,15 @@ def moe_matmul_grouped_dw(a, dc, counts, offsets, dw, stream=None):
     float32 or bfloat16."""
     if dw.dim() != 3:
         raise ValueError(f"dw: three dimensions are needed, not shape {tuple(dw.shape)}")
-    E, K, N = dw.shape
-    rows = _rows_of(a, "a")[0]
-    dev = _device(dw, "dw")
-    cn, of = _grouped_args(dev, counts, offsets, E)
-    _check(_lib.moe_matmul_grouped_dw(_gpu(a, dev, "bfloat16", "a", (rows, K)),
-                                      _gpu(dc, dev, "bfloat16", "dc", (rows, N)), cn, of, E, rows, K, N,
-                                      _gpu(dw, dev, None, "dw"), _act(dw, "dw"), _stream(stream)),
-           "moe_matmul_grouped_dw")
+    E, K, N = sw = dw.shape
+    rows = _two(a, "a")[0]
+    dev = _here(dw, "dw")
+    wd, code = _rows_dtype(dw, "dw")
+    rc = _lib.moe_matmul_grouped_dw(_at(a, dev, _bf16, (rows, K), "a"), _at(dc, dev, _bf16, (rows, N), "dc"),
+                                    _at(counts, dev, _i32, (E,), "counts"), _at(offsets, dev, _i32, (E + 1,), "offsets"),
+                                    E, rows, K, N, _at(dw, dev, wd, sw, "dw"), code, _on_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_matmul_grouped_dw")
 
 
 # ---------------------------------------------------------------------------

@@ -22,10 +22,14 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupWaves = kGroupThreads / 64;
-constexpr int kGroupSub = 4;                                  // 64-entry chunks a wave takes per round
-constexpr int kGroupRound = kGroupWaves * kGroupSub * 64;     // entries a block places per round: 4096
-constexpr int kGroupBlocks = 64;                              // most blocks of the two-launch form
+constexpr int kGroupBlocks = 64;     // most blocks of the two-launch form
 constexpr int kGroupExperts = 1024;
+// Forms: one block that counts what it places; several blocks that each count all the entries; or a launch that counts
+// (group_count) and one that places. A block places 1024 entries a round, or 4096 where rounds are long anyway.
+enum { kGroupOne, kGroupAll, kGroupTwo };
+constexpr int kGroupOneMost = kGroupThreads;   // entries up to which each form is taken
+constexpr int kGroupAllMost = 32768;
+constexpr int group_round(int sub) { return kGroupThreads * sub; }
 
 // Exclusive prefix sum of v over the block's threads (1024) and its total.
 __device__ __forceinline__ int block_prefix(int v, int* sums, int& total) {
@@ -49,13 +53,14 @@ __device__ __forceinline__ int block_prefix(int v, int* sums, int& total) {
 }
 
 // Choices per expert of each block's segment of the entries, hist[block][E].
-__global__ __launch_bounds__(kGroupThreads) void group_count(const int32_t* __restrict__ idx, int64_t n, int64_t seg,
-                                                             int E, int32_t* __restrict__ hist) {
+__global__ __launch_bounds__(kGroupThreads) void group_count(const int32_t* __restrict__ idx, int n, int seg, int E,
+                                                             int32_t* __restrict__ hist) {
   __shared__ int h[kGroupExperts];
   for (int e = threadIdx.x; e < E; e += kGroupThreads) h[e] = 0;
   __syncthreads();
-  const int64_t end = min(n, (int64_t)(blockIdx.x + 1) * seg);
-  for (int64_t i = (int64_t)blockIdx.x * seg + threadIdx.x; i < end; i += kGroupThreads) {
+  const int first = (int)min((int64_t)n, (int64_t)blockIdx.x * seg), end = (int)min((int64_t)n, (int64_t)first + seg);
+#pragma unroll 4
+  for (int i = first + (int)threadIdx.x; i < end; i += kGroupThreads) {
     const int e = idx[i];
     if ((unsigned)e < (unsigned)E) atomicAdd(&h[e], 1);  // integers: the order does not matter
   }
@@ -64,13 +69,13 @@ __global__ __launch_bounds__(kGroupThreads) void group_count(const int32_t* __re
 }
 
 // Places of a segment's entries. The rank of an entry among its expert's is
-// the number in earlier blocks (hist), earlier rounds (base), earlier waves and
-// chunks of the round (cnt) and lower lanes of its chunk: the lanes with the
-// same expert are found by one ballot per bit of the expert's number. With ONE
-// the only block counts for itself (n <= kGroupRound).
-template <bool ONE>
-__global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __restrict__ idx, int64_t n, int64_t seg,
-                                                             int k, int E, int bits, const int32_t* __restrict__ hist,
+// the number in earlier segments and rounds (base), earlier waves and chunks of
+// the round (cnt) and lower lanes of its chunk of 64: the lanes with the same
+// expert are found by one ballot per bit of the expert's number. SUB chunks a
+// wave per round.
+template <int FORM, int SUB>
+__global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __restrict__ idx, int n, int seg, int k,
+                                                             int E, int bits, const int32_t* __restrict__ hist,
                                                              int32_t* __restrict__ counts,
                                                              int32_t* __restrict__ offsets,
                                                              int32_t* __restrict__ perm_src,
@@ -79,7 +84,8 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __re
   __shared__ int sums[kGroupWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t below = (1ull << lane) - 1ull;
-  const int64_t first = ONE ? 0 : (int64_t)blockIdx.x * seg, end = ONE ? n : min(n, first + seg);
+  const int first = FORM == kGroupOne ? 0 : (int)min((int64_t)n, (int64_t)blockIdx.x * seg);
+  const int end = FORM == kGroupOne ? n : (int)min((int64_t)n, (int64_t)first + seg);
   int base = 0;  // thread e: the place of the next entry of expert e
   auto publish = [&](int count) {
     int total;
@@ -93,32 +99,48 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __re
     }
     return at;
   };
-  if constexpr (!ONE) {
+  if constexpr (FORM != kGroupOne) {
     int before = 0, all = 0;
-    if (tid < E)
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int c = hist[(size_t)b * E + tid];
-        before += b < (int)blockIdx.x ? c : 0;
-        all += c;
+    if constexpr (FORM == kGroupAll) {
+      if (tid < E) cnt[0][tid] = cnt[1][tid] = 0;
+      __syncthreads();
+#pragma unroll 8
+      for (int i = tid; i < n; i += kGroupThreads) {
+        const int e = idx[i];
+        if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[i < first ? 0 : 1][e], 1);  // integers: the order does not matter
       }
-    base = publish(all) + before;
+      __syncthreads();
+      if (tid < E) {
+        before = cnt[0][tid];
+        all = before + cnt[1][tid];
+      }
+    } else {
+      if (tid < E)
+#pragma unroll 8
+        for (int b = 0; b < (int)gridDim.x; ++b) {
+          const int c = hist[(size_t)b * E + tid];
+          before += b < (int)blockIdx.x ? c : 0;
+          all += c;
+        }
+    }
+    base = publish(all) + before;  // its barriers stand before the next use of cnt too
   }
-  for (int64_t r = first; ONE || r < end; r += kGroupRound) {
-    const int here = (int)min((int64_t)kGroupRound, end - r);
-    const int waves = (here + 64 * kGroupSub - 1) / (64 * kGroupSub);
+  for (int r = first; FORM == kGroupOne || r < end; r += group_round(SUB)) {
+    const int here = min(group_round(SUB), end - r);
+    const int waves = (here + 64 * SUB - 1) / (64 * SUB);
     for (int w = 0; w < waves; ++w)
       if (tid < E) cnt[w][tid] = 0;
-    __syncthreads();
-    int e[kGroupSub], rank[kGroupSub];
+    int e[SUB], rank[SUB];
 #pragma unroll
-    for (int c = 0; c < kGroupSub; ++c) {
-      const int i = (wave * kGroupSub + c) * 64 + lane;
+    for (int c = 0; c < SUB; ++c) {
+      const int i = (wave * SUB + c) * 64 + lane;
       const int v = i < here ? idx[r + i] : E;
       e[c] = (unsigned)v < (unsigned)E ? v : E;
     }
+    __syncthreads();
     if (wave < waves)
 #pragma unroll
-      for (int c = 0; c < kGroupSub; ++c) {
+      for (int c = 0; c < SUB; ++c) {
         uint64_t same = ~0ull;
         for (int b = 0; b < bits; ++b) {
           const bool on = (e[c] >> b) & 1;
@@ -133,8 +155,9 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __re
         __builtin_amdgcn_wave_barrier();  // the next chunk's reads follow this one's writes
       }
     __syncthreads();
-    int run = base, count = 0;
-    if constexpr (ONE) {
+    int run = base;
+    if constexpr (FORM == kGroupOne) {
+      int count = 0;
       if (tid < E)
         for (int w = 0; w < waves; ++w) count += cnt[w][tid];
       run = publish(count);
@@ -148,20 +171,21 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __re
     base = run;
     __syncthreads();
 #pragma unroll
-    for (int c = 0; c < kGroupSub; ++c) {
-      const int i = (wave * kGroupSub + c) * 64 + lane;
+    for (int c = 0; c < SUB; ++c) {
+      const int i = (wave * SUB + c) * 64 + lane;
       if (i >= here) continue;
       const bool kept = e[c] < E;
       const int p = kept ? cnt[wave][e[c]] + rank[c] : -1;
       perm_pos[r + i] = p;
-      if (kept) perm_src[p] = (int)((r + i) / k);
+      if (kept) perm_src[p] = (int)((unsigned)(r + i) / (unsigned)k);
     }
-    if constexpr (ONE) break;
+    if constexpr (FORM == kGroupOne) break;
     __syncthreads();
   }
 }
 
-int group_blocks(int64_t n) { return (int)std::min<int64_t>(kGroupBlocks, (n + kGroupRound - 1) / kGroupRound); }
+// Blocks and entries to a block of the two-launch form.
+int group_blocks(int n) { return std::min(kGroupBlocks, (n + group_round(4) - 1) / group_round(4)); }
 
 // ---------------------------------------------------------------------------
 // Rows. A block takes 256 >> ls tokens, 1 << ls threads each; a thread takes N
@@ -304,26 +328,31 @@ void with_flag(bool b, const F& f) {
 }  // namespace
 
 size_t group_workspace_bytes(int T, int k, int E) {
-  const int64_t n = (int64_t)T * k;
-  return n <= kGroupRound ? 0 : (size_t)group_blocks(n) * E * sizeof(int32_t);
+  const int n = T * k;
+  return n <= kGroupAllMost ? 0 : (size_t)group_blocks(n) * E * sizeof(int32_t);
 }
 
 hipError_t launch_group(const int32_t* idx, int T, int k, int E, int32_t* counts, int32_t* offsets, int32_t* perm_src,
                         int32_t* perm_pos, void* ws, hipStream_t s) {
-  const int64_t n = (int64_t)T * k;
+  const int n = T * k;
   int bits = 0;
   while ((1 << bits) < E + 1) ++bits;
-  if (n <= kGroupRound) {
-    hipLaunchKernelGGL(group_place<true>, dim3(1), dim3(kGroupThreads), 0, s, idx, n, (int64_t)kGroupRound, k, E, bits,
+  const dim3 threads(kGroupThreads);
+  if (n <= kGroupOneMost) {
+    hipLaunchKernelGGL((group_place<kGroupOne, 1>), dim3(1), threads, 0, s, idx, n, 0, k, E, bits, nullptr, counts,
+                       offsets, perm_src, perm_pos);
+  } else if (n <= kGroupAllMost) {
+    const int seg = group_round(1);
+    hipLaunchKernelGGL((group_place<kGroupAll, 1>), dim3((n + seg - 1) / seg), threads, 0, s, idx, n, seg, k, E, bits,
                        nullptr, counts, offsets, perm_src, perm_pos);
-    return hipGetLastError();
+  } else {
+    const int blocks = group_blocks(n), round = group_round(4);
+    const int seg = ((n + blocks - 1) / blocks + round - 1) / round * round;
+    int32_t* hist = static_cast<int32_t*>(ws);
+    hipLaunchKernelGGL(group_count, dim3(blocks), threads, 0, s, idx, n, seg, E, hist);
+    hipLaunchKernelGGL((group_place<kGroupTwo, 4>), dim3(blocks), threads, 0, s, idx, n, seg, k, E, bits, hist, counts,
+                       offsets, perm_src, perm_pos);
   }
-  const int blocks = group_blocks(n);
-  const int64_t seg = ((n + blocks - 1) / blocks + kGroupRound - 1) / kGroupRound * kGroupRound;
-  int32_t* hist = static_cast<int32_t*>(ws);
-  hipLaunchKernelGGL(group_count, dim3(blocks), dim3(kGroupThreads), 0, s, idx, n, seg, E, hist);
-  hipLaunchKernelGGL(group_place<false>, dim3(blocks), dim3(kGroupThreads), 0, s, idx, n, seg, k, E, bits, hist, counts,
-                     offsets, perm_src, perm_pos);
   return hipGetLastError();
 }
 
