@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const void* __restrict__ 
   v.load(x, (size_t)t * s.H + c);
   for (int j = 0; j < s.k; ++j) {
     const int p = pos[(size_t)t * s.k + j];
-    if ((unsigned)p < (unsigned)s.rows) v.store(out, (size_t)p * s.H + c);
+    if ((unsigned)p < (unsigned)s.rows) v.template store<true>(out, (size_t)p * s.H + c);
   }
 }
 
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256) void collect_backward_kernel(const void* __res
       if constexpr (DW) {
 #pragma unroll
         for (int j = 0; j < kRowsAtOnce; ++j)
-          if ((unsigned)p[j] < (unsigned)s.rows) v[j].load(rows, (size_t)p[j] * s.H + c);
+          if ((unsigned)p[j] < (unsigned)s.rows) v[j].template load<true>(rows, (size_t)p[j] * s.H + c);
       }
 #pragma unroll
       for (int j = 0; j < kRowsAtOnce; ++j)
@@ -282,7 +282,7 @@ __global__ __launch_bounds__(256) void collect_backward_kernel(const void* __res
             for (int i = 0; i < N; ++i) g[i] = wj[j] * d.get(i);
             RowVec<BF16, N> o;
             o.set(g);
-            o.store(drows, (size_t)p[j] * s.H + c);
+            o.template store<true>(drows, (size_t)p[j] * s.H + c);
           }
         }
     }

@@ -75,7 +75,7 @@ __device__ __forceinline__ void store8(void* p, size_t base, const KeptAt& a, co
   if constexpr (VEC) {
     RowVec<BF16, kKeptCols> v;
     v.set(f);
-    if (a.n > 0) v.store(p, base + a.c0);
+    if (a.n > 0) v.template store<true>(p, base + a.c0);
   } else {
 #pragma unroll
     for (int i = 0; i < kKeptCols; ++i) {
