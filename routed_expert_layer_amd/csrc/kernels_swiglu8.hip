@@ -18,14 +18,18 @@ namespace {
 constexpr int kKeptGroup = 128;  // columns that share a scale
 constexpr int kKeptLanes = 16, kKeptCols = 8;
 
-// 1 / (1 + e^-g) and 1 - it, neither by a difference: both keep their last bits.
+// 1 / (1 + e^-g) and 1 - it, neither by a difference: both keep their last bits (a NaN stays one). For bf16 results by
+// the hardware's exponential and reciprocal, a step of 2^-23 each and 1.5 |g| half steps from the exponent's argument
+// (below 2^-8 by far): 98304 rows of 2 x 2048 take 636 us for both passes so, 708 with expf and a
+// division.
+template <bool FAST>
 struct Sigmoid {
   float s, t;
   __device__ __forceinline__ explicit Sigmoid(float g) {
-    const float e = expf(-fabsf(g)), r = 1.f / (1.f + e);
+    const float e = FAST ? __expf(-fabsf(g)) : expf(-fabsf(g));
+    const float r = FAST ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
     s = g >= 0.f ? r : e * r;
     t = g >= 0.f ? e * r : r;
-    if (isnan(g)) s = t = g;
   }
 };
 
@@ -126,7 +130,7 @@ __global__ __launch_bounds__(256) void swiglu_save_kernel(const void* __restrict
   load8<BF16, VEC>(gu, r, a, g);
   load8<BF16, VEC>(gu, r + I, a, u);
 #pragma unroll
-  for (int i = 0; i < kKeptCols; ++i) f[i] = g[i] * Sigmoid(g[i]).s * u[i];
+  for (int i = 0; i < kKeptCols; ++i) f[i] = g[i] * Sigmoid<BF16>(g[i]).s * u[i];
   store8<BF16, VEC>(h, (size_t)a.row * I, a, f);
   float* sc = scales + (size_t)a.row * 2 * groups + a.group;
   keep8<BF16, VEC>(g, a, codes, r, sc);
@@ -164,7 +168,7 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __re
   load8<BF16, VEC>(dh, (size_t)a.row * I, a, d);
 #pragma unroll
   for (int i = 0; i < kKeptCols; ++i) {
-    const Sigmoid s(g[i]);
+    const Sigmoid<BF16> s(g[i]);
     const float gs = g[i] * s.s;
     dg[i] = d[i] * u[i] * fmaf(gs, s.t, s.s);
     du[i] = d[i] * gs;
