@@ -460,6 +460,21 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, OCC) void matmul_dw_kernel(
   tile_product<BM, WAVES_M, WAVES_N, RA, RB, true, true, OUT_BF16>(t, lds);
 }
 
+// Rows of a tile. 256 where that leaves work for most CUs (190 tiles, counted as half an empty tile for each expert), less
+// where it does not: 1500 tokens x 2 of 8 experts of 2048 x 2048 take 50 us in 256s, 35 in 128s and 40 in 64s, 333 tokens
+// 42, 29 and 22, 3000 tokens 52, 67 and 66. Groups of few rows leave most of a large tile empty and read the weights
+// alone: up to 8 rows an expert 64s read them as fast or faster (48 tokens x 8 of 128 experts of 2048 x 1536 116 us, 125 in
+// 256s; at 12 rows 144 and 141). W^T comes in 128-byte pieces of 256 rows, which more and smaller blocks fetch better: up
+// to 32 rows 64s (64 tokens x 6 of 64 experts of 2048 x 4096 174 us, 221 in 128s, 232 in 256s), up to 256 rows 128s (187
+// rows 289 us, 354 in 64s, 336 in 256s; at 375 rows 475 and 464).
+int tile_rows(bool transposed, int rows_max, int E, int64_t cols) {
+  const int mean = rows_max / E;
+  const auto enough = [&](int bm) { return cols * std::max(rows_max / bm + E / 2, std::min(E, rows_max)) >= 190; };
+  if (mean <= (transposed ? 32 : 8)) return 64;
+  if (enough(256) && !(transposed && mean <= 256)) return 256;
+  return enough(128) ? 128 : 64;
+}
+
 }  // namespace
 
 hipError_t launch_matmul_grouped(const void* a, const void* w, const int32_t* counts, const int32_t* offsets, int E,
@@ -474,8 +489,12 @@ hipError_t launch_matmul_grouped(const void* a, const void* w, const int32_t* co
   };
   const auto sized = [&](auto t, auto o) {
     constexpr bool T = decltype(t)::value, O = decltype(o)::value;
-    if (rows_max / E <= 8) run(matmul_rows_kernel<64, 1, 4, 2, T ? 2 : 4, 2, T, O>, 64, 256);
-    else run(matmul_rows_kernel<256, 2, 4, 2, T ? 2 : 4, 1, T, O>, 256, 512);
+    // LDS: 80 KiB, two blocks to a CU, for 64 rows; 144 for 128; 128 and, with W^T, 160 for 256
+    switch (tile_rows(T, rows_max, E, cols)) {
+      case 64: run(matmul_rows_kernel<64, 1, 4, 2, T ? 2 : 4, 2, T, O>, 64, 256); break;
+      case 128: run(matmul_rows_kernel<128, 2, 4, 3, T ? 3 : 6, 1, T, O>, 128, 512); break;
+      default: run(matmul_rows_kernel<256, 2, 4, 2, T ? 3 : 4, 1, T, O>, 256, 512);
+    }
   };
   if (transposed) out_bf16 ? sized(std::true_type{}, std::true_type{}) : sized(std::true_type{}, std::false_type{});
   else out_bf16 ? sized(std::false_type{}, std::true_type{}) : sized(std::false_type{}, std::false_type{});
@@ -491,8 +510,16 @@ hipError_t launch_matmul_grouped_dw(const void* a, const void* dc, const int32_t
     hipLaunchKernelGGL(kernel, dim3(tile_blocks(tiles)), dim3(threads), 0, s, pa, pd, counts, offsets, E, rows_max, K, N,
                        static_cast<char*>(dw));
   };
-  out_bf16 ? run(matmul_dw_kernel<256, 2, 4, 4, 4, 1, true>, 256, 512)
-           : run(matmul_dw_kernel<256, 2, 4, 4, 4, 1, false>, 256, 512);
+  // 256 rows of dW to a tile, unless the last round of 256 blocks is mostly empty: every tile is as much work as its
+  // expert has rows, and 300 tiles take two rounds (333 tokens x 5 of 20 experts of 1280 x 648 19.0 us, 15.8 in 64s; 128
+  // tiles of 32 experts of 512 x 512 10.7 and 8.5; 256 tiles of 16 experts of 1024 x 1024 11.4 and 12.6).
+  const int64_t tiles = (int64_t)((N + kBN - 1) / kBN) * ((K + 255) / 256) * E;
+  if (10 * tiles >= 7 * ((tiles + 255) / 256 * 256))
+    out_bf16 ? run(matmul_dw_kernel<256, 2, 4, 4, 4, 1, true>, 256, 512)
+             : run(matmul_dw_kernel<256, 2, 4, 4, 4, 1, false>, 256, 512);
+  else
+    out_bf16 ? run(matmul_dw_kernel<64, 1, 4, 4, 4, 2, true>, 64, 256)
+             : run(matmul_dw_kernel<64, 1, 4, 4, 4, 2, false>, 64, 256);
   return hipGetLastError();
 }
 
