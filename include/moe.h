@@ -485,9 +485,9 @@ int moe_combine(const float* y_perm, const int32_t* perm_pos, const float* topk_
  * In all of them an entry of perm_pos outside [0, rows_max) has no row: its
  * weight is not read into a sum and nothing is written for it. Entries must
  * name different rows where rows are written.
- * Limits: 1 <= k <= 16, 1 <= E <= 1024, T*k <= 2^30, 1 <= H <= 2^20; buffers
- * aligned to their elements (rows go in 16-byte pieces where H and the
- * addresses allow it) and not overlapping.
+ * Limits: 1 <= k <= 16, 1 <= E <= 1024, T*k <= 2^30, and of the calls on rows
+ * T < 2^24, 1 <= H <= 2^20; buffers aligned to their elements and not
+ * overlapping.
  * Errors: MOE_EINVAL, MOE_EHIP.
  * ------------------------------------------------------------------------ */
 size_t moe_group_workspace_size(int T, int k, int E);
@@ -521,7 +521,7 @@ int moe_collect_backward(const void* dout, int out_dtype, const void* rows, int 
  * n_rows: device int32, or NULL. With it only the first min(rows, *n_rows)
  * rows are worked on (offsets + E of a grouping that dropped entries); those
  * behind them are neither read nor written.
- * Limits: rows <= 2^30, 1 <= I <= 2^20, rows * ceil(I/128) <= 2^34; buffers
+ * Limits: 1 <= I <= 2^20, rows * ceil(I/128) <= 2^27; buffers
  * aligned to their elements and not overlapping.
  * Errors: MOE_EINVAL, MOE_EHIP.
  * ------------------------------------------------------------------------ */

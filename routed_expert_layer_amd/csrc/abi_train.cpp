@@ -22,7 +22,8 @@ size_t elem(int dtype) { return dtype == MOE_DT_BF16 ? 2 : 4; }
 constexpr int kMaxLen = 1 << 20;  // longest row
 
 int check_rows(const char* who, int T, int k, int H, int rows_max, const int32_t* perm_pos) {
-  if (T < 0 || k < 1 || k > 16 || H < 1 || H > kMaxLen || rows_max < 0 || (long long)T * k > (1ll << 30))
+  // a block to a token at most: 2^24 of 256 threads is the longest launch
+  if (T < 0 || T >= (1 << 24) || k < 1 || k > 16 || H < 1 || H > kMaxLen || rows_max < 0)
     return fail(MOE_EINVAL, "%s: unsupported sizes T=%d k=%d H=%d rows_max=%d", who, T, k, H, rows_max);
   if (T > 0 && !perm_pos) return fail(MOE_EINVAL, "%s: null pointer argument", who);
   if (off(perm_pos, 4)) return fail(MOE_EINVAL, "%s: a buffer is not aligned to its elements", who);
@@ -113,7 +114,7 @@ int moe_collect_backward(const void* dout, int out_dtype, const void* rows, int 
 int moe_swiglu_save(const void* gu, int dtype, int rows, const int32_t* n_rows, int I, void* h, int8_t* codes,
                     float* scales, void* stream) {
   if (!is_act(dtype)) return fail(MOE_EINVAL, "moe_swiglu_save: bad dtype %d", dtype);
-  if (rows < 0 || rows > (1 << 30) || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 34))
+  if (rows < 0 || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 27))
     return fail(MOE_EINVAL, "moe_swiglu_save: unsupported sizes rows=%d I=%d", rows, I);
   if (rows == 0) return MOE_OK;
   if (!gu || !h || !codes || !scales) return fail(MOE_EINVAL, "moe_swiglu_save: null pointer argument");
@@ -126,7 +127,7 @@ int moe_swiglu_save(const void* gu, int dtype, int rows, const int32_t* n_rows, 
 int moe_swiglu_backward(const int8_t* codes, const float* scales, const void* dh, int dtype, int rows,
                         const int32_t* n_rows, int I, void* dgu, void* h, void* stream) {
   if (!is_act(dtype)) return fail(MOE_EINVAL, "moe_swiglu_backward: bad dtype %d", dtype);
-  if (rows < 0 || rows > (1 << 30) || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 34))
+  if (rows < 0 || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 27))
     return fail(MOE_EINVAL, "moe_swiglu_backward: unsupported sizes rows=%d I=%d", rows, I);
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !dh || !dgu) return fail(MOE_EINVAL, "moe_swiglu_backward: null pointer argument");

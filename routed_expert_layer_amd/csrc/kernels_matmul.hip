@@ -265,6 +265,7 @@ __device__ __forceinline__ void tile_product(const Tile& t, char* lds) {
     };
     // This wave's loads for part p + 1 have landed and its reads of part p are done; behind the barrier every wave's.
     auto meet = [&](auto parity) {
+      asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(vmcnt_only(kAhead[decltype(parity)::value]));
       __builtin_amdgcn_s_waitcnt(lgkmcnt_only(0));
       __builtin_amdgcn_s_barrier();

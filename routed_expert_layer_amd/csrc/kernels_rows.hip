@@ -9,6 +9,7 @@
 // All of them move bytes: a row is read once, in 16-byte loads, and written
 // once; the sums stay in registers.
 #include <algorithm>
+#include <type_traits>
 
 #include "dev_common.hpp"
 #include "moe_kernels.hpp"
@@ -188,33 +189,35 @@ __global__ __launch_bounds__(kGroupThreads) void group_place(const int32_t* __re
 int group_blocks(int n) { return std::min(kGroupBlocks, (n + group_round(4) - 1) / group_round(4)); }
 
 // ---------------------------------------------------------------------------
-// Rows. A block takes 256 >> ls tokens, 1 << ls threads each; a thread takes N
-// elements of its token's row.
+// Rows. A block takes 256 >> ls tokens, 1 << ls threads each; a thread takes
+// kVecElems elements of its token's row.
 // ---------------------------------------------------------------------------
 struct RowShape {
   int T, k, H, rows, ls;
 };
 
-template <bool BF16, int N>
+template <bool BF16>
 __global__ __launch_bounds__(256) void dispatch_kernel(const void* __restrict__ x, const int32_t* __restrict__ pos,
                                                        const RowShape s, void* __restrict__ out) {
+  constexpr int N = kVecElems<BF16>;
   const int t = blockIdx.x * (256 >> s.ls) + ((int)threadIdx.x >> s.ls);
   const int c = (blockIdx.y * (1 << s.ls) + ((int)threadIdx.x & ((1 << s.ls) - 1))) * N;
   if (t >= s.T || c >= s.H) return;
   RowVec<BF16, N> v;
-  v.load(x, (size_t)t * s.H + c);
+  v.load(x, (size_t)t * s.H + c, s.H - c);
   for (int j = 0; j < s.k; ++j) {
     const int p = pos[(size_t)t * s.k + j];
-    if ((unsigned)p < (unsigned)s.rows) v.template store<true>(out, (size_t)p * s.H + c);
+    if ((unsigned)p < (unsigned)s.rows) v.template store<true>(out, (size_t)p * s.H + c, s.H - c);
   }
 }
 
 constexpr int kRowsAtOnce = 8;  // rows of a token whose loads are in flight together
 
-template <bool BF16, bool OUT_BF16, int N>
+template <bool BF16, bool OUT_BF16>
 __global__ __launch_bounds__(256) void collect_kernel(const void* __restrict__ rows, const int32_t* __restrict__ pos,
                                                       const float* __restrict__ w, const RowShape s,
                                                       void* __restrict__ out) {
+  constexpr int N = kVecElems<BF16>;
   const int t = blockIdx.x * (256 >> s.ls) + ((int)threadIdx.x >> s.ls);
   const int c = (blockIdx.y * (1 << s.ls) + ((int)threadIdx.x & ((1 << s.ls) - 1))) * N;
   if (t >= s.T || c >= s.H) return;
@@ -230,7 +233,7 @@ __global__ __launch_bounds__(256) void collect_kernel(const void* __restrict__ r
     }
 #pragma unroll
     for (int j = 0; j < kRowsAtOnce; ++j)
-      if ((unsigned)p[j] < (unsigned)s.rows) v[j].load(rows, (size_t)p[j] * s.H + c);
+      if ((unsigned)p[j] < (unsigned)s.rows) v[j].load(rows, (size_t)p[j] * s.H + c, s.H - c);
 #pragma unroll
     for (int j = 0; j < kRowsAtOnce; ++j)
       if ((unsigned)p[j] < (unsigned)s.rows) {
@@ -240,34 +243,37 @@ __global__ __launch_bounds__(256) void collect_kernel(const void* __restrict__ r
   }
   RowVec<OUT_BF16, N> o;
   o.set(acc);
-  o.store(out, (size_t)t * s.H + c);
+  o.store(out, (size_t)t * s.H + c, s.H - c);
 }
 
-// One block per token: dout's row is read once, each of the token's rows once.
-template <bool BF16, bool OUT_BF16, int N, bool DROWS, bool DW>
+// dout's row is read once, each of the token's rows once. 1 << ls threads to a token, all 256 or a part of a wave.
+template <bool BF16, bool OUT_BF16, bool DROWS, bool DW>
 __global__ __launch_bounds__(256) void collect_backward_kernel(const void* __restrict__ dout,
                                                                const void* __restrict__ rows,
                                                                const int32_t* __restrict__ pos,
                                                                const float* __restrict__ w, const RowShape s,
                                                                void* __restrict__ drows, float* __restrict__ dw) {
+  constexpr int N = kVecElems<BF16>;
   __shared__ float part[4][kRowsAtOnce];
-  const int t = blockIdx.x;
+  const int t = blockIdx.x * (256 >> s.ls) + ((int)threadIdx.x >> s.ls);
+  const int team = 1 << s.ls, rank = (int)threadIdx.x & (team - 1);
+  const bool on = t < s.T;  // the others stay for the barriers
   for (int j0 = 0; j0 < s.k; j0 += kRowsAtOnce) {
     int p[kRowsAtOnce];
     float wj[kRowsAtOnce], dot[kRowsAtOnce] = {};
 #pragma unroll
     for (int j = 0; j < kRowsAtOnce; ++j) {
-      p[j] = j0 + j < s.k ? pos[(size_t)t * s.k + j0 + j] : -1;
-      wj[j] = w && j0 + j < s.k ? w[(size_t)t * s.k + j0 + j] : 1.f;
+      p[j] = on && j0 + j < s.k ? pos[(size_t)t * s.k + j0 + j] : -1;
+      wj[j] = on && w && j0 + j < s.k ? w[(size_t)t * s.k + j0 + j] : 1.f;
     }
-    for (int c = (int)threadIdx.x * N; c < s.H; c += 256 * N) {
+    for (int c = rank * N; on && c < s.H; c += team * N) {
       RowVec<OUT_BF16, N> d;
-      d.load(dout, (size_t)t * s.H + c);
+      d.load(dout, (size_t)t * s.H + c, s.H - c);
       RowVec<BF16, N> v[kRowsAtOnce];
       if constexpr (DW) {
 #pragma unroll
         for (int j = 0; j < kRowsAtOnce; ++j)
-          if ((unsigned)p[j] < (unsigned)s.rows) v[j].template load<true>(rows, (size_t)p[j] * s.H + c);
+          if ((unsigned)p[j] < (unsigned)s.rows) v[j].template load<true>(rows, (size_t)p[j] * s.H + c, s.H - c);
       }
 #pragma unroll
       for (int j = 0; j < kRowsAtOnce; ++j)
@@ -282,22 +288,28 @@ __global__ __launch_bounds__(256) void collect_backward_kernel(const void* __res
             for (int i = 0; i < N; ++i) g[i] = wj[j] * d.get(i);
             RowVec<BF16, N> o;
             o.set(g);
-            o.template store<true>(drows, (size_t)p[j] * s.H + c);
+            o.template store<true>(drows, (size_t)p[j] * s.H + c, s.H - c);
           }
         }
     }
     if constexpr (DW) {
+      for (int m = min(team, 64) / 2; m > 0; m >>= 1)
 #pragma unroll
-      for (int j = 0; j < kRowsAtOnce; ++j) {
+        for (int j = 0; j < kRowsAtOnce; ++j) dot[j] += __shfl_xor(dot[j], m, 64);
+      if (team > 64) {
+        if ((threadIdx.x & 63) == 0)
 #pragma unroll
-        for (int m = 32; m > 0; m >>= 1) dot[j] += __shfl_xor(dot[j], m, 64);
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][j] = dot[j];
+          for (int j = 0; j < kRowsAtOnce; ++j) part[threadIdx.x >> 6][j] = dot[j];
+        __syncthreads();
+        const int j = threadIdx.x;
+        if (j < kRowsAtOnce && j0 + j < s.k)
+          dw[(size_t)t * s.k + j0 + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
+        __syncthreads();
+      } else if (on && rank == 0) {
+#pragma unroll
+        for (int j = 0; j < kRowsAtOnce; ++j)
+          if (j0 + j < s.k) dw[(size_t)t * s.k + j0 + j] = dot[j];
       }
-      __syncthreads();
-      const int j = threadIdx.x;
-      if (j < kRowsAtOnce && j0 + j < s.k)
-        dw[(size_t)t * s.k + j0 + j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
-      __syncthreads();
     }
   }
 }
@@ -307,16 +319,6 @@ int lane_bits(int n) {
   int ls = 0;
   while (ls < 8 && (1 << ls) < n) ++ls;
   return ls;
-}
-
-// f(N as a constant) for n of 1, 2, 4, 8 (8 only with bf16 rows).
-template <bool EIGHT, typename F>
-void with_elems(int n, const F& f) {
-  if constexpr (EIGHT)
-    if (n == 8) return f(std::integral_constant<int, 8>{});
-  if (n == 4) return f(std::integral_constant<int, 4>{});
-  if (n == 2) return f(std::integral_constant<int, 2>{});
-  return f(std::integral_constant<int, 1>{});
 }
 
 template <typename F>
@@ -358,35 +360,24 @@ hipError_t launch_group(const int32_t* idx, int T, int k, int E, int32_t* counts
 
 hipError_t launch_dispatch(const void* x, bool bf16, const int32_t* pos, int T, int k, int H, int rows, void* out,
                            hipStream_t s) {
-  const int es = bf16 ? 2 : 4;
-  const int n = row_vec_elems(H, bf16 ? 8 : 4, {{x, es}, {out, es}});
-  const int nv = (H + n - 1) / n, ls = lane_bits(nv);
+  const int n = bf16 ? 8 : 4, nv = (H + n - 1) / n, ls = lane_bits(nv);
   const RowShape sh{T, k, H, rows, ls};
   const dim3 grid((T + (256 >> ls) - 1) / (256 >> ls), (nv + (1 << ls) - 1) >> ls);
   with_flag(bf16, [&](auto b) {
-    constexpr bool B = decltype(b)::value;
-    with_elems<B>(n, [&](auto m) {
-      constexpr int N = decltype(m)::value;
-      hipLaunchKernelGGL((dispatch_kernel<B, N>), grid, dim3(256), 0, s, x, pos, sh, out);
-    });
+    hipLaunchKernelGGL(dispatch_kernel<decltype(b)::value>, grid, dim3(256), 0, s, x, pos, sh, out);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_collect(const void* rows, bool bf16, const int32_t* pos, const float* w, int T, int k, int H,
                           int n_rows, void* out, bool out_bf16, hipStream_t s) {
-  const int n = row_vec_elems(H, bf16 ? 8 : 4, {{rows, bf16 ? 2 : 4}, {out, out_bf16 ? 2 : 4}});
-  const int nv = (H + n - 1) / n, ls = lane_bits(nv);
+  const int n = bf16 ? 8 : 4, nv = (H + n - 1) / n, ls = lane_bits(nv);
   const RowShape sh{T, k, H, n_rows, ls};
   const dim3 grid((T + (256 >> ls) - 1) / (256 >> ls), (nv + (1 << ls) - 1) >> ls);
   with_flag(bf16, [&](auto b) {
-    constexpr bool B = decltype(b)::value;
     with_flag(out_bf16, [&](auto ob) {
-      constexpr bool OB = decltype(ob)::value;
-      with_elems<B>(n, [&](auto m) {
-        constexpr int N = decltype(m)::value;
-        hipLaunchKernelGGL((collect_kernel<B, OB, N>), grid, dim3(256), 0, s, rows, pos, w, sh, out);
-      });
+      hipLaunchKernelGGL((collect_kernel<decltype(b)::value, decltype(ob)::value>), grid, dim3(256), 0, s, rows, pos, w,
+                         sh, out);
     });
   });
   return hipGetLastError();
@@ -395,22 +386,22 @@ hipError_t launch_collect(const void* rows, bool bf16, const int32_t* pos, const
 hipError_t launch_collect_backward(const void* dout, bool out_bf16, const void* rows, bool bf16, const int32_t* pos,
                                    const float* w, int T, int k, int H, int n_rows, void* drows, float* dw,
                                    hipStream_t s) {
-  const int es = bf16 ? 2 : 4;
-  const int n = row_vec_elems(H, bf16 ? 8 : 4, {{dout, out_bf16 ? 2 : 4}, {rows, es}, {drows, es}});
-  const RowShape sh{T, k, H, n_rows, 8};
+  const int n = bf16 ? 8 : 4, nv = (H + n - 1) / n;
+  // 256 threads to a token, so that few tokens fill the chip too; a wave or less where there are tokens enough and one or
+  // two rows of each, whose sums would take as long as the rows (5000 tokens x 1 row of 720 values 18.5 us, 11.6 so; 4096 x
+  // 6 of 4096 83 and 93), or where the row is short.
+  const int most = T >= 2048 && k <= 2 ? 6 : 8;
+  const int ls = lane_bits(nv) <= 6 ? lane_bits(nv) : most;
+  const RowShape sh{T, k, H, n_rows, ls};
+  const dim3 grid((T + (256 >> ls) - 1) / (256 >> ls));
   with_flag(bf16, [&](auto b) {
-    constexpr bool B = decltype(b)::value;
     with_flag(out_bf16, [&](auto ob) {
-      constexpr bool OB = decltype(ob)::value;
-      with_elems<B>(n, [&](auto m) {
-        constexpr int N = decltype(m)::value;
-        with_flag(drows != nullptr, [&](auto dr) {
-          with_flag(dw != nullptr, [&](auto dd) {
-            constexpr bool DR = decltype(dr)::value, DD = decltype(dd)::value;
-            if constexpr (DR || DD)
-              hipLaunchKernelGGL((collect_backward_kernel<B, OB, N, DR, DD>), dim3(T), dim3(256), 0, s, dout, rows, pos,
-                                 w, sh, drows, dw);
-          });
+      with_flag(drows != nullptr, [&](auto dr) {
+        with_flag(dw != nullptr, [&](auto dd) {
+          constexpr bool DR = decltype(dr)::value, DD = decltype(dd)::value;
+          if constexpr (DR || DD)
+            hipLaunchKernelGGL((collect_backward_kernel<decltype(b)::value, decltype(ob)::value, DR, DD>), grid,
+                               dim3(256), 0, s, dout, rows, pos, w, sh, drows, dw);
         });
       });
     });

@@ -33,63 +33,40 @@ struct Sigmoid {
   }
 };
 
-// Where a thread works: a row and eight columns, c0 + i * step (i < n), of a group of 128.
+// Where a thread works: a row and up to eight columns from c0 on, of a group of 128.
 struct KeptAt {
   int64_t row;
-  int group, c0, n, step;
+  int group, c0, left;  // left: columns of g (and u) from c0 on, 0 for a thread past them
   bool on;
 };
 
-template <bool VEC>
 __device__ __forceinline__ KeptAt kept_at(int64_t rows, int I, int groups) {
   const int64_t q = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kKeptLanes;
-  const int l = threadIdx.x & (kKeptLanes - 1);
   KeptAt a;
   a.row = q / groups;
   a.group = (int)(q % groups);
-  a.step = VEC ? 1 : kKeptLanes;
-  a.c0 = a.group * kKeptGroup + (VEC ? l * kKeptCols : l);
-  const int left = min(I, (a.group + 1) * kKeptGroup) - a.c0;
-  a.n = left <= 0 ? 0 : min(kKeptCols, (left + a.step - 1) / a.step);
+  a.c0 = a.group * kKeptGroup + ((int)threadIdx.x & (kKeptLanes - 1)) * kKeptCols;
   a.on = a.row < rows;
+  a.left = a.on ? max(0, I - a.c0) : 0;
   return a;
 }
 
-// Eight columns of a row from `base` on (VEC: one load, 16-byte aligned).
-template <bool BF16, bool VEC>
+template <bool BF16>
 __device__ __forceinline__ void load8(const void* p, size_t base, const KeptAt& a, float (&f)[kKeptCols]) {
-  if constexpr (VEC) {
-    RowVec<BF16, kKeptCols> v;
-    if (a.n > 0) v.load(p, base + a.c0);
+  RowVec<BF16, kKeptCols> v;
+  v.load(p, base + a.c0, a.left);
 #pragma unroll
-    for (int i = 0; i < kKeptCols; ++i) f[i] = a.n > 0 ? v.get(i) : 0.f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kKeptCols; ++i) {
-      RowVec<BF16, 1> v;
-      v.w[0] = 0;
-      if (i < a.n) v.load(p, base + a.c0 + i * kKeptLanes);
-      f[i] = v.get(0);
-    }
-  }
+  for (int i = 0; i < kKeptCols; ++i) f[i] = v.get(i);
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 __device__ __forceinline__ void store8(void* p, size_t base, const KeptAt& a, const float (&f)[kKeptCols]) {
-  if constexpr (VEC) {
-    RowVec<BF16, kKeptCols> v;
-    v.set(f);
-    if (a.n > 0) v.template store<true>(p, base + a.c0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kKeptCols; ++i) {
-      RowVec<BF16, 1> v;
-      const float one[1] = {f[i]};
-      v.set(one);
-      if (i < a.n) v.store(p, base + a.c0 + i * kKeptLanes);
-    }
-  }
+  RowVec<BF16, kKeptCols> v;
+  v.set(f);
+  v.template store<true>(p, base + a.c0, a.left);
 }
+
+typedef uint32_t codes_t __attribute__((ext_vector_type(2), aligned(1)));  // eight codes at any byte
 
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
 #pragma unroll
@@ -97,7 +74,7 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return v;
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 __device__ __forceinline__ void keep8(const float (&f)[kKeptCols], const KeptAt& a, int8_t* codes, size_t base,
                                       float* scale) {
   uint32_t m = 0;
@@ -106,66 +83,66 @@ __device__ __forceinline__ void keep8(const float (&f)[kKeptCols], const KeptAt&
   const RowQuant q(max16(m));
   if (!a.on) return;
   if ((threadIdx.x & (kKeptLanes - 1)) == 0) *scale = q.scale();
-  if constexpr (VEC) {
-    if (a.n > 0)
-      *reinterpret_cast<u32x2_t*>(codes + base + a.c0) =
-          u32x2_t{q.pack4<BF16>(f[0], f[1], f[2], f[3]), q.pack4<BF16>(f[4], f[5], f[6], f[7])};
+  const codes_t v{q.pack4<BF16>(f[0], f[1], f[2], f[3]), q.pack4<BF16>(f[4], f[5], f[6], f[7])};
+  int8_t* p = codes + base + a.c0;
+  if (a.left >= kKeptCols) {
+    *reinterpret_cast<codes_t*>(p) = v;
   } else {
 #pragma unroll
-    for (int i = 0; i < kKeptCols; ++i)
-      if (i < a.n) codes[base + a.c0 + i * kKeptLanes] = (int8_t)(q.code<BF16>(f[i]) & 0xFFu);
+    for (int i = 0; i < kKeptCols - 1; ++i)
+      if (i < a.left) p[i] = (int8_t)(v[i >> 2] >> (8 * (i & 3)));
   }
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 __global__ __launch_bounds__(256) void swiglu_save_kernel(const void* __restrict__ gu, int64_t rows,
                                                           const int32_t* __restrict__ n_rows, int I, int groups,
                                                           void* __restrict__ h, int8_t* __restrict__ codes,
                                                           float* __restrict__ scales) {
   if (n_rows) rows = min(rows, (int64_t)*n_rows);
-  KeptAt a = kept_at<VEC>(rows, I, groups);
-  if (!a.on) a.n = 0;  // the 16 lanes of a group agree, but the wave stays whole for the reductions
+  const KeptAt a = kept_at(rows, I, groups);  // a thread past the rows stays for the reductions
   const size_t r = (size_t)a.row * 2 * I;
   float g[kKeptCols], u[kKeptCols], f[kKeptCols];
-  load8<BF16, VEC>(gu, r, a, g);
-  load8<BF16, VEC>(gu, r + I, a, u);
+  load8<BF16>(gu, r, a, g);
+  load8<BF16>(gu, r + I, a, u);
 #pragma unroll
   for (int i = 0; i < kKeptCols; ++i) f[i] = g[i] * Sigmoid<BF16>(g[i]).s * u[i];
-  store8<BF16, VEC>(h, (size_t)a.row * I, a, f);
+  store8<BF16>(h, (size_t)a.row * I, a, f);
   float* sc = scales + (size_t)a.row * 2 * groups + a.group;
-  keep8<BF16, VEC>(g, a, codes, r, sc);
-  keep8<BF16, VEC>(u, a, codes, r + I, sc + groups);
+  keep8<BF16>(g, a, codes, r, sc);
+  keep8<BF16>(u, a, codes, r + I, sc + groups);
 }
 
-template <bool VEC>
 __device__ __forceinline__ void kept8(const int8_t* codes, size_t base, const KeptAt& a, float scale,
                                       float (&f)[kKeptCols]) {
-  if constexpr (VEC) {
-    u32x2_t v{0, 0};
-    if (a.n > 0) v = *reinterpret_cast<const u32x2_t*>(codes + base + a.c0);
-#pragma unroll
-    for (int i = 0; i < kKeptCols; ++i) f[i] = (float)(int8_t)(v[i >> 2] >> (8 * (i & 3))) * scale;
+  const int8_t* p = codes + base + a.c0;
+  codes_t v{0, 0};
+  if (a.left >= kKeptCols) {
+    v = *reinterpret_cast<const codes_t*>(p);
   } else {
 #pragma unroll
-    for (int i = 0; i < kKeptCols; ++i) f[i] = i < a.n ? (float)codes[base + a.c0 + i * kKeptLanes] * scale : 0.f;
+    for (int i = 0; i < kKeptCols - 1; ++i)
+      if (i < a.left) v[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
   }
+#pragma unroll
+  for (int i = 0; i < kKeptCols; ++i) f[i] = (float)(int8_t)(v[i >> 2] >> (8 * (i & 3))) * scale;
 }
 
-template <bool BF16, bool VEC>
+template <bool BF16>
 __global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __restrict__ codes,
                                                               const float* __restrict__ scales,
                                                               const void* __restrict__ dh, int64_t rows,
                                                               const int32_t* __restrict__ n_rows, int I, int groups,
                                                               void* __restrict__ dgu, void* __restrict__ h) {
   if (n_rows) rows = min(rows, (int64_t)*n_rows);
-  const KeptAt a = kept_at<VEC>(rows, I, groups);
-  if (!a.on) return;
+  const KeptAt a = kept_at(rows, I, groups);
+  if (a.left == 0) return;
   const size_t r = (size_t)a.row * 2 * I;
   const float* sc = scales + (size_t)a.row * 2 * groups + a.group;
   float g[kKeptCols], u[kKeptCols], d[kKeptCols], dg[kKeptCols], du[kKeptCols], f[kKeptCols];
-  kept8<VEC>(codes, r, a, sc[0], g);
-  kept8<VEC>(codes, r + I, a, sc[groups], u);
-  load8<BF16, VEC>(dh, (size_t)a.row * I, a, d);
+  kept8(codes, r, a, sc[0], g);
+  kept8(codes, r + I, a, sc[groups], u);
+  load8<BF16>(dh, (size_t)a.row * I, a, d);
 #pragma unroll
   for (int i = 0; i < kKeptCols; ++i) {
     const Sigmoid<BF16> s(g[i]);
@@ -174,19 +151,9 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __re
     du[i] = d[i] * gs;
     f[i] = gs * u[i];
   }
-  store8<BF16, VEC>(dgu, r, a, dg);
-  store8<BF16, VEC>(dgu, r + I, a, du);
-  if (h) store8<BF16, VEC>(h, (size_t)a.row * I, a, f);
-}
-
-bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-template <typename F>
-void with_kinds(bool bf16, bool vec, const F& f) {
-  if (bf16 && vec) f(std::true_type{}, std::true_type{});
-  else if (bf16) f(std::true_type{}, std::false_type{});
-  else if (vec) f(std::false_type{}, std::true_type{});
-  else f(std::false_type{}, std::false_type{});
+  store8<BF16>(dgu, r, a, dg);
+  store8<BF16>(dgu, r + I, a, du);
+  if (h) store8<BF16>(h, (size_t)a.row * I, a, f);
 }
 
 }  // namespace
@@ -194,24 +161,26 @@ void with_kinds(bool bf16, bool vec, const F& f) {
 hipError_t launch_swiglu_save(const void* gu, bool bf16, int rows, const int32_t* n_rows, int I, void* h,
                               int8_t* codes, float* scales, hipStream_t s) {
   const int groups = (I + kKeptGroup - 1) / kKeptGroup;
-  const unsigned grid = (unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256);
-  const bool vec = I % 8 == 0 && aligned_to(gu, 16) && aligned_to(h, 16) && aligned_to(codes, 8);
-  with_kinds(bf16, vec, [&](auto b, auto v) {
-    hipLaunchKernelGGL((swiglu_save_kernel<decltype(b)::value, decltype(v)::value>), dim3(grid), dim3(256), 0, s, gu,
-                       (int64_t)rows, n_rows, I, groups, h, codes, scales);
-  });
+  const dim3 grid((unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256));
+  if (bf16)
+    hipLaunchKernelGGL(swiglu_save_kernel<true>, grid, dim3(256), 0, s, gu, (int64_t)rows, n_rows, I, groups, h, codes,
+                       scales);
+  else
+    hipLaunchKernelGGL(swiglu_save_kernel<false>, grid, dim3(256), 0, s, gu, (int64_t)rows, n_rows, I, groups, h, codes,
+                       scales);
   return hipGetLastError();
 }
 
 hipError_t launch_swiglu_backward(const int8_t* codes, const float* scales, const void* dh, bool bf16, int rows,
                                   const int32_t* n_rows, int I, void* dgu, void* h, hipStream_t s) {
   const int groups = (I + kKeptGroup - 1) / kKeptGroup;
-  const unsigned grid = (unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256);
-  const bool vec = I % 8 == 0 && aligned_to(dh, 16) && aligned_to(dgu, 16) && aligned_to(h, 16) && aligned_to(codes, 8);
-  with_kinds(bf16, vec, [&](auto b, auto v) {
-    hipLaunchKernelGGL((swiglu_backward_kernel<decltype(b)::value, decltype(v)::value>), dim3(grid), dim3(256), 0, s,
-                       codes, scales, dh, (int64_t)rows, n_rows, I, groups, dgu, h);
-  });
+  const dim3 grid((unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256));
+  if (bf16)
+    hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, dim3(256), 0, s, codes, scales, dh, (int64_t)rows, n_rows, I,
+                       groups, dgu, h);
+  else
+    hipLaunchKernelGGL(swiglu_backward_kernel<false>, grid, dim3(256), 0, s, codes, scales, dh, (int64_t)rows, n_rows, I,
+                       groups, dgu, h);
   return hipGetLastError();
 }
 

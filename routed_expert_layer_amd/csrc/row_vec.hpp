@@ -1,7 +1,6 @@
 // Rows of fp32 or bf16 in registers: N elements at a time, as fp32.
 #pragma once
-#include <initializer_list>
-#include <utility>
+#include <type_traits>
 
 #include "dev_common.hpp"
 
@@ -10,54 +9,71 @@ namespace {
 
 template <bool BF16>
 constexpr int kElem = BF16 ? 2 : 4;
+template <bool BF16>
+constexpr int kVecElems = 16 / kElem<BF16>;  // elements of 16 bytes
 
-// N elements at p (aligned to their size, or to 16 bytes where that is less).
+// N elements (8, 16 or 32 bytes) at any element of a row: global loads and stores of vectors need no more alignment than
+// their elements on this GPU, so rows of odd lengths go in 16-byte pieces too, all but the last few elements. (With
+// pieces of the widest size that divides the row instead, 7754 tokens x 6 rows of 219 bf16 values take 10.3 us to send out
+// and 24.1 for the gradient, 7.3 and 16.5 so; 9949 rows of 2 x 1509 74.8 us through SwiGLU and back, 51.5 so.)
 template <bool BF16, int N>
 struct RowVec {
-  static constexpr int kBytes = N * kElem<BF16>;
-  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  using elem_t = std::conditional_t<BF16, uint16_t, uint32_t>;
+  static constexpr int kWords = N * kElem<BF16> / 4;
+  static_assert(kWords == 2 || kWords == 4 || kWords == 8, "8, 16 or 32 bytes");
+  static constexpr int kPiece = kWords < 4 ? kWords : 4;  // words to a load
+  typedef uint32_t piece_t __attribute__((ext_vector_type(kPiece), aligned(kElem<BF16>)));
   uint32_t w[kWords];
 
-  // STREAM: past the caches, for rows that are read once.
+  // `left` elements are left in the row: the ones past them are 0 and not read or written. STREAM: past the caches, for
+  // rows that are read once.
   template <bool STREAM = false>
-  __device__ __forceinline__ void load(const void* base, size_t elem) {
-    const char* p = static_cast<const char*>(base) + elem * kElem<BF16>;
-    if constexpr (kBytes >= 16) {
+  __device__ __forceinline__ void load(const void* base, size_t elem, int left) {
+    const elem_t* p = static_cast<const elem_t*>(base) + elem;
+    if (left >= N) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) {
-        const u32x4_t v = STREAM ? ld16_nt(p + 16 * i) : ld16(p + 16 * i);
+      for (int i = 0; i < kWords / kPiece; ++i) {
+        const piece_t* q = reinterpret_cast<const piece_t*>(p) + i;
+        piece_t v;
+        if constexpr (STREAM) v = __builtin_nontemporal_load(q);
+        else v = *q;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+        for (int j = 0; j < kPiece; ++j) w[kPiece * i + j] = v[j];
       }
-    } else if constexpr (kBytes == 8) {
-      const u32x2_t v = *reinterpret_cast<const u32x2_t*>(p);
-      w[0] = v[0];
-      w[1] = v[1];
-    } else if constexpr (kBytes == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+      for (int i = 0; i < N - 1; ++i)
+        if (i < left) {
+          if constexpr (BF16) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+          else w[i] = p[i];
+        }
     }
   }
   // STREAM: past the caches, for rows that the experts' products read next: dispatching 4096 tokens to 6 of 64 experts
   // (201 MB of rows) takes 38 us so and 47 through the caches, where the end of the kernel waits for what they hold, and
   // with the product behind it (which is bound by its arithmetic) 847 and 854; 256 tokens 333 and 337.
   template <bool STREAM = false>
-  __device__ __forceinline__ void store(void* base, size_t elem) const {
-    char* p = static_cast<char*>(base) + elem * kElem<BF16>;
-    if constexpr (kBytes >= 16) {
+  __device__ __forceinline__ void store(void* base, size_t elem, int left) const {
+    elem_t* p = static_cast<elem_t*>(base) + elem;
+    if (left >= N) {
 #pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) {
-        const u32x4_t v{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
-        if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p) + i);
-        else reinterpret_cast<u32x4_t*>(p)[i] = v;
+      for (int i = 0; i < kWords / kPiece; ++i) {
+        piece_t v;
+#pragma unroll
+        for (int j = 0; j < kPiece; ++j) v[j] = w[kPiece * i + j];
+        piece_t* q = reinterpret_cast<piece_t*>(p) + i;
+        if constexpr (STREAM) __builtin_nontemporal_store(v, q);
+        else *q = v;
       }
-    } else if constexpr (kBytes == 8) {
-      *reinterpret_cast<u32x2_t*>(p) = u32x2_t{w[0], w[1]};
-    } else if constexpr (kBytes == 4) {
-      *reinterpret_cast<uint32_t*>(p) = w[0];
     } else {
-      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+#pragma unroll
+      for (int i = 0; i < N - 1; ++i)
+        if (i < left) {
+          if constexpr (BF16) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+          else p[i] = w[i];
+        }
     }
   }
   __device__ __forceinline__ float get(int i) const {
@@ -69,8 +85,6 @@ struct RowVec {
     if constexpr (!BF16) {
 #pragma unroll
       for (int i = 0; i < N; ++i) w[i] = __float_as_uint(f[i]);
-    } else if constexpr (N == 1) {
-      w[0] = __builtin_bit_cast(uint16_t, (__bf16)f[0]);
     } else {
       typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
@@ -79,21 +93,6 @@ struct RowVec {
     }
   }
 };
-
-// Elements a thread takes at a time of rows of `len` elements: the most (8 of
-// bf16, 4 of fp32) that divide the row and that every buffer is aligned for.
-// Buffers come with their element's bytes.
-inline int row_vec_elems(size_t len, int most, std::initializer_list<std::pair<const void*, int>> bufs) {
-  for (int n = most; n > 1; n >>= 1) {
-    bool ok = len % n == 0;
-    for (const auto& b : bufs) {
-      const size_t a = (size_t)n * b.second < 16 ? (size_t)n * b.second : 16;
-      ok = ok && (reinterpret_cast<uintptr_t>(b.first) % a) == 0;
-    }
-    if (ok) return n;
-  }
-  return 1;
-}
 
 }  // namespace
 }  // namespace moe

@@ -399,6 +399,7 @@ class TrainExperts:
         T = x.shape[0]
         if T > self.T:
             raise ValueError(f"{T} tokens, and buffers for {self.T}")
+        self.topk_w = None
         n, sc, pos = T * self.k, self.scratch, self.perm_pos[:T]
         L.moe_group(topk_idx, self.E, self.counts, self.offsets, self.perm_src, pos, self.group_ws, stream)
         L.moe_dispatch(x, pos, self.x_perm[:n], stream)

@@ -124,6 +124,19 @@ def test_expert_numbers(L, E):
     run_all(L, r.integers(0, 4, E), 64, 72, E, True, True, torch.float32)
 
 
+# Cases that reach the tiles of 64, 128 and 256 rows with ragged edges on every side: short sums, many columns.
+TILES = [([300, 257, 256, 255, 1, 0, 129, 31], 72, 6000), ([300, 257, 256, 255, 1, 0, 129, 31], 6000, 72),
+         ([300, 257, 256, 255, 1, 0, 129, 31], 104, 4096), ([700, 600, 513, 511], 6000, 72),
+         ([700, 600, 513, 511], 88, 6008), ([33, 0, 127, 90, 260, 5, 64, 1], 520, 2056), ([2, 0, 1, 7] * 16, 264, 2056),
+         ([40] * 40, 1288, 96), ([1] * 300, 96, 264)]
+
+
+@pytest.mark.parametrize("odt", [torch.float32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("counts,K,N", TILES, ids=lambda v: str(v) if isinstance(v, int) else f"{len(v)}x{max(v)}")
+def test_tiles(L, counts, K, N, odt):
+    run_all(L, counts, K, N, K + N, True, True, odt)
+
+
 def test_groups_past_the_rows(L):
     """A group that reaches past the rows, or has a bad first row, is left out; its weight gradient is zeros."""
     K, N, rows = 64, 64, 100

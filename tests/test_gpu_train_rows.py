@@ -85,6 +85,66 @@ def test_group_is_the_routings(L):
         assert np.array_equal(npi(o[n]), npi(getattr(rb, n))), n
 
 
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (512, 64, 8), (6000, 40, 6)])
+def test_group_in_a_graph(L, T, E, k):
+    """Every form of the grouping captured, and replayed with other choices in the same buffer."""
+    from routed_expert_layer_amd.runtime import DeviceDecodeLayer
+    cases = [choices(T, E, k, 50 + i, 0.1 * i, float(i)) for i in range(3)]
+    want = [{n: t.clone() for n, t in grouped(L, c, E).items()} for c in cases]
+    idx = torch.from_numpy(cases[0]).to(dev)
+    o = {n: torch.empty_like(t) for n, t in want[0].items()}
+    ws = torch.empty(max(L.moe_group_workspace_size(T, k, E), 4), dtype=torch.uint8, device=dev)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = DeviceDecodeLayer.capture(
+        lambda: L.moe_group(idx, E, o["counts"], o["offsets"], o["perm_src"], o["perm_pos"], ws, s), s)
+    for i in (1, 0, 2, 2, 1):
+        idx.copy_(torch.from_numpy(cases[i]).to(dev))
+        for t in (*o.values(), ws):
+            t.fill_(FILL if t.dtype == torch.int32 else 255)
+        torch.cuda.synchronize()
+        L.moe_graph_launch(graph, s)
+        torch.cuda.synchronize()
+        for n in o:
+            assert torch.equal(o[n], want[i][n]), n
+
+
+def test_binding_refuses(L):
+    """Types, shapes, layouts and host tensors that the kernels do not take are turned away by name."""
+    f = lambda *s: torch.zeros(s, device=dev)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+    b = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    c8 = torch.zeros((4, 16), dtype=torch.int8, device=dev)
+    calls = [lambda: L.moe_group(i(4, 2), 4, i(4), i(4), i(8), i(4, 2)), lambda: L.moe_group(f(4, 2), 4, i(4), i(5), i(8), i(4, 2)),
+             lambda: L.moe_group(i(4, 2), 4, i(4), i(5), i(7), i(4, 2)), lambda: L.moe_group(i(2, 4).t(), 4, i(4), i(5), i(8), i(4, 2)),
+             lambda: L.moe_group(i(4, 2), 4, i(4), i(5), i(8), i(4, 2).cpu()),
+             lambda: L.moe_dispatch(f(4, 8), i(4, 2), b(8, 8)), lambda: L.moe_dispatch(f(4, 8), i(5, 2), f(8, 8)),
+             lambda: L.moe_dispatch(f(8, 4).t(), i(4, 2), f(8, 8)), lambda: L.moe_dispatch(f(4, 8).half(), i(4, 2), f(8, 8).half()),
+             lambda: L.moe_dispatch(f(4, 8), i(4, 2).long(), f(8, 8)), lambda: L.moe_dispatch(f(4, 8), i(4, 2), f(8, 7)),
+             lambda: L.moe_collect(f(8, 8), i(4, 2), f(4, 3), f(4, 8)), lambda: L.moe_collect(f(8, 8), i(4, 2), b(4, 2), f(4, 8)),
+             lambda: L.moe_collect(f(8, 8), i(4, 2), None, f(4, 9)), lambda: L.moe_collect(f(8, 16)[:, ::2], i(4, 2), None, f(4, 8)),
+             lambda: L.moe_collect_backward(f(4, 8), f(8, 9), i(4, 2), None, None, f(4, 2)),
+             lambda: L.moe_collect_backward(f(4, 8), f(8, 8), i(4, 2), None, b(8, 8), f(4, 2)),
+             lambda: L.moe_collect_backward(f(4, 8), f(8, 8), i(4, 2), None, None, b(4, 2)),
+             lambda: L.moe_swiglu_save(f(4, 16), b(4, 8), c8, f(4, 2)), lambda: L.moe_swiglu_save(f(4, 16), f(4, 8), c8, f(4, 3)),
+             lambda: L.moe_swiglu_save(f(4, 16), f(4, 8), c8, f(4, 2), i(2)), lambda: L.moe_swiglu_save(f(4, 16), f(4, 8), c8.float(), f(4, 2)),
+             lambda: L.moe_swiglu_backward(c8, f(4, 2), f(4, 8), f(4, 8)),
+             lambda: L.moe_swiglu_backward(c8, f(4, 2), b(4, 8), b(4, 16), f(4, 8)),
+             lambda: L.moe_matmul_grouped(b(4, 8), b(2, 8, 16), i(2), i(3), b(4, 8)),
+             lambda: L.moe_matmul_grouped(b(4, 8), b(2, 8, 16), i(2), i(3), b(4, 16), transposed=True),
+             lambda: L.moe_matmul_grouped(f(4, 8), b(2, 8, 16), i(2), i(3), b(4, 16)),
+             lambda: L.moe_matmul_grouped(b(4, 8), b(2, 16, 8).transpose(1, 2), i(2), i(3), b(4, 16)),
+             lambda: L.moe_matmul_grouped(b(4, 8), b(2, 8, 16), i(3), i(3), b(4, 16)),
+             lambda: L.moe_matmul_grouped_dw(b(4, 8), b(5, 16), i(2), i(3), b(2, 8, 16)),
+             lambda: L.moe_matmul_grouped_dw(b(4, 8), b(4, 16), i(2), i(3), b(2, 8, 16).half())]
+    for n, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {n} was taken")
+    with pytest.raises(L.MoEError):
+        L.moe_matmul_grouped(b(4, 12), b(2, 12, 16), i(2), i(3), b(4, 16))
+
+
 def rows_case(L, T, E, k, H, dt, drop, seed, spare=3):
     """Positions, rows (NaN where no entry names them) and tokens; rows_max is `spare` above the rows in use."""
     idx = choices(T, E, k, seed, drop)

@@ -32,7 +32,7 @@ def test_group(L):
         assert L.moe_group_workspace_size(*bad) == 0
 
 
-SIZES = [dict(T=-1), dict(k=0), dict(k=17), dict(T=1 << 30), dict(H=0), dict(H=(1 << 20) + 1), dict(n=-1), dict(dt=2),
+SIZES = [dict(T=-1), dict(k=0), dict(k=17), dict(T=1 << 24), dict(H=0), dict(H=(1 << 20) + 1), dict(n=-1), dict(dt=2),
          dict(dt=-1)]
 
 
@@ -65,7 +65,7 @@ def test_collect_backward(L):
 def test_swiglu(L):
     names = ("g", "dt", "n", "nr", "I", "h", "c", "s", "st")
     save = caller(L._lib.moe_swiglu_save, names, dict(g=16, dt=1, n=4, nr=None, I=64, h=16, c=16, s=16, st=None))
-    sizes = [dict(dt=2), dict(n=-1), dict(n=(1 << 30) + 1), dict(I=0), dict(I=(1 << 20) + 1),
+    sizes = [dict(dt=2), dict(n=-1), dict(n=(1 << 27) + 1), dict(I=0), dict(I=(1 << 20) + 1),
              dict(n=1 << 30, I=1 << 20), dict(nr=18), dict(s=18), dict(s=None), dict(h=17)]
     refused(L, save, sizes + [dict(g=None), dict(h=None), dict(c=None), dict(g=17), dict(dt=0, g=18)])
     assert save(n=0, g=None, h=None, c=None, s=None) == L.MOE_OK
