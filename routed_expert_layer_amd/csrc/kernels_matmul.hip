@@ -316,25 +316,47 @@ __device__ __forceinline__ void tile_product(const Tile& t, char* lds) {
     default: sum(std::integral_constant<int, MF>{}); break;
   }
 
-  // Lane l holds row l % 16 of a fragment and its columns 4 (l / 16) .. + 3. Of bf16 results two fragments exchange
-  // halves between neighbouring rows of 16 lanes, so that a lane has eight columns and four lanes 32.
+  // Lane l holds row l % 16 of a fragment and its columns 4 (l / 16) .. + 3. Of fp32 results four lanes then store 64 bytes
+  // of a row. Of bf16 results two fragments exchange halves between neighbouring rows of 16 lanes, so that a lane has eight
+  // columns, and the tile goes through LDS (16-byte pieces exchanged by an XOR of the row, as above), so that a wave stores
+  // whole rows: the lanes' own stores of 64 bytes a row took 1145 us for the weight gradients of 4096 tokens x 6 of 64
+  // experts of 4096 x 4096 and 531 for 512 tokens, where the stores are most of the work, whole rows past the caches 1106
+  // and 421. (fp32 gains as much where stores are most of the work, 512 tokens of 4096 x 2048 421 and 400, and loses it
+  // where they are not, 4096 tokens 716 and 730; it stays as it is.) Weight gradients are read much later; rows are read
+  // next and stay in the caches.
   const int g = lane >> 4;
+  if constexpr (OUT_BF16) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    static_assert(BM * kBN * 2 <= kLdsBytes<BM, RA, RB, SLOW_A, SLOW_B>, "the tile fits where the operands were");
+    auto pack = [](float x, float y) { return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)x, (__bf16)y}); };
+    __syncthreads();  // every wave is done with the operands
 #pragma unroll
-  for (int j = 0; j < MF; ++j) {
-    const int m = (wm * MF + j) * 16 + (lane & 15);
-    if constexpr (OUT_BF16) {
-      typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-      auto pack = [](float x, float y) { return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)x, (__bf16)y}); };
+    for (int j = 0; j < MF; ++j) {
+      const int m = (wm * MF + j) * 16 + (lane & 15);
 #pragma unroll
       for (int i = 0; i < NF; i += 2) {
         const f32x4_t v = acc[i][j], w = acc[i + 1][j];
         const auto lo = __builtin_amdgcn_permlane16_swap(pack(v[0], v[1]), pack(w[0], w[1]), false, false);
         const auto hi = __builtin_amdgcn_permlane16_swap(pack(v[2], v[3]), pack(w[2], w[3]), false, false);
-        const int n = (wn * NF + i + (g & 1)) * 16 + 8 * (g >> 1);
-        if (m < t.m && n < t.n)
-          *reinterpret_cast<u32x4_t*>(t.c + ((size_t)m * t.ldc + n) * 2) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
+        const int piece = (wn * NF + i + (g & 1)) * 2 + (g >> 1);
+        *reinterpret_cast<u32x4_t*>(lds + m * kBN * 2 + ((piece ^ (m & 15)) << 4)) = u32x4_t{lo[0], hi[0], lo[1], hi[1]};
       }
-    } else {
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int r = 0; r < BM / (2 * kWaves); ++r) {
+      const int m = (r * kWaves + wave) * 2 + (lane >> 5), piece = lane & 31;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(lds + m * kBN * 2 + ((piece ^ (m & 15)) << 4));
+      if (m < t.m && piece * 8 < t.n) {
+        u32x4_t* to = reinterpret_cast<u32x4_t*>(t.c + ((size_t)m * t.ldc + piece * 8) * 2);
+        if constexpr (SLOW_A) __builtin_nontemporal_store(v, to);
+        else *to = v;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < MF; ++j) {
+      const int m = (wm * MF + j) * 16 + (lane & 15);
 #pragma unroll
       for (int i = 0; i < NF; ++i) {
         const int n = (wn * NF + i) * 16 + 4 * g;
