@@ -16,6 +16,13 @@
 // that the reads of a wave fall on all banks. Each operand has a ring of its
 // own in LDS: of parts for a slow one, of pairs of parts for a fast one, whose
 // rows then come in whole cache lines.
+//
+// What bounds them: long groups the matrix cores under the power limit and the
+// operands' way from the memory-side cache (1536 rows an expert of 4096 x 4096:
+// 1190 to 1245 TFLOP/s, W^T 1200 to 1230, weight gradients 1100 to 1160; the
+// library's dense products 1277, 1484, 1172; matrix cores busy 58% of the
+// cycles at 1.9 GHz), few rows the weights' bytes (3 rows an expert 6.3 to 6.6
+// TB/s), short weight gradients their stores (5.2 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -385,7 +392,9 @@ __device__ __forceinline__ int64_t tile_index(int64_t total) {
 }
 unsigned tile_blocks(int64_t tiles) { return (unsigned)((tiles + 8 * kRun - 1) / (8 * kRun) * 8 * kRun); }
 
-// Place of tile number `left` of `rows` x `cols`: bands of eight rows, in them column by column.
+// Place of tile number `left` of `rows` x `cols`: bands of eight rows, in them column by column, so that 32 tiles are
+// eight by four (bands of 4 and 16 and runs of 16 and 64 tiles: weight gradients of 16384 tokens 2980, 3040, 3020 and 3110
+// us, 2970 so).
 __device__ __forceinline__ void tile_place(int left, int rows, int cols, int& m, int& n) {
   const int band = left / (8 * cols), in = left - band * 8 * cols, high = min(8, rows - band * 8);
   m = band * 8 + in % high;

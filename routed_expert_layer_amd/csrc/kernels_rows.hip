@@ -7,7 +7,10 @@
 //   backward:  drows[pos[t, j]] = w[t, j] dout[t],  dw[t, j] = <dout[t], rows[pos[t, j]]>
 //
 // All of them move bytes: a row is read once, in 16-byte loads, and written
-// once; the sums stay in registers.
+// once; the sums stay in registers. Bytes bound them: 4096 tokens to 6 experts'
+// rows of 4096 bf16 values 38 us (235 MB at 6.2 TB/s, mostly writes), the
+// gradient of 16384 tokens' sums of 6 rows 322 us (1.75 GB at 5.4 TB/s; a copy
+// reaches 4.9); a pass over few rows is its launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -26,7 +29,10 @@ constexpr int kGroupWaves = kGroupThreads / 64;
 constexpr int kGroupBlocks = 64;     // most blocks of the two-launch form
 constexpr int kGroupExperts = 1024;
 // Forms: one block that counts what it places; several blocks that each count all the entries; or a launch that counts
-// (group_count) and one that places. A block places 1024 entries a round, or 4096 where rounds are long anyway.
+// (group_count) and one that places. A block places 1024 entries a round, or 4096 where rounds are long anyway. Counting
+// everything in each block saves a launch and costs a load and an LDS atomic for 1024 entries: 24576 entries of 256 experts
+// 8.2 us, 11.8 with two launches, 32768 9.3 and 10.7, 40000 10.5 and 11.3, 65536 14.2 and 11.2. 6 entries take 3.0 us,
+// latency of loads and of ten steps through LDS.
 enum { kGroupOne, kGroupAll, kGroupTwo };
 constexpr int kGroupOneMost = kGroupThreads;   // entries up to which each form is taken
 constexpr int kGroupAllMost = 32768;
