@@ -524,7 +524,8 @@ def moe_combine(y_perm, perm_pos, topk_w, out, stream=None):
 
 # ---------------------------------------------------------------------------
 # The checks of the calls below: an attribute of a tensor takes 0.05 us and a Python call 0.1, so that a launch of 3 us
-# would wait for checks written with a call for each (6.2 us a moe_collect call so, 4.6 with these).
+# would wait for checks written with a call for each (a moe_collect call takes 3.1 us more than the C call so, 2.2 with
+# these).
 _torch = _bf16 = _f32 = _i32 = _i8 = _raw_device = None
 
 

@@ -39,13 +39,13 @@ constexpr int kBN = 256;     // columns of a tile
 constexpr int kPart = 32;    // sum steps of a part
 constexpr uint32_t kNone = 0x80000000u;  // a lane offset past every buffer: the load returns zeros
 
-// One operand of a tile: SIZE rows or columns of results. SLOW: the sum index
-// is the slow one in memory. A slot of its ring holds kStep of the sum.
 template <typename T>
 struct type_of {
   using type = T;
 };
 
+// One operand of a tile: SIZE rows or columns of results. SLOW: the sum index
+// is the slow one in memory. A slot of its ring holds kStep of the sum.
 template <bool SLOW, int SIZE>
 struct Side {
   static constexpr int kParts = SLOW ? 1 : 2, kStep = kPart * kParts;

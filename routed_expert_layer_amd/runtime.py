@@ -371,8 +371,8 @@ class TrainExperts:
     Between forward and backward a layer keeps, for each chosen row, the token (bf16), the expert's output (bf16) and the
     SwiGLU inputs in 8 bits with a scale for 128 columns: 4H + 2I (1 + 4/128) bytes. The rest is scratch, which layers
     of one size that run one after another on one stream may share (`scratch` of another TrainExperts). Every call
-    only enqueues work on the stream, so both passes can be captured; the gate's own gradient starts at the returned
-    gradient of topk_w."""
+    only enqueues work on the stream, so both passes can be captured (into one graph, or one each: replays do not change
+    what an eager backward finds); the gate's own gradient starts at the returned gradient of topk_w."""
 
     def __init__(self, H, I, E, k, T, device="cuda", scratch=None):
         self.H, self.I, self.E, self.k, self.T = H, I, E, k, T
@@ -412,7 +412,8 @@ class TrainExperts:
 
     def backward(self, dout, W13, W2, dx, dtopk_w, dW13, dW2, stream=None):
         """The gradients of the last forward for dout [T, H] (float32 or bfloat16): dx [T, H], dtopk_w fp32 [T, k],
-        dW13 and dW2 (float32 or bfloat16). What forward kept is used up."""
+        dW13 and dW2 (float32 or bfloat16). What forward kept is used up; where dout, dtopk_w, dW13 or dW2 are refused it
+        is still there."""
         if self.topk_w is None:
             raise RuntimeError("backward without a forward before it")
         T = dout.shape[0]
@@ -423,6 +424,6 @@ class TrainExperts:
         L.moe_swiglu_backward(self.codes[:n], self.scales[:n], dh, dgu, h, self.offsets[self.E:], stream)
         L.moe_matmul_grouped_dw(h, dy, self.counts, self.offsets, dW2, stream)
         L.moe_matmul_grouped_dw(self.x_perm[:n], dgu, self.counts, self.offsets, dW13, stream)
+        self.topk_w = None  # the next product overwrites the experts' outputs
         L.moe_matmul_grouped(dgu, W13, self.counts, self.offsets, dx_perm, transposed=True, stream=stream)
         L.moe_collect(dx_perm, pos, None, dx, stream)
-        self.topk_w = None

@@ -165,6 +165,31 @@ def test_graph(R):
             assert torch.equal(o[n], eager[i][n]) and torch.equal(o2[n], eager[j][n]), n
 
 
+def test_refused_backward(R):
+    """A backward pass refused at an output leaves what forward kept, or says that it is gone; never other gradients."""
+    T, E, k, H, I = 40, 6, 2, 136, 72
+    c = case(T, E, k, H, I, 5)
+    layer = R.TrainExperts(H, I, E, k, T)
+    want, got = outputs(c), outputs(c)
+    with pytest.raises(RuntimeError):
+        backward(layer, c, want)
+    forward(layer, c, want)
+    backward(layer, c, want)
+    with pytest.raises(RuntimeError):
+        backward(layer, c, got)
+    forward(layer, c, got)
+    for name in ("dw", "dW2", "dW13"):
+        with pytest.raises(ValueError):
+            backward(layer, c, {**got, name: got[name][:1]})
+    backward(layer, c, got)
+    assert all(torch.equal(want[n], got[n]) for n in want)
+    forward(layer, c, got)
+    with pytest.raises(ValueError):
+        backward(layer, c, {**got, "dx": got["dx"][:1]})
+    with pytest.raises(RuntimeError):
+        backward(layer, c, got)
+
+
 def test_two_streams(R):
     """Two layers at once on two streams, buffers of their own."""
     T, E, k, H, I = 700, 16, 4, 256, 128

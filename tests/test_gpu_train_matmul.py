@@ -118,10 +118,48 @@ def test_other_values(L, odt):
     run_all(L, [40, 0, 300, 1], 328, 200, 11, True, False, odt)
 
 
-@pytest.mark.parametrize("E", [1, 1024])
-def test_expert_numbers(L, E):
+@pytest.mark.parametrize("E,most", [(1, 4), (1024, 4), (1023, 30)])
+def test_expert_numbers(L, E, most):
     r = np.random.default_rng(E)
-    run_all(L, r.integers(0, 4, E), 64, 72, E, True, True, torch.float32)
+    run_all(L, r.integers(0, most, E), 64, 72, E, True, True, torch.float32)
+
+
+@pytest.mark.parametrize("T", [5, 700])
+def test_in_a_graph(L, T):
+    """The three products captured, and replayed after the rows, the weights and the groups have changed."""
+    from routed_expert_layer_amd.runtime import DeviceDecodeLayer
+    E, K, N = 12, 264, 1032
+    g = torch.Generator(device=dev).manual_seed(T)
+    whole = lambda *s: torch.randint(-4, 5, s, generator=g, device=dev).to(BF)  # noqa: E731
+    cases = []
+    for i in range(3):
+        counts = np.bincount(np.random.default_rng(i).integers(0, E - i, T), minlength=E)
+        c = torch.from_numpy(counts.astype(np.int32)).to(dev)
+        o = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(dev)
+        cases.append(dict(a=whole(T, K), d=whole(T, N), w=whole(E, K, N), c=c, o=o))
+
+    def run(v, out, s=None):
+        L.moe_matmul_grouped(v["a"], v["w"], v["c"], v["o"], out[0], stream=s)
+        L.moe_matmul_grouped(v["d"], v["w"], v["c"], v["o"], out[1], transposed=True, stream=s)
+        L.moe_matmul_grouped_dw(v["a"], v["d"], v["c"], v["o"], out[2], stream=s)
+    outs = lambda: [torch.full(s, FILL, dtype=BF, device=dev) for s in ((T, N), (T, K), (E, K, N))]  # noqa: E731
+    want = []
+    for v in cases:
+        want.append(outs())
+        run(v, want[-1])
+    v, out = {n: t.clone() for n, t in cases[0].items()}, outs()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = DeviceDecodeLayer.capture(lambda: run(v, out, s), s)
+    for i in (2, 0, 1, 1):
+        for n in v:
+            v[n].copy_(cases[i][n])
+        for t in out:
+            t.fill_(FILL)
+        torch.cuda.synchronize()
+        L.moe_graph_launch(graph, s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want[i]))
 
 
 # Cases that reach the tiles of 64, 128 and 256 rows with ragged edges on every side: short sums, many columns.

@@ -222,6 +222,40 @@ def test_collect_backward(L, T, E, k, H, dt, odt, drop):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("H", [72, 131])
+def test_positions_past_the_rows(L, H, dt):
+    """Positions that lie outside the rows' buffer, on either side, count as dropped in every call; what lies behind the
+    buffer stays as it was."""
+    T, E, k = 50, 8, 3
+    n, pos, p, rows, x, w = rows_case(L, T, E, k, H, dt, 0.1, 9)
+    few = n // 2
+    p = torch.where(p == 5, torch.tensor(-2 ** 31, dtype=torch.int32, device=dev), p)
+    p = torch.where(p == 7, torch.tensor(2 ** 31 - 1, dtype=torch.int32, device=dev), p)
+    pos = np.where((npi(p) < 0) | (npi(p) >= few), -1, npi(p))
+    w = torch.nan_to_num(w, nan=0.5)
+    out = torch.full((n, H), float(FILL), dtype=dt, device=dev)
+    L.moe_dispatch(x, p, out[:few])
+    want = torch.full((n, H), float(FILL), dtype=dt)
+    for t, j in np.argwhere(pos >= 0):
+        want[pos[t, j]] = x[t].cpu()
+    assert torch.equal(out.cpu(), want)
+    got = torch.empty((T, H), device=dev)
+    L.moe_collect(rows[:few], p, w, got)
+    size = tr.collect(rows[:few].abs(), pos, np.abs(np64(w)))
+    assert np.all(np.abs(np64(got) - tr.collect(rows[:few], pos, np64(w))) <= (k + 1) * 2.0 ** -24 * size)
+    out.fill_(FILL)
+    dw = torch.full((T, k), float("nan"), device=dev)
+    L.moe_collect_backward(x, rows[:few], p, w, out[:few], dw)
+    want, want_w = tr.collect_backward(x, rows[:few], pos, np64(w))
+    named = pos[pos >= 0]
+    assert np.all(np.abs(np64(out)[named] - want[named]) <= (HALF[dt] + 2.0 ** -23) * np.abs(want[named]))
+    rest = np.setdiff1d(np.arange(n), named)
+    assert np.all(np64(out)[rest] == FILL)
+    size = tr.collect_backward(x.abs(), rows[:few].abs(), pos)[1]
+    assert np.all(np.abs(np64(dw) - want_w) <= H * 2.0 ** -24 * size) and np.all(np64(dw)[pos < 0] == 0)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("off", [1, 2, 4])
 def test_unaligned_rows(L, dt, off):
     """Buffers that start off 16 bytes take the narrower loads."""
