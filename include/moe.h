@@ -521,7 +521,7 @@ int moe_collect_backward(const void* dout, int out_dtype, const void* rows, int 
  * n_rows: device int32, or NULL. With it only the first min(rows, *n_rows)
  * rows are worked on (offsets + E of a grouping that dropped entries); those
  * behind them are neither read nor written.
- * Limits: 1 <= I <= 2^20, rows * ceil(I/128) <= 2^27; buffers
+ * Limits: 1 <= I <= 2^20, rows * ceil(I/128) <= 2^26; buffers
  * aligned to their elements and not overlapping.
  * Errors: MOE_EINVAL, MOE_EHIP.
  * ------------------------------------------------------------------------ */

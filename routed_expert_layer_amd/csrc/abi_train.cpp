@@ -114,7 +114,7 @@ int moe_collect_backward(const void* dout, int out_dtype, const void* rows, int 
 int moe_swiglu_save(const void* gu, int dtype, int rows, const int32_t* n_rows, int I, void* h, int8_t* codes,
                     float* scales, void* stream) {
   if (!is_act(dtype)) return fail(MOE_EINVAL, "moe_swiglu_save: bad dtype %d", dtype);
-  if (rows < 0 || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 27))
+  if (rows < 0 || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 26))
     return fail(MOE_EINVAL, "moe_swiglu_save: unsupported sizes rows=%d I=%d", rows, I);
   if (rows == 0) return MOE_OK;
   if (!gu || !h || !codes || !scales) return fail(MOE_EINVAL, "moe_swiglu_save: null pointer argument");
@@ -127,7 +127,7 @@ int moe_swiglu_save(const void* gu, int dtype, int rows, const int32_t* n_rows, 
 int moe_swiglu_backward(const int8_t* codes, const float* scales, const void* dh, int dtype, int rows,
                         const int32_t* n_rows, int I, void* dgu, void* h, void* stream) {
   if (!is_act(dtype)) return fail(MOE_EINVAL, "moe_swiglu_backward: bad dtype %d", dtype);
-  if (rows < 0 || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 27))
+  if (rows < 0 || I < 1 || I > kMaxLen || (long long)rows * ((I + 127) / 128) > (1ll << 26))
     return fail(MOE_EINVAL, "moe_swiglu_backward: unsupported sizes rows=%d I=%d", rows, I);
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !dh || !dgu) return fail(MOE_EINVAL, "moe_swiglu_backward: null pointer argument");

@@ -5,8 +5,10 @@
 //   backward, from g^, u^ = code * scale:
 //     dg = dh u^ s (1 + g^ (1 - s)),  du = dh g^ s,  h^ = g^ s u^
 //
-// Sixteen lanes take 128 columns of g and the same of u, eight of each a lane,
-// so a scale is one reduction over 16 lanes and every byte is moved once.
+// A lane takes 16 bytes of g and the same columns of u, so that a wave's loads
+// and stores are whole lines: 16 lanes 128 columns of bf16, 32 of fp32 (eight
+// columns a lane there too: 16384 rows of 2 x 2048 fp32 back in 146 us, 86 so).
+// A scale is one reduction over those lanes, and every byte is moved once.
 // Bytes bound both passes: 98304 bf16 rows of 2 x 2048 take 636 us, 3.65 GB at
 // 5.7 TB/s (a copy reaches 4.9).
 #include "dev_common.hpp"
@@ -18,7 +20,6 @@ namespace moe {
 namespace {
 
 constexpr int kKeptGroup = 128;  // columns that share a scale
-constexpr int kKeptLanes = 16, kKeptCols = 8;
 
 // 1 / (1 + e^-g) and 1 - it, neither by a difference: both keep their last bits (a NaN stays one). For bf16 results by
 // the hardware's exponential and reciprocal, a step of 2^-23 each and 1.5 |g| half steps from the exponent's argument
@@ -35,64 +36,62 @@ struct Sigmoid {
   }
 };
 
-// Where a thread works: a row and up to eight columns from c0 on, of a group of 128.
+// Where a thread works: a row and the columns from c on.
 struct KeptAt {
   int64_t row;
-  int group, c0, left;  // left: columns of g (and u) from c0 on, 0 for a thread past them
-  bool on;
+  int c, left;  // left: columns of g (and u) from c on, 0 for a thread without any
 };
 
-__device__ __forceinline__ KeptAt kept_at(int64_t rows, int I, int groups) {
-  const int64_t q = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kKeptLanes;
-  KeptAt a;
-  a.row = q / groups;
-  a.group = (int)(q % groups);
-  a.c0 = a.group * kKeptGroup + ((int)threadIdx.x & (kKeptLanes - 1)) * kKeptCols;
-  a.on = a.row < rows;
-  a.left = a.on ? max(0, I - a.c0) : 0;
-  return a;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, size_t base, const KeptAt& a, float (&f)[kKeptCols]) {
-  RowVec<BF16, kKeptCols> v;
-  v.load(p, base + a.c0, a.left);
+template <bool BF16, int N>
+__device__ __forceinline__ void load(const void* p, size_t base, const KeptAt& a, float (&f)[N]) {
+  RowVec<BF16, N> v;
+  v.load(p, base + a.c, a.left);
 #pragma unroll
-  for (int i = 0; i < kKeptCols; ++i) f[i] = v.get(i);
+  for (int i = 0; i < N; ++i) f[i] = v.get(i);
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store8(void* p, size_t base, const KeptAt& a, const float (&f)[kKeptCols]) {
-  RowVec<BF16, kKeptCols> v;
+template <bool BF16, int N>
+__device__ __forceinline__ void store(void* p, size_t base, const KeptAt& a, const float (&f)[N]) {
+  RowVec<BF16, N> v;
   v.set(f);
-  v.template store<true>(p, base + a.c0, a.left);
+  v.template store<true>(p, base + a.c, a.left);
 }
 
-typedef uint32_t codes_t __attribute__((ext_vector_type(2), aligned(1)));  // eight codes at any byte
+template <int N>
+using codes_t __attribute__((aligned(1))) = uint32_t __attribute__((ext_vector_type(N / 4)));  // N codes at any byte
 
-__device__ __forceinline__ uint32_t max16(uint32_t v) {
-#pragma unroll
-  for (int d = kKeptLanes / 2; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d, kKeptLanes));
-  return v;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void keep8(const float (&f)[kKeptCols], const KeptAt& a, int8_t* codes, size_t base,
-                                      float* scale) {
+template <bool BF16, int N>
+__device__ __forceinline__ void keep(const float (&f)[N], const KeptAt& a, bool first, int8_t* codes, size_t base,
+                                     float* scale) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kKeptCols; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-  const RowQuant q(max16(m));
-  if (!a.on) return;
-  if ((threadIdx.x & (kKeptLanes - 1)) == 0) *scale = q.scale();
-  const codes_t v{q.pack4<BF16>(f[0], f[1], f[2], f[3]), q.pack4<BF16>(f[4], f[5], f[6], f[7])};
-  int8_t* p = codes + base + a.c0;
-  if (a.left >= kKeptCols) {
-    *reinterpret_cast<codes_t*>(p) = v;
-  } else {
+  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
 #pragma unroll
-    for (int i = 0; i < kKeptCols - 1; ++i)
-      if (i < a.left) p[i] = (int8_t)(v[i >> 2] >> (8 * (i & 3)));
+  for (int d = kKeptGroup / N / 2; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 64));
+  const RowQuant q(m);
+  if (a.left == 0) return;
+  if (first) *scale = q.scale();
+  codes_t<N> v;
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) v[i] = q.pack4<BF16>(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  int8_t* p = codes + base + a.c;
+  if (a.left >= N) {
+    *reinterpret_cast<codes_t<N>*>(p) = v;
+  } else {
+    typedef uint16_t half_t __attribute__((aligned(1)));
+    typedef uint32_t word_t __attribute__((aligned(1)));
+    uint32_t rest = v[0];  // four, two and one of them
+    if (N > 4 && a.left >= 4) {
+      *reinterpret_cast<word_t*>(p) = rest;
+      rest = v[N / 4 - 1];
+      p += 4;
+    }
+    if (a.left & 2) {
+      *reinterpret_cast<half_t*>(p) = (uint16_t)rest;
+      rest >>= 16;
+      p += 2;
+    }
+    if (a.left & 1) *p = (int8_t)rest;
   }
 }
 
@@ -102,32 +101,41 @@ __global__ __launch_bounds__(256) void swiglu_save_kernel(const void* __restrict
                                                           void* __restrict__ h, int8_t* __restrict__ codes,
                                                           float* __restrict__ scales) {
   if (n_rows) rows = min(rows, (int64_t)*n_rows);
-  const KeptAt a = kept_at(rows, I, groups);  // a thread past the rows stays for the reductions
+  constexpr int N = kVecElems<BF16>, kLanes = kKeptGroup / N;
+  const uint32_t q = (blockIdx.x * 256u + threadIdx.x) / kLanes;  // rows * groups is 2^26 at most
+  const int group = (int)(q % (uint32_t)groups), lane = (int)threadIdx.x & (kLanes - 1);
+  const int c0 = group * kKeptGroup + lane * N;
+  KeptAt a{(int64_t)(q / (uint32_t)groups), c0, 0};
+  a.left = a.row < rows ? max(0, I - c0) : 0;  // a thread without columns stays for the reductions
   const size_t r = (size_t)a.row * 2 * I;
-  float g[kKeptCols], u[kKeptCols], f[kKeptCols];
-  load8<BF16>(gu, r, a, g);
-  load8<BF16>(gu, r + I, a, u);
+  float g[N], u[N], f[N];
+  load<BF16>(gu, r, a, g);
+  load<BF16>(gu, r + I, a, u);
 #pragma unroll
-  for (int i = 0; i < kKeptCols; ++i) f[i] = g[i] * Sigmoid<BF16>(g[i]).s * u[i];
-  store8<BF16>(h, (size_t)a.row * I, a, f);
-  float* sc = scales + (size_t)a.row * 2 * groups + a.group;
-  keep8<BF16>(g, a, codes, r, sc);
-  keep8<BF16>(u, a, codes, r + I, sc + groups);
+  for (int i = 0; i < N; ++i) f[i] = g[i] * Sigmoid<BF16>(g[i]).s * u[i];
+  store<BF16>(h, (size_t)a.row * I, a, f);
+  float* sc = scales + (size_t)a.row * 2 * groups + group;
+  keep<BF16>(g, a, lane == 0, codes, r, sc);
+  keep<BF16>(u, a, lane == 0, codes, r + I, sc + groups);
 }
 
-__device__ __forceinline__ void kept8(const int8_t* codes, size_t base, const KeptAt& a, float scale,
-                                      float (&f)[kKeptCols]) {
-  const int8_t* p = codes + base + a.c0;
-  codes_t v{0, 0};
-  if (a.left >= kKeptCols) {
-    v = *reinterpret_cast<const codes_t*>(p);
+// sc: the row's scales. The row's last piece may begin in the group before the last.
+template <int N>
+__device__ __forceinline__ void kept(const int8_t* codes, size_t base, const KeptAt& a, const float* sc, float (&f)[N]) {
+  const int8_t* p = codes + base + a.c;
+  const int g0 = a.c / kKeptGroup, g1 = (a.c + min(a.left, N) - 1) / kKeptGroup;
+  const int turn = g1 * kKeptGroup - a.c;  // the columns from here on have the second scale
+  const float s0 = sc[g0], s1 = sc[g1];
+  codes_t<N> v = 0;
+  if (a.left >= N) {
+    v = *reinterpret_cast<const codes_t<N>*>(p);
   } else {
 #pragma unroll
-    for (int i = 0; i < kKeptCols - 1; ++i)
+    for (int i = 0; i < N - 1; ++i)
       if (i < a.left) v[i >> 2] |= (uint32_t)(uint8_t)p[i] << (8 * (i & 3));
   }
 #pragma unroll
-  for (int i = 0; i < kKeptCols; ++i) f[i] = (float)(int8_t)(v[i >> 2] >> (8 * (i & 3))) * scale;
+  for (int i = 0; i < N; ++i) f[i] = (float)(int8_t)(v[i >> 2] >> (8 * (i & 3))) * (i < turn ? s0 : s1);
 }
 
 template <bool BF16>
@@ -137,25 +145,28 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __re
                                                               const int32_t* __restrict__ n_rows, int I, int groups,
                                                               void* __restrict__ dgu, void* __restrict__ h) {
   if (n_rows) rows = min(rows, (int64_t)*n_rows);
-  const KeptAt a = kept_at(rows, I, groups);
-  if (a.left == 0) return;
+  constexpr int N = kVecElems<BF16>;
+  const uint32_t q = blockIdx.x * 256u + threadIdx.x, pieces = (uint32_t)(I + N - 1) / N;
+  KeptAt a{(int64_t)(q / pieces), piece_start<N>((int)(q % pieces) * N, I), 0};
+  if (a.row >= rows) return;
+  a.left = I - a.c;
   const size_t r = (size_t)a.row * 2 * I;
-  const float* sc = scales + (size_t)a.row * 2 * groups + a.group;
-  float g[kKeptCols], u[kKeptCols], d[kKeptCols], dg[kKeptCols], du[kKeptCols], f[kKeptCols];
-  kept8(codes, r, a, sc[0], g);
-  kept8(codes, r + I, a, sc[groups], u);
-  load8<BF16>(dh, (size_t)a.row * I, a, d);
+  const float* sc = scales + (size_t)a.row * 2 * groups;
+  float g[N], u[N], d[N], dg[N], du[N], f[N];
+  kept(codes, r, a, sc, g);
+  kept(codes, r + I, a, sc + groups, u);
+  load<BF16>(dh, (size_t)a.row * I, a, d);
 #pragma unroll
-  for (int i = 0; i < kKeptCols; ++i) {
+  for (int i = 0; i < N; ++i) {
     const Sigmoid<BF16> s(g[i]);
     const float gs = g[i] * s.s;
     dg[i] = d[i] * u[i] * fmaf(gs, s.t, s.s);
     du[i] = d[i] * gs;
     f[i] = gs * u[i];
   }
-  store8<BF16>(dgu, r, a, dg);
-  store8<BF16>(dgu, r + I, a, du);
-  if (h) store8<BF16>(h, (size_t)a.row * I, a, f);
+  store<BF16>(dgu, r, a, dg);
+  store<BF16>(dgu, r + I, a, du);
+  if (h) store<BF16>(h, (size_t)a.row * I, a, f);
 }
 
 }  // namespace
@@ -163,7 +174,8 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __re
 hipError_t launch_swiglu_save(const void* gu, bool bf16, int rows, const int32_t* n_rows, int I, void* h,
                               int8_t* codes, float* scales, hipStream_t s) {
   const int groups = (I + kKeptGroup - 1) / kKeptGroup;
-  const dim3 grid((unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256));
+  const int lanes = kKeptGroup / (bf16 ? kVecElems<true> : kVecElems<false>);
+  const dim3 grid((unsigned)(((int64_t)rows * groups * lanes + 255) / 256));
   if (bf16)
     hipLaunchKernelGGL(swiglu_save_kernel<true>, grid, dim3(256), 0, s, gu, (int64_t)rows, n_rows, I, groups, h, codes,
                        scales);
@@ -176,7 +188,8 @@ hipError_t launch_swiglu_save(const void* gu, bool bf16, int rows, const int32_t
 hipError_t launch_swiglu_backward(const int8_t* codes, const float* scales, const void* dh, bool bf16, int rows,
                                   const int32_t* n_rows, int I, void* dgu, void* h, hipStream_t s) {
   const int groups = (I + kKeptGroup - 1) / kKeptGroup;
-  const dim3 grid((unsigned)(((int64_t)rows * groups * kKeptLanes + 255) / 256));
+  const int each = bf16 ? kVecElems<true> : kVecElems<false>, pieces = (I + each - 1) / each;
+  const dim3 grid((unsigned)(((int64_t)rows * pieces + 255) / 256));
   if (bf16)
     hipLaunchKernelGGL(swiglu_backward_kernel<true>, grid, dim3(256), 0, s, codes, scales, dh, (int64_t)rows, n_rows, I,
                        groups, dgu, h);

@@ -222,6 +222,38 @@ def test_collect_backward(L, T, E, k, H, dt, odt, drop):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("H", [*range(1, 20), 61, 509, 2050, 2063, 4099])
+def test_ends_of_rows(L, H, dt):
+    """Every length of a row's last piece, in every call: whole numbers, so that the sums have one value, and an infinity
+    in one of the last eight columns, which is summed once like any other."""
+    T, E, k = 11, 6, 3
+    n, pos, p, rows, x, w = rows_case(L, T, E, k, H, dt, 0.2, H)
+    g = torch.Generator().manual_seed(H)
+    whole = lambda *s: torch.randint(-4, 5, s, generator=g).to(dt).to(dev)  # noqa: E731
+    x, rows, w = whole(T, H), whole(n + 3, H), torch.randint(-2, 3, (T, k), generator=g).float().to(dev)
+    out = torch.full((n + 3, H), float(FILL), dtype=dt, device=dev)
+    L.moe_dispatch(x, p, out)
+    want = torch.full((n + 3, H), float(FILL), dtype=dt)
+    for t, j in np.argwhere(pos >= 0):
+        want[pos[t, j]] = x[t].cpu()
+    assert torch.equal(out.cpu(), want)
+    got = torch.empty((T, H), device=dev)
+    L.moe_collect(rows, p, w, got)
+    assert np.array_equal(np64(got), tr.collect(rows, pos, np64(w)))
+    out.fill_(FILL)
+    dw = torch.full((T, k), float("nan"), device=dev)
+    L.moe_collect_backward(x, rows, p, w, out, dw)
+    want, want_w = tr.collect_backward(x, rows, pos, np64(w))
+    assert np.array_equal(np64(out)[:n], want[:n]) and np.all(np64(out)[n:] == FILL)
+    assert np.array_equal(np64(dw), np.where(pos >= 0, want_w, 0))
+    for c in range(max(0, H - 9), H):
+        ones, r = torch.ones_like(x), rows.clone()
+        r[:, c] = float("inf")
+        L.moe_collect_backward(ones, r, p, w, None, dw)
+        assert np.array_equal(np64(dw), np.where(pos >= 0, np.inf, 0))
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("H", [72, 131])
 def test_positions_past_the_rows(L, H, dt):
     """Positions that lie outside the rows' buffer, on either side, count as dropped in every call; what lies behind the

@@ -93,6 +93,22 @@ def test_save_and_backward(L, R, I, dt):
 
 
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("I", [*range(2, 21), *range(121, 142), *range(257, 264)])
+def test_ends_of_rows(L, I, dt):
+    """Every length of a row's last piece, also where it begins in the group before, whose scale is another."""
+    R = 5
+    gu, dh = inputs(R, I, dt, I)
+    far = torch.tensor([1.0, 2.0 ** -9, 2.0 ** 3], device=dev).repeat_interleave(128)[:I].to(dt)
+    gu *= torch.cat([far, far.flip(0)])
+    o = buffers(R, I, dt)
+    n = torch.tensor([R - 1], dtype=torch.int32, device=dev)
+    L.moe_swiglu_save(gu, o["h"], o["codes"], o["scales"], n)
+    check_save(gu, o, R - 1, I, dt)
+    L.moe_swiglu_backward(o["codes"], o["scales"], dh, o["dgu"], o["again"], n)
+    check_backward(o, dh, R - 1, I, dt)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("R,I,off", [(7, 256, 1), (7, 256, 2), (3, 384, 4)])
 def test_unaligned(L, R, I, off, dt):
     """Buffers that start off 16 bytes give the same bits."""
