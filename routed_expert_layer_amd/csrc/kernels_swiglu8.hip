@@ -9,8 +9,10 @@
 // and stores are whole lines: 16 lanes 128 columns of bf16, 32 of fp32 (eight
 // columns a lane there too: 16384 rows of 2 x 2048 fp32 back in 146 us, 86 so).
 // A scale is one reduction over those lanes, and every byte is moved once.
-// Bytes bound both passes: 98304 bf16 rows of 2 x 2048 take 636 us, 3.65 GB at
-// 5.7 TB/s (a copy reaches 4.9).
+// Bytes bound both passes: 98304 bf16 rows of 2 x 2048 take 668 us, 3.65 GB at
+// 5.5 TB/s (a copy reaches 4.9).
+#include <type_traits>
+
 #include "dev_common.hpp"
 #include "moe_kernels.hpp"
 #include "row_quant.hpp"
@@ -21,20 +23,42 @@ namespace {
 
 constexpr int kKeptGroup = 128;  // columns that share a scale
 
-// 1 / (1 + e^-g) and 1 - it, neither by a difference: both keep their last bits (a NaN stays one). For bf16 results by
-// the hardware's exponential and reciprocal, a step of 2^-23 each and 1.5 |g| half steps from the exponent's argument
-// (below 2^-8 by far): 98304 rows of 2 x 2048 take 636 us for both passes so, 708 with expf and a
-// division.
-template <bool FAST>
-struct Sigmoid {
-  float s, t;
-  __device__ __forceinline__ explicit Sigmoid(float g) {
-    const float e = FAST ? __expf(-fabsf(g)) : expf(-fabsf(g));
-    const float r = FAST ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
-    s = g >= 0.f ? r : e * r;
-    t = g >= 0.f ? e * r : r;
+// s(g) = 1 / (1 + e^-g), t = 1 - s and g s, none by a difference that loses bits. The exponent's argument has 48 bits,
+// the reciprocal is corrected by what 1 + e and it were rounded by, and for g >= 0 g s = g - g t is rounded once, so that
+// all are off by some half steps of 2^-24 at any g. That shows in bf16 results too: where t is small, g u is often next to
+// a tie and the last bits of s decide: with the hardware's exponential and reciprocal as they are 1.7e-5 of 8192 x 2048
+// values of h went to the other side, 0.5e-5 so; both passes of 98304 rows 642 us and 668. FAR: of gates below -64 s and g s are 2^64 times as large, and `down` takes
+// products with them back: e^g then is a normal number down to e^-131, and what the hardware's exponential loses below
+// 2^-126 is not lost to a large u or dh. An infinity or NaN in g reaches every result.
+template <bool FAR>
+struct Silu {
+  float s, t, gs, down;
+  __device__ __forceinline__ explicit Silu(float g) {
+#pragma clang fp contract(off)  // p is rounded: its residue is `low`
+    constexpr float kLog2E = 1.44269504f, kLog2ELow = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const bool far = FAR && g < -64.f;
+    const float x = fminf(fabsf(g), 512.f);
+    const float p = x * -kLog2E, low = fmaf(x, -kLog2ELow, fmaf(x, -kLog2E, -p));
+    const float w = __builtin_amdgcn_exp2f(far ? p + 64.f : p);  // the sum is exact
+    const float e = fmaf(w, low * kLn2, w);                      // far: below 2^-27, 1 + e is 1 either way
+    const float q = __builtin_amdgcn_rcpf(1.f + e), r = fmaf(fmaf(-q, e, 1.f - q), q, q), er = e * r;
+    const bool up = g >= 0.f;
+    s = up ? r : er;
+    t = up ? er : r;
+    gs = fmaf(up ? -x : g, er, up ? g : 0.f);
+    down = far ? 0x1p-64f : 1.f;
   }
 };
+
+// f with Silu's form for these gates: most threads have none far out, and the same bits by either.
+template <int N, typename F>
+__device__ __forceinline__ void with_silu(const float (&g)[N], const F& f) {
+  float least = g[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) least = fminf(least, g[i]);
+  if (least < -64.f) f(std::true_type{});
+  else f(std::false_type{});
+}
 
 // Where a thread works: a row and the columns from c on.
 struct KeptAt {
@@ -111,8 +135,13 @@ __global__ __launch_bounds__(256) void swiglu_save_kernel(const void* __restrict
   float g[N], u[N], f[N];
   load<BF16>(gu, r, a, g);
   load<BF16>(gu, r + I, a, u);
+  with_silu(g, [&](auto far) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) f[i] = g[i] * Sigmoid<BF16>(g[i]).s * u[i];
+    for (int i = 0; i < N; ++i) {
+      const Silu<decltype(far)::value> v(g[i]);
+      f[i] = v.gs * u[i] * v.down;
+    }
+  });
   store<BF16>(h, (size_t)a.row * I, a, f);
   float* sc = scales + (size_t)a.row * 2 * groups + group;
   keep<BF16>(g, a, lane == 0, codes, r, sc);
@@ -156,14 +185,15 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __re
   kept(codes, r, a, sc, g);
   kept(codes, r + I, a, sc + groups, u);
   load<BF16>(dh, (size_t)a.row * I, a, d);
+  with_silu(g, [&](auto far) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const Sigmoid<BF16> s(g[i]);
-    const float gs = g[i] * s.s;
-    dg[i] = d[i] * u[i] * fmaf(gs, s.t, s.s);
-    du[i] = d[i] * gs;
-    f[i] = gs * u[i];
-  }
+    for (int i = 0; i < N; ++i) {
+      const Silu<decltype(far)::value> v(g[i]);
+      dg[i] = d[i] * u[i] * fmaf(v.gs, v.t, v.s) * v.down;
+      du[i] = d[i] * v.gs * v.down;
+      f[i] = v.gs * u[i] * v.down;
+    }
+  });
   store<BF16>(dgu, r, a, dg);
   store<BF16>(dgu, r + I, a, du);
   if (h) store<BF16>(h, (size_t)a.row * I, a, f);
