@@ -189,7 +189,10 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const int8_t* __re
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const Silu<decltype(far)::value> v(g[i]);
-      dg[i] = d[i] * u[i] * fmaf(v.gs, v.t, v.s) * v.down;
+      // s's derivative is 1.1 at most: half of it times the larger factor stays in range, and so does what follows where
+      // the result does (dh u alone may not)
+      const float a = fabsf(d[i]) > fabsf(u[i]) ? d[i] : u[i], b = fabsf(d[i]) > fabsf(u[i]) ? u[i] : d[i];
+      dg[i] = a * (0.5f * fmaf(v.gs, v.t, v.s)) * b * (2.f * v.down);
       du[i] = d[i] * v.gs * v.down;
       f[i] = v.gs * u[i] * v.down;
     }

@@ -34,9 +34,9 @@ def far(dt, seed, lo, hi):
 
 
 def off(got, want, size, steps, dt):
-    """Entries that are off by more than their steps and rounding; results below 2^-120 of a type's range are left out."""
+    """Entries that are off by more than their steps and rounding; results that are no normal numbers are left out."""
     tol = steps * 2.0 ** -24 * size
-    held = np.abs(want) >= 2.0 ** -120
+    held = np.abs(want) >= 2.0 ** -125
     assert held.mean() > 0.4
     return (np.abs(np64(got) - want) > tol + HALF[dt] * (np.abs(want) + tol))[held]
 
@@ -70,3 +70,27 @@ def test_small_sigmoids(L, dt, lo, hi):
     want = tr.swiglu(g, u)
     held = np.abs(u) > 0
     assert not off(again, np.where(held, want, 0), np.abs(want), STEPS + 2 + np.abs(g), dt).any()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,u", [(70, 70), (100, 40), (40, 100), (-100, 120), (120, -100), (-60, -60), (126, 0), (0, 126)])
+def test_far_factors(L, dt, d, u):
+    """dh and u of 2^d and 2^u whose product the type does not hold, where dgu's gate half is in its range: it comes out."""
+    R, I = 8, 256
+    r = np.random.default_rng(1)
+    gu = torch.empty((R, 2 * I))
+    gu[:, :I] = torch.tensor(-r.uniform(30, 60, (R, I)) if d + u > 128 else r.uniform(-5, 5, (R, I)))
+    gu[:, I:] = 2.0 ** u * torch.tensor(r.choice([-1.0, 1.0], (R, I)))
+    dh = 2.0 ** d * torch.tensor(r.choice([-1.0, 0.75, 1.25], (R, I)))
+    gu, dh = gu.to(dt).to(dev), dh.to(dt).to(dev)
+    h, dgu = torch.empty((R, I), dtype=dt, device=dev), torch.empty((R, 2 * I), dtype=dt, device=dev)
+    codes, scales = torch.empty((R, 2 * I), dtype=torch.int8, device=dev), torch.empty((R, 4), device=dev)
+    L.moe_swiglu_save(gu, h, codes, scales)
+    L.moe_swiglu_backward(codes, scales, dh, dgu)
+    c, s = codes.cpu().numpy(), scales.cpu().numpy()
+    g, u, dh = tr.kept(c[:, :I], s[:, :2]), tr.kept(c[:, I:], s[:, 2:]), np64(dh)
+    dg, _ = tr.swiglu_backward(g, u, dh)
+    # as above, with the larger of two factors chosen and halves exact; dg's second factor is near 0 at g = -1.3
+    size = np.abs(dh * u * tr.sigmoid(g)) * (1 + np.abs(g) * tr.sigmoid(-g))
+    assert np.abs(dg).max() < 2.0 ** 127.9
+    assert not off(dgu[:, :I], dg, size, STEPS + 2 + np.abs(g), dt).any()
