@@ -824,8 +824,11 @@ int moe_cpu_threads(void);
  * moe_graph_begin(stream): starts capturing `stream` (a created stream, not
  *   the default one; thread-local capture mode). moe_graph_end(stream): ends
  *   the capture and instantiates it. moe_graph_launch: replays the graph on a
- *   stream. moe_graph_destroy frees it. Errors: EINVAL, EHIP (for example a
- *   call that is not allowed during capture).
+ *   stream. moe_graph_destroy frees it. moe_stream_capturing: 1 in *capturing
+ *   where what is enqueued on the stream goes into a graph (by moe_graph_begin
+ *   or any other capture), 0 where it runs; the default stream is never
+ *   captured. Errors: EINVAL, EHIP (for example a call that is not allowed
+ *   during capture).
  * ------------------------------------------------------------------------- */
 typedef struct moe_device_decoder moe_device_decoder_t;
 typedef struct moe_graph moe_graph_t;
@@ -851,6 +854,7 @@ int moe_graph_begin(void* stream);
 moe_graph_t* moe_graph_end(void* stream, int* status);
 int moe_graph_launch(moe_graph_t* graph, void* stream);
 int moe_graph_destroy(moe_graph_t* graph);
+int moe_stream_capturing(void* stream, int* capturing);
 
 #ifdef __cplusplus
 }

@@ -29,7 +29,7 @@ SYMBOLS = [
     "moe_cpu_ffn", "moe_cpu_threads", "moe_cache_set_split", "moe_decoder_cpu_runs",
     "moe_device_decoder_create", "moe_device_decoder_destroy", "moe_device_decoder_step", "moe_device_decoder_stats",
     "moe_device_decoder_trace", "moe_device_decoder_clear_trace", "moe_device_decoder_slot_of",
-    "moe_graph_begin", "moe_graph_end", "moe_graph_launch", "moe_graph_destroy",
+    "moe_graph_begin", "moe_graph_end", "moe_graph_launch", "moe_graph_destroy", "moe_stream_capturing",
     "moe_cache_resize", "moe_cache_capacity", "moe_decoder_resize", "moe_device_decoder_resize",
     "moe_ffn_grouped", "moe_prefill_layer", "moe_route_noalloc",
     "moe_select_workspace_size", "moe_select", "moe_route_scored", "moe_experts_workspace_size", "moe_experts",
@@ -164,6 +164,7 @@ _sig("moe_graph_begin", I32, P)
 _sig("moe_graph_end", P, P, PI)
 _sig("moe_graph_launch", I32, P, P)
 _sig("moe_graph_destroy", I32, P)
+_sig("moe_stream_capturing", I32, P, PI)
 _sig("moe_cache_resize", I32, P, I32, P, I32, PI)
 _sig("moe_cache_capacity", I32, P)
 _sig("moe_decoder_resize", I32, P, I32, P, P)
@@ -995,6 +996,17 @@ def moe_graph_launch(graph, stream=None):
 
 def moe_graph_destroy(graph):
     graph.close()
+
+
+def moe_stream_capturing(stream=None):
+    """Whether what is enqueued on the stream (None: the current one) goes into a graph, by moe_graph_begin or other means."""
+    if stream is None:
+        import torch
+        if not torch.cuda.is_initialized():
+            return False
+    on = ctypes.c_int(0)
+    _check(_lib.moe_stream_capturing(_stream(stream), ctypes.byref(on)), "moe_stream_capturing")
+    return on.value != 0
 
 
 # ---------------------------------------------------------------------------

@@ -397,4 +397,15 @@ int moe_graph_destroy(moe_graph_t* g) {
   return MOE_OK;
 }
 
+int moe_stream_capturing(void* stream, int* capturing) {
+  if (!capturing) return dd_fail(MOE_EINVAL, "moe_stream_capturing: null result");
+  *capturing = 0;
+  if (!stream) return MOE_OK;
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  hipError_t e = hipStreamIsCapturing(reinterpret_cast<hipStream_t>(stream), &st);
+  if (e != hipSuccess) return dd_fail(MOE_EHIP, "moe_stream_capturing: %s", hipGetErrorString(e));
+  *capturing = st != hipStreamCaptureStatusNone;
+  return MOE_OK;
+}
+
 }  // extern "C"

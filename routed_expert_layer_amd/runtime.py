@@ -364,18 +364,12 @@ class PrefillLayer:
                           layer_base, self.stride, self.wfmt, self.H, self.I, self.y_perm, self.ffn_ws, stream)
 
 
-class TrainExperts:
-    """The expert half of a layer with its backward pass, on row-major bf16 weights W13 [E, H, 2I] (gate columns, then
-    up) and W2 [E, I, H], for the choices of any gate (entries outside [0, E) are experts of another GPU: dropped).
+class _KeptPass:
+    """What a forward pass of TrainExperts leaves for its backward pass."""
 
-    Between forward and backward a layer keeps, for each chosen row, the token (bf16), the expert's output (bf16) and the
-    SwiGLU inputs in 8 bits with a scale for 128 columns: 4H + 2I (1 + 4/128) bytes. The rest is scratch, which layers
-    of one size that run one after another on one stream may share (`scratch` of another TrainExperts). Every call
-    only enqueues work on the stream, so both passes can be captured (into one graph, or one each: replays do not change
-    what an eager backward finds); the gate's own gradient starts at the returned gradient of topk_w."""
+    BUFFERS = ("counts", "offsets", "perm_src", "perm_pos", "group_ws", "x_perm", "y_perm", "codes", "scales")
 
-    def __init__(self, H, I, E, k, T, device="cuda", scratch=None):
-        self.H, self.I, self.E, self.k, self.T = H, I, E, k, T
+    def __init__(self, H, I, E, k, T, device):
         rows = max(T * k, 1)
         i32 = dict(dtype=torch.int32, device=device)
         bf = dict(dtype=torch.bfloat16, device=device)
@@ -384,14 +378,54 @@ class TrainExperts:
         self.group_ws = torch.empty(max(L.moe_group_workspace_size(T, k, E), 4), dtype=torch.uint8, device=device)
         self.x_perm, self.y_perm = torch.empty((rows, H), **bf), torch.empty((rows, H), **bf)
         self.codes = torch.empty((rows, 2 * I), dtype=torch.int8, device=device)
-        self.scales = torch.empty((rows, 2 * ((I + 127) // 128)), device=device)
+        self.scales = torch.empty((rows, 2 * ((I + 127) // 128)), dtype=torch.float32, device=device)
+        self.topk_w = None  # of the forward that filled the buffers, while a backward may follow it
+
+
+class TrainExperts:
+    """The expert half of a layer with its backward pass, on row-major bf16 weights W13 [E, H, 2I] (gate columns, then
+    up) and W2 [E, I, H], for the choices of any gate (entries outside [0, E) are experts of another GPU: dropped).
+
+    Between forward and backward a layer keeps, for each chosen row, the token (bf16), the expert's output (bf16) and the
+    SwiGLU inputs in 8 bits with a scale for 128 columns: 4H + 2I (1 + 4/128) bytes. The rest is scratch, which layers
+    of one size that run one after another on one stream may share (`scratch` of another TrainExperts). The gate's own
+    gradient starts at the returned gradient of topk_w. Every call only enqueues work on its stream.
+
+    Both passes can be captured, into one graph or one each. A captured backward takes what its captured forward keeps; a
+    replayed backward (any number of them) belongs behind a replay of that forward, with no other captured forward of
+    this layer replayed between. Eager passes do not see replays, nor replays them: after the first capture they keep
+    their rows in buffers of their own, which the next eager forward allocates. Capturing ends an eager pass whose
+    backward is still to come."""
+
+    def __init__(self, H, I, E, k, T, device="cuda", scratch=None):
+        self.H, self.I, self.E, self.k, self.T = H, I, E, k, T
+        self._captured = None  # the buffers that graphs were captured with
+        self._eager = self._new_kept(device)
+        rows = max(T * k, 1)
+        bf = dict(dtype=torch.bfloat16, device=device)
         if scratch is None:
             scratch = dict(gu=torch.empty((rows, 2 * I), **bf), h=torch.empty((rows, I), **bf),
                            dh=torch.empty((rows, I), **bf), dy=torch.empty((rows, H), **bf))
         if scratch["gu"].shape != (rows, 2 * I) or scratch["dy"].shape != (rows, H):
             raise ValueError("scratch of a layer of another size")
         self.scratch = scratch
-        self.topk_w = None
+
+    def _new_kept(self, device):
+        """New buffers of a pass, which are the layer's attributes from then on."""
+        kept = _KeptPass(self.H, self.I, self.E, self.k, self.T, device)
+        for n in kept.BUFFERS:
+            setattr(self, n, getattr(kept, n))
+        return kept
+
+    def _pass_on(self, stream):
+        """The buffers of the passes that `stream` takes: captured ones, or eager ones (None before their first forward
+        behind a capture)."""
+        if not L.moe_stream_capturing(stream):
+            return self._eager
+        if self._captured is None:
+            self._captured, self._eager = self._eager, None
+            self._captured.topk_w = None
+        return self._captured
 
     def forward(self, x, topk_idx, topk_w, W13, W2, out, stream=None):
         """out [T, H] (float32 or bfloat16) = sum_j topk_w[t, j] expert(topk_idx[t, j])(x[t]); x bf16 [T, H]. topk_w is
@@ -399,31 +433,39 @@ class TrainExperts:
         T = x.shape[0]
         if T > self.T:
             raise ValueError(f"{T} tokens, and buffers for {self.T}")
-        self.topk_w = None
-        n, sc, pos = T * self.k, self.scratch, self.perm_pos[:T]
-        L.moe_group(topk_idx, self.E, self.counts, self.offsets, self.perm_src, pos, self.group_ws, stream)
-        L.moe_dispatch(x, pos, self.x_perm[:n], stream)
-        L.moe_matmul_grouped(self.x_perm[:n], W13, self.counts, self.offsets, sc["gu"][:n], stream=stream)
-        L.moe_swiglu_save(sc["gu"][:n], sc["h"][:n], self.codes[:n], self.scales[:n], self.offsets[self.E:], stream)
-        L.moe_matmul_grouped(sc["h"][:n], W2, self.counts, self.offsets, self.y_perm[:n], stream=stream)
-        L.moe_collect(self.y_perm[:n], pos, topk_w, out, stream)
-        self.topk_w = topk_w
+        kept = self._pass_on(stream)
+        if kept is None:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+                # memory that no other stream works on
+                kept = self._eager = self._new_kept(self.x_perm.device)
+        kept.topk_w = None
+        n, sc, pos = T * self.k, self.scratch, kept.perm_pos[:T]
+        L.moe_group(topk_idx, self.E, kept.counts, kept.offsets, kept.perm_src, pos, kept.group_ws, stream)
+        L.moe_dispatch(x, pos, kept.x_perm[:n], stream)
+        L.moe_matmul_grouped(kept.x_perm[:n], W13, kept.counts, kept.offsets, sc["gu"][:n], stream=stream)
+        L.moe_swiglu_save(sc["gu"][:n], sc["h"][:n], kept.codes[:n], kept.scales[:n], kept.offsets[self.E:], stream)
+        L.moe_matmul_grouped(sc["h"][:n], W2, kept.counts, kept.offsets, kept.y_perm[:n], stream=stream)
+        L.moe_collect(kept.y_perm[:n], pos, topk_w, out, stream)
+        kept.topk_w = topk_w
         return out
 
     def backward(self, dout, W13, W2, dx, dtopk_w, dW13, dW2, stream=None):
-        """The gradients of the last forward for dout [T, H] (float32 or bfloat16): dx [T, H], dtopk_w fp32 [T, k],
-        dW13 and dW2 (float32 or bfloat16). What forward kept is used up; where dout, dtopk_w, dW13 or dW2 are refused it
-        is still there."""
-        if self.topk_w is None:
-            raise RuntimeError("backward without a forward before it")
+        """The gradients of the last forward (under capture: of the last captured one) for dout [T, H] (float32 or
+        bfloat16): dx [T, H], dtopk_w fp32 [T, k], dW13 and dW2 (float32 or bfloat16). What forward kept is used up;
+        where dout, dtopk_w, dW13 or dW2 are refused it is still there."""
+        kept = self._pass_on(stream)
+        if kept is None or kept.topk_w is None:
+            raise RuntimeError("backward without a forward before it" + ("" if self._captured is None else
+                               " (eager and captured passes go by themselves)"))
         T = dout.shape[0]
-        n, sc, pos, w = T * self.k, self.scratch, self.perm_pos[:T], self.topk_w
-        dy, dh, h, dgu, dx_perm = sc["dy"][:n], sc["dh"][:n], sc["h"][:n], sc["gu"][:n], self.y_perm[:n]
-        L.moe_collect_backward(dout, self.y_perm[:n], pos, w, dy, dtopk_w, stream)
-        L.moe_matmul_grouped(dy, W2, self.counts, self.offsets, dh, transposed=True, stream=stream)
-        L.moe_swiglu_backward(self.codes[:n], self.scales[:n], dh, dgu, h, self.offsets[self.E:], stream)
-        L.moe_matmul_grouped_dw(h, dy, self.counts, self.offsets, dW2, stream)
-        L.moe_matmul_grouped_dw(self.x_perm[:n], dgu, self.counts, self.offsets, dW13, stream)
-        self.topk_w = None  # the next product overwrites the experts' outputs
-        L.moe_matmul_grouped(dgu, W13, self.counts, self.offsets, dx_perm, transposed=True, stream=stream)
+        n, sc, pos, w = T * self.k, self.scratch, kept.perm_pos[:T], kept.topk_w
+        dy, dh, h, dgu, dx_perm = sc["dy"][:n], sc["dh"][:n], sc["h"][:n], sc["gu"][:n], sc["dy"][:n]
+        L.moe_collect_backward(dout, kept.y_perm[:n], pos, w, dy, dtopk_w, stream)
+        L.moe_matmul_grouped(dy, W2, kept.counts, kept.offsets, dh, transposed=True, stream=stream)
+        L.moe_swiglu_backward(kept.codes[:n], kept.scales[:n], dh, dgu, h, kept.offsets[self.E:], stream)
+        L.moe_matmul_grouped_dw(h, dy, kept.counts, kept.offsets, dW2, stream)
+        L.moe_matmul_grouped_dw(kept.x_perm[:n], dgu, kept.counts, kept.offsets, dW13, stream)
+        kept.topk_w = None
+        # dy is done with; what forward kept is only read, so that a replay of this pass may be replayed again
+        L.moe_matmul_grouped(dgu, W13, kept.counts, kept.offsets, dx_perm, transposed=True, stream=stream)
         L.moe_collect(dx_perm, pos, None, dx, stream)
