@@ -373,8 +373,8 @@ class _KeptPass:
         rows = max(T * k, 1)
         i32 = dict(dtype=torch.int32, device=device)
         bf = dict(dtype=torch.bfloat16, device=device)
-        self.counts, self.offsets = torch.zeros(E, **i32), torch.zeros(E + 1, **i32)
-        self.perm_src, self.perm_pos = torch.zeros(rows, **i32), torch.zeros((T, k), **i32)
+        self.counts, self.offsets = torch.empty(E, **i32), torch.empty(E + 1, **i32)
+        self.perm_src, self.perm_pos = torch.empty(rows, **i32), torch.empty((T, k), **i32)
         self.group_ws = torch.empty(max(L.moe_group_workspace_size(T, k, E), 4), dtype=torch.uint8, device=device)
         self.x_perm, self.y_perm = torch.empty((rows, H), **bf), torch.empty((rows, H), **bf)
         self.codes = torch.empty((rows, 2 * I), dtype=torch.int8, device=device)
@@ -389,7 +389,8 @@ class TrainExperts:
     Between forward and backward a layer keeps, for each chosen row, the token (bf16), the expert's output (bf16) and the
     SwiGLU inputs in 8 bits with a scale for 128 columns: 4H + 2I (1 + 4/128) bytes. The rest is scratch, which layers
     of one size that run one after another on one stream may share (`scratch` of another TrainExperts). The gate's own
-    gradient starts at the returned gradient of topk_w. Every call only enqueues work on its stream.
+    gradient starts at the returned gradient of topk_w. Every call only enqueues work on its stream; buffers are not
+    filled beforehand, and a first pass on another stream than the one that was current here is the caller's to order.
 
     Both passes can be captured, into one graph or one each. A captured backward takes what its captured forward keeps; a
     replayed backward (any number of them) belongs behind a replay of that forward, with no other captured forward of

@@ -3,6 +3,7 @@ statements, which run at once or, while a stream is being captured, when the gra
 import numpy as np
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from oracle import train as tr
 
@@ -251,3 +252,16 @@ def test_capturing_refused():
     assert L._lib.moe_stream_capturing(None, None) == L.MOE_EINVAL and L.moe_last_error()
     assert L._lib.moe_stream_capturing(None, ctypes.byref(on)) == L.MOE_OK and on.value == 0
     assert L.moe_stream_capturing() is False
+
+def test_buffers_are_not_filled(R):
+    """Nothing is enqueued when a layer is made: a fill on the stream current then could come after a first pass on
+    another stream."""
+    class Calls(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.seen.add(func.overloadpacket.__name__)
+            return func(*args, **(kwargs or {}))
+    calls = Calls()
+    calls.seen = set()
+    with calls:
+        R.TrainExperts(H, I, E, k, T, "cpu")
+    assert calls.seen <= {"empty"}, calls.seen
