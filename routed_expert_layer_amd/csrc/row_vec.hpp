@@ -29,7 +29,7 @@ template <bool BF16, int N>
 struct RowVec {
   using elem_t = std::conditional_t<BF16, uint16_t, uint32_t>;
   static constexpr int kWords = N * kElem<BF16> / 4;
-  static_assert(kWords == 2 || kWords == 4 || kWords == 8, "8, 16 or 32 bytes");
+  static_assert(N == 4 || N == 8, "a row's last piece goes in parts of four, two and one: up to seven elements");
   static constexpr int kPiece = kWords < 4 ? kWords : 4;  // words to a load
   typedef uint32_t piece_t __attribute__((ext_vector_type(kPiece), aligned(kElem<BF16>)));
   template <int M>  // M elements

@@ -253,6 +253,7 @@ def test_capturing_refused():
     assert L._lib.moe_stream_capturing(None, ctypes.byref(on)) == L.MOE_OK and on.value == 0
     assert L.moe_stream_capturing() is False
 
+
 def test_buffers_are_not_filled(R):
     """Nothing is enqueued when a layer is made: a fill on the stream current then could come after a first pass on
     another stream."""
