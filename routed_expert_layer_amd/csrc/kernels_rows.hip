@@ -334,11 +334,16 @@ int lane_bits(int n) {
   return ls;
 }
 
-// Whether rows that other kernels read next are stored past the caches: unless their pieces lie across cache lines, two of
-// which then make a line together. 4096 x 6 rows of 4095 bf16 values 55 us past the caches, 37 through them, 30000 x 6 of
-// 219 22.6 and 18.4; 7754 x 6 of 219 6.6 and 6.9. The gradient 92 and 78, 51 and 44; 16384 x 6 of 1001 fp32 values 166 and
-// 183.
-bool past_caches(bool bf16, int H) { return H % (bf16 ? kVecElems<true> : kVecElems<false>) == 0; }
+// Whether rows that other kernels read next are stored past the caches. Rows whose pieces lie across cache lines, two of
+// which then make a line together, are not where the memory-side cache holds them all. Past the caches and through them, us
+// (buffers in turn): 30000 x 6 rows of 219 bf16 values out 22.9 and 18.5, their gradient 52.9 and 44.2; 4096 x 6 of 4095
+// 55.2 and 52.5, 93 and 95; more than it holds: 16384 x 6 of 4095 207 and 244, 359 and 387; 16384 x 6 of 1001 fp32 values
+// 100 and 104, 168 and 184; 8192 x 2 of 4097 68 and 93, 137 and 155. Near its size it goes either way: 4096 x 6 of 2047
+// fp32 values (201 MB) out 57 and 51, 30000 x 6 of 219 (158 MB) 40 and 51.
+constexpr int64_t kCacheBytes = 1 << 28;
+bool past_caches(bool bf16, int H, int64_t rows) {
+  return H % (bf16 ? kVecElems<true> : kVecElems<false>) == 0 || rows * H * (bf16 ? 2 : 4) > kCacheBytes;
+}
 
 template <typename F>
 void with_flag(bool b, const F& f) {
@@ -383,7 +388,7 @@ hipError_t launch_dispatch(const void* x, bool bf16, const int32_t* pos, int T, 
   const RowShape sh{T, k, H, rows, ls};
   const dim3 grid((T + (256 >> ls) - 1) / (256 >> ls), (nv + (1 << ls) - 1) >> ls);
   with_flag(bf16, [&](auto b) {
-    with_flag(past_caches(bf16, H), [&](auto p) {
+    with_flag(past_caches(bf16, H, std::min((int64_t)T * k, (int64_t)rows)), [&](auto p) {
       hipLaunchKernelGGL((dispatch_kernel<decltype(b)::value, decltype(p)::value>), grid, dim3(256), 0, s, x, pos, sh, out);
     });
   });
@@ -419,7 +424,7 @@ hipError_t launch_collect_backward(const void* dout, bool out_bf16, const void* 
     with_flag(out_bf16, [&](auto ob) {
       with_flag(drows != nullptr, [&](auto dr) {
         with_flag(dw != nullptr, [&](auto dd) {
-          with_flag(drows && past_caches(bf16, H), [&](auto pc) {
+          with_flag(drows && past_caches(bf16, H, std::min((int64_t)T * k, (int64_t)n_rows)), [&](auto pc) {
             constexpr bool DR = decltype(dr)::value, DD = decltype(dd)::value, P = decltype(pc)::value;
             if constexpr (DR || (DD && !P))
               hipLaunchKernelGGL((collect_backward_kernel<decltype(b)::value, decltype(ob)::value, DR, DD, P>), grid,

@@ -96,3 +96,26 @@ def test_passes_by_their_roundings(R, T, E, k, H, I, drop):  # noqa: F811
         got = np64(o[name])
         off = np.linalg.norm(got - want[name]) / np.linalg.norm(want[name])
         assert off <= 2 * n ** 0.5 * 2.0 ** -8 / 7 ** 0.5, (name, off)
+
+
+@pytest.mark.parametrize("T,k,H,dt", [(16384, 6, 1403, torch.bfloat16), (16389, 4, 1030, torch.float32),
+                                      (8192, 6, 1371, torch.float32)])
+def test_more_rows_than_the_caches_hold(L, T, k, H, dt):  # noqa: F811
+    """Rows of odd lengths, more than 256 MiB of them: copies are equal, gradients the products rounded once."""
+    g = torch.Generator(device=dev).manual_seed(H)
+    idx = torch.randint(-1, 40, (T, k), generator=g, device=dev, dtype=torch.int32)
+    o = grouped(L, npi(idx).astype(np.int32), 40)
+    n, pos = int(o["offsets"][40]), o["perm_pos"]
+    x = torch.randn((T, H), generator=g, device=dev).to(dt)
+    w = torch.rand((T, k), generator=g, device=dev)
+    rows = torch.full((T * k, H), float(FILL), dtype=dt, device=dev)
+    assert rows.numel() * rows.element_size() > 1 << 28
+    L.moe_dispatch(x, pos, rows)
+    t, j = torch.nonzero(pos >= 0, as_tuple=True)
+    at = pos[t, j].long()
+    assert len(at) == n and torch.equal(rows[at], x[t]) and torch.all(rows[n:] == FILL)
+    drows, dw = torch.full_like(rows, float(FILL)), torch.full((T, k), float("nan"), device=dev)
+    L.moe_collect_backward(x, rows, pos, w, drows, dw)
+    assert torch.equal(drows[at], (w[t, j, None] * x[t].float()).to(dt)) and torch.all(drows[n:] == FILL)
+    want = (x[t].double() ** 2).sum(1)
+    assert torch.all((dw[t, j].double() - want).abs() <= H * 2.0 ** -24 * want) and torch.all(dw[pos < 0] == 0)
