@@ -17,12 +17,12 @@
 // own in LDS: of parts for a slow one, of pairs of parts for a fast one, whose
 // rows then come in whole cache lines.
 //
-// What bounds them: long groups the matrix cores under the power limit and the
-// operands' way from the memory-side cache (1536 rows an expert of 4096 x 4096:
-// 1190 to 1245 TFLOP/s, W^T 1200 to 1230, weight gradients 1100 to 1160; the
-// library's dense products 1277, 1484, 1172; matrix cores busy 58% of the
-// cycles at 1.9 GHz), few rows the weights' bytes (3 rows an expert 6.3 to 6.6
-// TB/s), short weight gradients their stores (5.2 TB/s).
+// What bounds them: long groups the operands' way from the memory-side cache,
+// at a clock that the power limit holds at 1.8 to 2.0 GHz of 2.4 (1536 rows an
+// expert of 4096 x 4096: 1165 to 1245 TFLOP/s, W^T 1180 to 1230, weight
+// gradients 1100 to 1165; the library's dense products 1277, 1484, 1172; matrix
+// cores busy 65, 63 and 54% of the cycles), few rows the weights' bytes (3 rows
+// an expert 6.3 to 6.6 TB/s), short weight gradients their stores (5.2 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -544,7 +544,9 @@ hipError_t launch_matmul_grouped_dw(const void* a, const void* dc, const int32_t
   };
   // 256 rows of dW to a tile, unless the last round of 256 blocks is mostly empty: every tile is as much work as its
   // expert has rows, and 300 tiles take two rounds (333 tokens x 5 of 20 experts of 1280 x 648 19.0 us, 15.8 in 64s; 128
-  // tiles of 32 experts of 512 x 512 10.7 and 8.5; 256 tiles of 16 experts of 1024 x 1024 11.4 and 12.6).
+  // tiles of 32 experts of 512 x 512 10.7 and 8.5; 256 tiles of 16 experts of 1024 x 1024 11.4 and 12.6). Long sums are no
+  // exception, though 64s read 2.5 times the operands: 4096 rows for each of 8 experts of 1536 x 1536 (288 tiles) 198 us
+  // in 256s and 195 in 64s, of 1024 x 1024 (128 tiles) 93 and 88, 20 experts of 1280 x 648 with 1024 rows each 59 and 52.
   const int64_t tiles = (int64_t)((N + kBN - 1) / kBN) * ((K + 255) / 256) * E;
   if (10 * tiles >= 7 * ((tiles + 255) / 256 * 256))
     out_bf16 ? run(matmul_dw_kernel<256, 2, 4, 4, 4, 1, true>, 256, 512)

@@ -9,8 +9,8 @@ namespace {
 
 // Where the piece of N elements that begins at column c of a row of n is taken: the last one ends with the row, so that
 // it is moved whole too; its first elements are then those of the piece before (the same values, written twice). Rows
-// shorter than a piece begin at 0. (7754 tokens' sums of 6 rows of 219 bf16 values 6.5 us with a shorter last piece, 5.1
-// so, 4096 x 6 of 4095 back 112 and 95; copies are as fast with one, 6.6 and 7.9 us, and have one.)
+// shorter than a piece begin at 0. (7754 tokens' sums of 6 rows of 219 bf16 values 7.5 us with a shorter last piece, 6.6
+// so, their gradient 21.6 and 13.5, that of 4096 x 6 of 4095 120 and 95; copies are as fast with one, and have one.)
 template <int N>
 __device__ __forceinline__ int piece_start(int c, int n) {
   return min(c, max(n - N, 0));
@@ -24,7 +24,7 @@ constexpr int kVecElems = 16 / kElem<BF16>;  // elements of 16 bytes
 // N elements (8, 16 or 32 bytes) at any element of a row: global loads and stores of vectors need no more alignment than
 // their elements on this GPU, so rows of odd lengths go in 16-byte pieces too, all but the last few elements. (With
 // pieces of the widest size that divides the row instead, 7754 tokens x 6 rows of 219 bf16 values take 10.3 us to send out
-// and 24.1 for the gradient, 6.9 and 13.1 so; 9949 rows of 2 x 1509 74.8 us through SwiGLU and back, 50.4 so.)
+// and 24.1 for the gradient, 7.0 and 13.5 so; 9949 rows of 2 x 1509 74.8 us through SwiGLU and back, 54 so.)
 template <bool BF16, int N>
 struct RowVec {
   using elem_t = std::conditional_t<BF16, uint16_t, uint32_t>;
@@ -78,7 +78,7 @@ struct RowVec {
       }
     }
   }
-  // STREAM: past the caches, for whole 16-byte rows that the experts' products read next: dispatching 4096 tokens to 6 of
+  // STREAM: past the caches, for rows that the experts' products read next: dispatching 4096 tokens to 6 of
   // 64 experts (201 MB of rows) takes 38 us so and 47 through the caches, where the end of the kernel waits for what they
   // hold, and with the product behind it (which is bound by its arithmetic) 847 and 854; 256 tokens 333 and 337.
   template <bool STREAM = false>
