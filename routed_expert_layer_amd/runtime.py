@@ -395,7 +395,7 @@ class TrainExperts:
     Both passes can be captured, into one graph or one each. A captured backward takes what its captured forward keeps; a
     replayed backward (any number of them) belongs behind a replay of that forward, with no other captured forward of
     this layer replayed between. Eager passes do not see replays, nor replays them: after the first capture they keep
-    their rows in buffers of their own, which the next eager forward allocates. Capturing ends an eager pass whose
+    their rows in buffers of their own, which the next eager forward allocates. The first capture ends an eager pass whose
     backward is still to come."""
 
     def __init__(self, H, I, E, k, T, device="cuda", scratch=None):
